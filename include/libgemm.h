@@ -326,6 +326,173 @@ int gemm_f16_guarded(const float* A, const float* B, void* C, int out_dtype,
 /* Bytes of workspace gemm_f16_guarded needs (GEMM_ERR_DIM for a bad size). */
 int64_t gemm_f16_guarded_workspace_size(int64_t M, int64_t N, int64_t K);
 
+/* -------------------------------- products whose weight depends on the row */
+/* P3 §1 places the matrix product at the centre of a network's layers; in a
+ * mixture of experts each row of A meets its own expert's weight, and with
+ * adapters each request's rows add their own low-rank term. The rows come in
+ * groups: offsets[groups + 1] (device, int32, in order) gives group g the rows
+ * [offsets[g], offsets[g + 1]); groups may be empty, and rows before
+ * offsets[0] or from offsets[groups] on belong to no group. The host never
+ * reads offsets, so the calls can be enqueued behind the kernels that write
+ * them. Offsets out of order or outside [0, rows] give unspecified results but
+ * no access outside the operands. groups is at most 4096. */
+
+/*
+ * gemm_f16_grouped — C[r] = A[r] · B[g(r)] for FP16 operands, FP32
+ * accumulation; rows of no group are written as zeros.
+ *   A        device, _Float16[rows*K], row-major
+ *   B        device, _Float16[groups*K*N]: one row-major B[K,N] per group
+ *   offsets  device, int32[groups + 1]
+ *   C        device, float or _Float16 [rows*N] per out_dtype (GEMM_OUT_F32 or
+ *            GEMM_OUT_F16)
+ * rows = 0 or N = 0 is a no-op; K = 0 or groups = 0 writes zeros. Errors as
+ * gemm_f16, plus GEMM_ERR_DIM for groups outside [0, 4096].
+ * gemm_f16_grouped_bt takes each group's weight K-major, Bt[groups][N][K]; the
+ * gradient to the rows of one is the other call on the same weights.
+ */
+int gemm_f16_grouped(const void* A, const void* B, const int32_t* offsets, void* C, int out_dtype,
+                     int64_t rows, int64_t N, int64_t K, int64_t groups, hipStream_t stream);
+int gemm_f16_grouped_bt(const void* A, const void* Bt, const int32_t* offsets, void* C, int out_dtype,
+                        int64_t rows, int64_t N, int64_t K, int64_t groups, hipStream_t stream);
+
+/*
+ * gemm_fp8_grouped — C[r] = (sA·A[r]) · (sB[g]·B[g]), g = g(r), for FP8 codes
+ * of formats fmt_a and fmt_b (P2 §2.1, §3.2).
+ *   sA    device, one float (per-tensor scale of A)
+ *   sB    device, float[groups]: one scale per group's weight
+ *   sOut  device, one float; required iff out_dtype is an FP8 output
+ * Outputs (F32, F16, E4M3, E5M2), element value and errors as gemm_fp8_fmt;
+ * the rest as gemm_f16_grouped. The _bt call takes Bt[groups][N][K].
+ */
+int gemm_fp8_grouped(const uint8_t* A, int fmt_a, const uint8_t* B, int fmt_b, const int32_t* offsets,
+                     const float* sA, const float* sB, const float* sOut, void* C, int out_dtype,
+                     int64_t rows, int64_t N, int64_t K, int64_t groups, hipStream_t stream);
+int gemm_fp8_grouped_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b, const int32_t* offsets,
+                        const float* sA, const float* sB, const float* sOut, void* C, int out_dtype,
+                        int64_t rows, int64_t N, int64_t K, int64_t groups, hipStream_t stream);
+
+/*
+ * gemm_fp8_grouped_channel — gemm_fp8_grouped with a scale per row of A and
+ * per output column of each group's weight:
+ *   sA  device, float[rows];  sB  device, float[groups*N]
+ */
+int gemm_fp8_grouped_channel(const uint8_t* A, int fmt_a, const uint8_t* B, int fmt_b,
+                             const int32_t* offsets, const float* sA, const float* sB,
+                             const float* sOut, void* C, int out_dtype, int64_t rows, int64_t N,
+                             int64_t K, int64_t groups, hipStream_t stream);
+int gemm_fp8_grouped_channel_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b,
+                                const int32_t* offsets, const float* sA, const float* sB,
+                                const float* sOut, void* C, int out_dtype, int64_t rows, int64_t N,
+                                int64_t K, int64_t groups, hipStream_t stream);
+
+/*
+ * gemm_f16_grouped_wgrad — the gradient to the weights of grouped products:
+ * C[g] = A[rows of g]ᵀ · B[rows of g], zeros for an empty group.
+ *   A  device, _Float16[rows*M];  B  device, _Float16[rows*N]
+ *   C  device, float or _Float16 [groups*M*N] per out_dtype
+ * For C[r] = A[r]·W[g] with W[K,N] pass A and dC (M = K); for K-major weights
+ * W[N,K] pass dC and A. Rows of no group take no part.
+ */
+int gemm_f16_grouped_wgrad(const void* A, const void* B, const int32_t* offsets, void* C, int out_dtype,
+                           int64_t rows, int64_t M, int64_t N, int64_t groups, hipStream_t stream);
+
+/*
+ * gemm_f16_lora_bt — a product shared by all rows plus each row's low-rank
+ * adapter: C[r] = A[r]·Btᵀ + lscale[a]·(A[r]·LA[a]ᵀ)·LB[a]ᵀ, a = adapter[r].
+ *   A, Bt      device, _Float16[rows*K] and _Float16[N*K] (K-major weight)
+ *   LA, LB     device, _Float16[adapters*rank*K] and _Float16[adapters*N*rank]
+ *   adapter    device, int32[rows]; a value outside [0, adapters) (-1, say):
+ *              the row has no adapter, and no adapter's values reach it
+ *   lscale     device, float[adapters]
+ *   C          device, float or _Float16 [rows*N] per out_dtype
+ *   workspace  device, 16-byte aligned, at least
+ *              gemm_lora_workspace_size(rows, rank) bytes, contents on entry
+ *              and return unspecified; calls that share it must not overlap
+ * The low-rank values are FP32 (two launches). rank = 0 or adapters = 0 is the
+ * plain product (no workspace needed). Errors as gemm_f16_bt, plus
+ * GEMM_ERR_WORKSPACE.
+ */
+int gemm_f16_lora_bt(const void* A, const void* Bt, const void* LA, const void* LB, const int32_t* adapter,
+                     const float* lscale, void* C, int out_dtype, int64_t rows, int64_t N, int64_t K,
+                     int64_t rank, int64_t adapters, void* workspace, int64_t workspace_bytes,
+                     hipStream_t stream);
+
+/*
+ * gemm_fp8_lora_bt — the same with the shared product in FP8, scaled per
+ * channel (sA[rows], sB[N], as gemm_fp8_channel): A and Bt are codes, X the
+ * FP16 [rows*K] activations that the FP16 adapters multiply.
+ */
+int gemm_fp8_lora_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b, const float* sA,
+                     const float* sB, const void* X, const void* LA, const void* LB,
+                     const int32_t* adapter, const float* lscale, void* C, int out_dtype, int64_t rows,
+                     int64_t N, int64_t K, int64_t rank, int64_t adapters, void* workspace,
+                     int64_t workspace_bytes, hipStream_t stream);
+
+/* Bytes of workspace the adapter calls need (GEMM_ERR_DIM for a bad size). */
+int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank);
+
+/* ------------------------------------------------------- expert routing */
+
+/*
+ * moe_route_f32 — each token's topk experts, their weights, and the order of
+ * the (token, choice) rows by expert that the grouped products take.
+ *   logits   device, float[tokens*experts]
+ *   topk     1 .. min(32, experts); experts 1 .. 1024; tokens*topk < 2^31
+ *   renorm   != 0: weights are a softmax over the chosen logits; 0: over all of
+ *            the token's logits
+ *   expert   device, int32[tokens*topk], written: the largest logits first,
+ *            equal ones by the lower index; -inf and NaN are never chosen, and
+ *            places left over are -1
+ *   weight   device, float[tokens*topk], written; 0 where expert is -1
+ *   offsets  device, int32[experts + 1], written: rows of each expert
+ *   row      device, int32[tokens*topk], written: the row of (t, j) in the order
+ *            by (expert, t), -1 where expert is -1
+ *   token    device, int32[tokens*topk], written: the token of each row, -1 from
+ *            offsets[experts] on
+ *   workspace  device, 16-byte aligned, moe_route_workspace_size(tokens,
+ *            experts) bytes (0 for up to 64 tokens: may then be NULL)
+ * A logit of +inf takes weight 1 (shared equally by several). Deterministic.
+ */
+int moe_route_f32(const float* logits, int64_t tokens, int64_t experts, int64_t topk, int renorm,
+                  int32_t* expert, float* weight, int32_t* offsets, int32_t* row, int32_t* token,
+                  void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t moe_route_workspace_size(int64_t tokens, int64_t experts);
+
+/* moe_route_backward_f32 — dlogits[tokens*experts] (written) from dweight, with
+ * the logits and the expert and weight that moe_route_f32 wrote for them. */
+int moe_route_backward_f32(const float* logits, const int32_t* expert, const float* weight,
+                           const float* dweight, int64_t tokens, int64_t experts, int64_t topk,
+                           int renorm, float* dlogits, hipStream_t stream);
+
+/*
+ * moe_gather — y[r] = x[token[r]] for r < rows, zeros where token[r] is outside
+ * [0, tokens). x[tokens*width] and y[rows*width] hold elements of elem_bytes
+ * (1, 2 or 4; copied as they are).
+ */
+int moe_gather(const void* x, const int32_t* token, void* y, int64_t tokens, int64_t rows, int64_t width,
+               int elem_bytes, hipStream_t stream);
+
+/*
+ * moe_combine — y[t] = sum over j of weight[t,j]·z[row[t,j]], over the j whose
+ * row lies in [0, rows), summed in FP32 in the order of j.
+ *   z        device, float or _Float16 [rows*width] (z_dtype GEMM_OUT_F32 / _F16)
+ *   weight   device, float[tokens*topk], or NULL: every weight 1 (the gradient
+ *            of moe_gather)
+ *   y        device, float or _Float16 [tokens*width] (y_dtype)
+ */
+int moe_combine(const void* z, int z_dtype, const int32_t* row, const float* weight, void* y, int y_dtype,
+                int64_t tokens, int64_t topk, int64_t rows, int64_t width, hipStream_t stream);
+
+/*
+ * moe_combine_backward — dz[row[t,j]] = weight[t,j]·dy[t] and dweight[t,j] =
+ * <z[row[t,j]], dy[t]> (0 where (t,j) has no row). dy, z and dz are of one type
+ * (dtype GEMM_OUT_F32 or GEMM_OUT_F16). Each row may be named once; rows of dz
+ * that no (t,j) names are not written.
+ */
+int moe_combine_backward(const void* dy, const void* z, int dtype, const int32_t* row, const float* weight,
+                         void* dz, float* dweight, int64_t tokens, int64_t topk, int64_t rows,
+                         int64_t width, hipStream_t stream);
+
 /* Human-readable name of a status code (a static string). */
 const char* gemm_status_str(int status);
 

@@ -44,6 +44,23 @@ Functions keep the C names:
     gemm_fp8_exact(A, fmt_a, B, fmt_b, sA, sB, C, sOut=None, stream=None, out_fmt=None)
     gemm_fp8_exact_bt(A, fmt_a, Bt, fmt_b, sA, sB, C, sOut=None, stream=None, out_fmt=None)
     select_config_exact(out_dtype, M, N, K, fmt_a=0, fmt_b=0, b_kmajor=0) -> str
+  Products whose weight depends on the row (offsets int32 [groups + 1]; B one weight per group):
+    gemm_f16_grouped(A, B, offsets, C, stream=None)              B[groups, K, N]
+    gemm_f16_grouped_bt(A, Bt, offsets, C, stream=None)          Bt[groups, N, K]
+    gemm_fp8_grouped(A, fmt_a, B, fmt_b, offsets, sA, sB, C, sOut=None, stream=None, out_fmt=None)
+    gemm_fp8_grouped_bt, gemm_fp8_grouped_channel, gemm_fp8_grouped_channel_bt: the same arguments
+    gemm_f16_grouped_wgrad(A, B, offsets, C, stream=None)        C[groups, M, N]
+    gemm_f16_lora_bt(A, Bt, LA, LB, adapter, lscale, C, workspace=None, stream=None)
+    gemm_fp8_lora_bt(A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C, workspace=None, stream=None)
+    lora_workspace_size(rows, rank) -> int
+  Expert routing:
+    moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=None, row=None, token=None,
+                  workspace=None, stream=None) -> (expert, weight, offsets, row, token)
+    moe_route_backward_f32(logits, expert, weight, dweight, renorm=True, dlogits=None, stream=None) -> dlogits
+    moe_route_workspace_size(tokens, experts) -> int
+    moe_gather(x, token, y=None, stream=None) -> y
+    moe_combine(z, row, weight, y=None, stream=None) -> y
+    moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None) -> (dZ, dweight)
 The output dtype of a GEMM is taken from C: float32, float16, or 8-bit codes
 (uint8 or torch.float8_e4m3fn: E4M3; torch.float8_e5m2, or uint8 with
 out_fmt=FMT_E5M2: E5M2). FP8 operands are uint8 codes or torch float8 tensors.
@@ -165,6 +182,35 @@ def lib() -> ctypes.CDLL:
     L.gemm_fp8_exact_bt.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, i32, i64, i64, i64, vp]
     L.gemm_select_config_exact.restype = i32
     L.gemm_select_config_exact.argtypes = [i32, i64, i64, i64, i32, i32, i32, ctypes.c_char_p, i32]
+    for name in ("gemm_f16_grouped", "gemm_f16_grouped_bt"):
+        f = getattr(L, name)
+        f.restype = i32
+        f.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    for name in ("gemm_fp8_grouped", "gemm_fp8_grouped_bt", "gemm_fp8_grouped_channel",
+                 "gemm_fp8_grouped_channel_bt"):
+        f = getattr(L, name)
+        f.restype = i32
+        f.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    L.gemm_f16_grouped_wgrad.restype = i32
+    L.gemm_f16_grouped_wgrad.argtypes = [vp, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    L.gemm_f16_lora_bt.restype = i32
+    L.gemm_f16_lora_bt.argtypes = [vp] * 7 + [i32] + [i64] * 5 + [vp, i64, vp]
+    L.gemm_fp8_lora_bt.restype = i32
+    L.gemm_fp8_lora_bt.argtypes = [vp, i32, vp, i32] + [vp] * 8 + [i32] + [i64] * 5 + [vp, i64, vp]
+    L.gemm_lora_workspace_size.restype = i64
+    L.gemm_lora_workspace_size.argtypes = [i64, i64]
+    L.moe_route_f32.restype = i32
+    L.moe_route_f32.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.moe_route_workspace_size.restype = i64
+    L.moe_route_workspace_size.argtypes = [i64, i64]
+    L.moe_route_backward_f32.restype = i32
+    L.moe_route_backward_f32.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, vp]
+    L.moe_gather.restype = i32
+    L.moe_gather.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp]
+    L.moe_combine.restype = i32
+    L.moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, vp]
+    L.moe_combine_backward.restype = i32
+    L.moe_combine_backward.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i64, i64, i64, vp]
     _lib = L
     return L
 
@@ -744,3 +790,292 @@ def amax_quantize_fp8_pair_bt(xa, xb, fmt=FMT_E4M3, pow2=False, amax=None, scale
                                            workspace.numel() * workspace.element_size(), _stream_handle(stream)),
            "amax_quantize_fp8_pair_bt")
     return amax, scale, qa, qbt
+
+
+# ------------------------------------ products whose weight depends on the row
+
+def _need(t, dtype, shape, what):
+    """Checks an argument's type and shape (None in shape: any size)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
+        raise ValueError(f"{what} must have shape {tuple('any' if w is None else w for w in shape)}, "
+                         f"not {tuple(t.shape)}")
+
+
+def _scratch(nbytes, device, stream):
+    """Workspace of one call, kept by the allocator until the call's stream is past it."""
+    torch = _torch()
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if stream is not None and nbytes:
+        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return ws
+
+
+def _grouped_dims(A, B, offsets, C, bt):
+    if A.dim() != 2 or B.dim() != 3 or C.dim() != 2:
+        raise ValueError("A and C must be 2-D and B 3-D, one weight per group")
+    rows, K = A.shape
+    groups = B.shape[0]
+    N, K2 = (B.shape[1], B.shape[2]) if bt else (B.shape[2], B.shape[1])
+    if K2 != K or tuple(C.shape) != (rows, N):
+        raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
+    _need(offsets, _torch().int32, (groups + 1,), "offsets")
+    return rows, N, K, groups
+
+
+def _grouped_f16(name, A, B, offsets, C, bt, stream):
+    torch = _torch()
+    if A.dtype != torch.float16 or B.dtype != torch.float16:
+        raise ValueError(f"{name} takes float16 operands")
+    rows, N, K, groups = _grouped_dims(A, B, offsets, C, bt)
+    _check(getattr(lib(), name)(_ptr(A), _ptr(B), _ptr(offsets), _ptr(C), _out_dtype(C), rows, N, K, groups,
+                                _stream_handle(stream)), name)
+    return C
+
+
+def gemm_f16_grouped(A, B, offsets, C, stream=None):
+    """C[r] = A[r] @ B[g] for the rows offsets[g] <= r < offsets[g + 1]; float16 A[rows, K] and B[groups, K, N],
+    int32 offsets[groups + 1] on the device; C float32 or float16 [rows, N], zeros in rows of no group."""
+    return _grouped_f16("gemm_f16_grouped", A, B, offsets, C, False, stream)
+
+
+def gemm_f16_grouped_bt(A, Bt, offsets, C, stream=None):
+    """gemm_f16_grouped with K-major weights Bt[groups, N, K]: C[r] = A[r] @ Bt[g].T."""
+    return _grouped_f16("gemm_f16_grouped_bt", A, Bt, offsets, C, True, stream)
+
+
+def _grouped_fp8(name, A, fmt_a, B, fmt_b, offsets, sA, sB, C, sOut, stream, out_fmt, bt, channel):
+    torch = _torch()
+    A, B = _u8(A, fmt_a), _u8(B, fmt_b)
+    out = _out_dtype(C, out_fmt)
+    Cv = _u8(C) if out in (OUT_E4M3, OUT_E5M2) else C
+    rows, N, K, groups = _grouped_dims(A, B, offsets, Cv, bt)
+    for what, s, n in (("sA", sA, rows if channel else 1), ("sB", sB, groups * N if channel else groups)):
+        if s.dtype != torch.float32 or s.numel() != n:
+            raise ValueError(f"{what} must hold {n} float32 scales")
+    _check(getattr(lib(), name)(_ptr(A), int(fmt_a), _ptr(B), int(fmt_b), _ptr(offsets), _ptr(sA), _ptr(sB),
+                                _ptr(sOut), _ptr(Cv), out, rows, N, K, groups, _stream_handle(stream)), name)
+    return C
+
+
+def gemm_fp8_grouped(A, fmt_a, B, fmt_b, offsets, sA, sB, C, sOut=None, stream=None, out_fmt=None):
+    """gemm_f16_grouped for FP8 codes A[rows, K] and B[groups, K, N]: C[r] = (sA*A[r]) @ (sB[g]*B[g]), sA one
+    float32 scale, sB one per group; C float32, float16 or 8-bit codes (with sOut)."""
+    return _grouped_fp8("gemm_fp8_grouped", A, fmt_a, B, fmt_b, offsets, sA, sB, C, sOut, stream, out_fmt, False,
+                        False)
+
+
+def gemm_fp8_grouped_bt(A, fmt_a, Bt, fmt_b, offsets, sA, sB, C, sOut=None, stream=None, out_fmt=None):
+    """gemm_fp8_grouped with K-major weights Bt[groups, N, K]."""
+    return _grouped_fp8("gemm_fp8_grouped_bt", A, fmt_a, Bt, fmt_b, offsets, sA, sB, C, sOut, stream, out_fmt, True,
+                        False)
+
+
+def gemm_fp8_grouped_channel(A, fmt_a, B, fmt_b, offsets, sA, sB, C, sOut=None, stream=None, out_fmt=None):
+    """gemm_fp8_grouped with a scale per row of A (sA[rows]) and per output column of each weight (sB[groups, N])."""
+    return _grouped_fp8("gemm_fp8_grouped_channel", A, fmt_a, B, fmt_b, offsets, sA, sB, C, sOut, stream, out_fmt,
+                        False, True)
+
+
+def gemm_fp8_grouped_channel_bt(A, fmt_a, Bt, fmt_b, offsets, sA, sB, C, sOut=None, stream=None, out_fmt=None):
+    """gemm_fp8_grouped_channel with K-major weights Bt[groups, N, K]."""
+    return _grouped_fp8("gemm_fp8_grouped_channel_bt", A, fmt_a, Bt, fmt_b, offsets, sA, sB, C, sOut, stream, out_fmt,
+                        True, True)
+
+
+def gemm_f16_grouped_wgrad(A, B, offsets, C, stream=None):
+    """C[g] = A[rows of g].T @ B[rows of g] for float16 A[rows, M], B[rows, N]; C float32 or float16 [groups, M, N],
+    zeros for an empty group."""
+    torch = _torch()
+    if A.dtype != torch.float16 or B.dtype != torch.float16:
+        raise ValueError("gemm_f16_grouped_wgrad takes float16 operands")
+    if A.dim() != 2 or B.dim() != 2 or C.dim() != 3 or A.shape[0] != B.shape[0]:
+        raise ValueError("A[rows, M], B[rows, N] and C[groups, M, N] are needed")
+    rows, M, N, groups = A.shape[0], A.shape[1], B.shape[1], C.shape[0]
+    if tuple(C.shape) != (groups, M, N):
+        raise ValueError(f"shape mismatch: A{tuple(A.shape)} B{tuple(B.shape)} C{tuple(C.shape)}")
+    _need(offsets, torch.int32, (groups + 1,), "offsets")
+    _check(lib().gemm_f16_grouped_wgrad(_ptr(A), _ptr(B), _ptr(offsets), _ptr(C), _out_dtype(C), rows, M, N, groups,
+                                        _stream_handle(stream)), "gemm_f16_grouped_wgrad")
+    return C
+
+
+def lora_workspace_size(rows: int, rank: int) -> int:
+    n = int(lib().gemm_lora_workspace_size(rows, rank))
+    _check(n if n < 0 else 0, "gemm_lora_workspace_size")
+    return n
+
+
+def _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream):
+    torch = _torch()
+    rows, K = X.shape
+    if LA.dim() != 3 or LB.dim() != 3:
+        raise ValueError("LA[adapters, rank, K] and LB[adapters, N, rank] are needed")
+    adapters, rank = LA.shape[0], LA.shape[1]
+    _need(LA, torch.float16, (adapters, rank, K), "LA")
+    _need(LB, torch.float16, (adapters, N, rank), "LB")
+    _need(adapter, torch.int32, (rows,), "adapter")
+    _need(lscale, torch.float32, (adapters,), "lscale")
+    if workspace is None:
+        workspace = _scratch(lora_workspace_size(rows, rank), X.device, stream)
+    return rows, K, rank, adapters, workspace
+
+
+def gemm_f16_lora_bt(A, Bt, LA, LB, adapter, lscale, C, workspace=None, stream=None):
+    """C[r] = A[r] @ Bt.T + lscale[a] * (A[r] @ LA[a].T) @ LB[a].T with a = adapter[r] (int32, -1: none); float16
+    A[rows, K], Bt[N, K], LA[adapters, rank, K], LB[adapters, N, rank], float32 lscale[adapters]; C float32 or
+    float16 [rows, N]. workspace: lora_workspace_size(rows, rank) bytes, allocated when None."""
+    torch = _torch()
+    if A.dtype != torch.float16 or Bt.dtype != torch.float16:
+        raise ValueError("gemm_f16_lora_bt takes float16 operands")
+    M, N, K = _dims_bt(A, Bt, C)
+    rows, K, rank, adapters, ws = _lora_dims(A, N, LA, LB, adapter, lscale, workspace, stream)
+    _check(lib().gemm_f16_lora_bt(_ptr(A), _ptr(Bt), _ptr(LA), _ptr(LB), _ptr(adapter), _ptr(lscale), _ptr(C),
+                                  _out_dtype(C), rows, N, K, rank, adapters, *_ws_args(ws), _stream_handle(stream)),
+           "gemm_f16_lora_bt")
+    return C
+
+
+def gemm_fp8_lora_bt(A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C, workspace=None, stream=None):
+    """gemm_f16_lora_bt with the shared product in FP8: codes A[rows, K] and Bt[N, K] with float32 scales sA[rows]
+    and sB[N], and the float16 activations X[rows, K] that the adapters multiply."""
+    torch = _torch()
+    A, Bt = _u8(A, fmt_a), _u8(Bt, fmt_b)
+    M, N, K = _dims_bt(A, Bt, C)
+    _need(sA, torch.float32, (M,), "sA")
+    _need(sB, torch.float32, (N,), "sB")
+    _need(X, torch.float16, (M, K), "X")
+    rows, K, rank, adapters, ws = _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream)
+    _check(lib().gemm_fp8_lora_bt(_ptr(A), int(fmt_a), _ptr(Bt), int(fmt_b), _ptr(sA), _ptr(sB), _ptr(X), _ptr(LA),
+                                  _ptr(LB), _ptr(adapter), _ptr(lscale), _ptr(C), _out_dtype(C), rows, N, K, rank,
+                                  adapters, *_ws_args(ws), _stream_handle(stream)), "gemm_fp8_lora_bt")
+    return C
+
+
+# -------------------------------------------------------------- expert routing
+
+def moe_route_workspace_size(tokens: int, experts: int) -> int:
+    n = int(lib().moe_route_workspace_size(tokens, experts))
+    _check(n if n < 0 else 0, "moe_route_workspace_size")
+    return n
+
+
+def moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=None, row=None, token=None,
+                  workspace=None, stream=None):
+    """The topk experts of each token and the order of the rows by expert, from float32 logits[tokens, experts]:
+    (expert[tokens, topk] int32, weight[tokens, topk] float32, offsets[experts + 1], row[tokens, topk],
+    token[tokens * topk]). Equal logits go to the lower index; -inf and NaN are never chosen (expert and row -1,
+    weight 0). renorm: weights sum to 1 over the chosen experts, else they are the softmax over all."""
+    torch = _torch()
+    _need(logits, torch.float32, (None, None), "logits")
+    T, E = logits.shape
+    topk = int(topk)
+    dev = logits.device
+    if topk < 1 or topk > E:
+        raise ValueError(f"topk must be between 1 and the {E} experts, not {topk}")
+
+    def out(t, dtype, shape, what):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=dev)
+        _need(t, dtype, shape, what)
+        return t
+
+    expert = out(expert, torch.int32, (T, topk), "expert")
+    weight = out(weight, torch.float32, (T, topk), "weight")
+    offsets = out(offsets, torch.int32, (E + 1,), "offsets")
+    row = out(row, torch.int32, (T, topk), "row")
+    token = out(token, torch.int32, (T * topk,), "token")
+    if workspace is None:
+        n = moe_route_workspace_size(T, E)
+        workspace = _scratch(n, dev, stream) if n else None
+    _check(lib().moe_route_f32(_ptr(logits), T, E, topk, 1 if renorm else 0, _ptr(expert), _ptr(weight),
+                               _ptr(offsets), _ptr(row), _ptr(token), *_ws_args(workspace), _stream_handle(stream)),
+           "moe_route_f32")
+    return expert, weight, offsets, row, token
+
+
+def moe_route_backward_f32(logits, expert, weight, dweight, renorm=True, dlogits=None, stream=None):
+    """dlogits[tokens, experts] of moe_route_f32's weights, from dweight[tokens, topk]."""
+    torch = _torch()
+    _need(logits, torch.float32, (None, None), "logits")
+    T, E = logits.shape
+    _need(expert, torch.int32, (T, None), "expert")
+    K = expert.shape[1]
+    _need(weight, torch.float32, (T, K), "weight")
+    _need(dweight, torch.float32, (T, K), "dweight")
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+    _need(dlogits, torch.float32, (T, E), "dlogits")
+    _check(lib().moe_route_backward_f32(_ptr(logits), _ptr(expert), _ptr(weight), _ptr(dweight), T, E, K,
+                                        1 if renorm else 0, _ptr(dlogits), _stream_handle(stream)),
+           "moe_route_backward_f32")
+    return dlogits
+
+
+def moe_gather(x, token, y=None, stream=None):
+    """y[r] = x[token[r]] for x[tokens, width] of any 1-, 2- or 4-byte type and int32 token[rows]; zeros where
+    token[r] is outside [0, tokens)."""
+    torch = _torch()
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, width]")
+    _need(token, torch.int32, (None,), "token")
+    rows = token.shape[0]
+    if y is None:
+        y = torch.empty((rows, x.shape[1]), dtype=x.dtype, device=x.device)
+    _need(y, x.dtype, (rows, x.shape[1]), "y")
+    _check(lib().moe_gather(_ptr(x), _ptr(token), _ptr(y), x.shape[0], rows, x.shape[1], x.element_size(),
+                            _stream_handle(stream)), "moe_gather")
+    return y
+
+
+def _float_dtype(t, what):
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return OUT_F32
+    if t.dtype == torch.float16:
+        return OUT_F16
+    raise ValueError(f"{what} must be float32 or float16, not {t.dtype}")
+
+
+def moe_combine(z, row, weight, y=None, stream=None):
+    """y[t] = sum_j weight[t, j] * z[row[t, j]] over the j with a row (int32 row[tokens, topk], -1: none), summed in
+    float32; z[rows, width] and y[tokens, width] float32 or float16 (y as z when None). weight None: all 1, the
+    gradient of moe_gather."""
+    torch = _torch()
+    zt = _float_dtype(z, "z")
+    if z.dim() != 2:
+        raise ValueError("z must be [rows, width]")
+    _need(row, torch.int32, (None, None), "row")
+    T, K = row.shape
+    if weight is not None:
+        _need(weight, torch.float32, (T, K), "weight")
+    if y is None:
+        y = torch.empty((T, z.shape[1]), dtype=z.dtype, device=z.device)
+    yt = _float_dtype(y, "y")
+    _need(y, y.dtype, (T, z.shape[1]), "y")
+    _check(lib().moe_combine(_ptr(z), zt, _ptr(row), _ptr(weight), _ptr(y), yt, T, K, z.shape[0], z.shape[1],
+                             _stream_handle(stream)), "moe_combine")
+    return y
+
+
+def moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None):
+    """(dZ, dweight) of moe_combine: dZ[row[t, j]] = weight[t, j] * dy[t], dweight[t, j] = <z[row[t, j]], dy[t]>.
+    dy, z and dZ are of one type (float32 or float16). Rows that no (t, j) names are not written; dZ=None allocates
+    zeros."""
+    torch = _torch()
+    dt = _float_dtype(z, "z")
+    _need(row, torch.int32, (None, None), "row")
+    T, K = row.shape
+    _need(weight, torch.float32, (T, K), "weight")
+    _need(z, z.dtype, (None, None), "z")
+    _need(dy, z.dtype, (T, z.shape[1]), "dy")
+    if dZ is None:
+        dZ = torch.zeros_like(z)
+    _need(dZ, z.dtype, tuple(z.shape), "dZ")
+    if dweight is None:
+        dweight = torch.empty((T, K), dtype=torch.float32, device=z.device)
+    _need(dweight, torch.float32, (T, K), "dweight")
+    _check(lib().moe_combine_backward(_ptr(dy), _ptr(z), dt, _ptr(row), _ptr(weight), _ptr(dZ), _ptr(dweight), T, K,
+                                      z.shape[0], z.shape[1], _stream_handle(stream)), "moe_combine_backward")
+    return dZ, dweight

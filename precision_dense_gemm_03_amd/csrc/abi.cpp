@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstring>
 
+#include "abi_common.h"
 #include "kernels.h"
 #include "libgemm.h"
 
@@ -17,37 +18,19 @@ using namespace libgemm;
 
 namespace {
 
-constexpr int64_t kMaxDim = 0x7FFFFFFF;
 constexpr int kMaxDevices = 64;
 
-bool dim_ok(int64_t d) { return d >= 0 && d <= kMaxDim; }
-
-// Byte counts are formed only after this check: an operand of 2^62 bytes or
-// more is a GEMM_ERR_DIM (no device holds one), so every later product of a
-// dimension pair and an element size fits in int64.
-constexpr unsigned __int128 kMaxBytes = (unsigned __int128)1 << 62;
-bool bytes_ok(int64_t a, int64_t b, int64_t es) {
-    if (a < 0 || b < 0) return false;
-    return (unsigned __int128)a * (unsigned __int128)b * (unsigned __int128)es < kMaxBytes;
-}
 // A[M,K] with element size ea, B[K,N] with eb, C[M,N] with ec.
 bool gemm_sizes_ok(int64_t M, int64_t N, int64_t K, int64_t ea, int64_t eb, int64_t ec) {
     return dim_ok(M) && dim_ok(N) && dim_ok(K) && bytes_ok(M, K, ea) && bytes_ok(K, N, eb) && bytes_ok(M, N, ec);
 }
 
-// Byte ranges [p, p+n) and [q, q+m) overlap (empty ranges never do).
-bool overlaps(const void* p, int64_t n, const void* q, int64_t m) {
-    if (!p || !q || n <= 0 || m <= 0) return false;
-    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-    return a < b + (uintptr_t)m && b < a + (uintptr_t)n;
-}
-
-int64_t out_size(int out_dtype) { return out_dtype == GEMM_OUT_F32 ? 4 : (out_dtype == GEMM_OUT_F16 ? 2 : 1); }
-
 // 0 unknown, 1 gfx950, 2 other architecture; filled once per device.
 std::atomic<int> g_device_state[kMaxDevices];
 
-int check_device() {
+}  // namespace
+
+int libgemm::check_device() {
     int dev = -1;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices) {
         (void)hipGetLastError();
@@ -66,13 +49,7 @@ int check_device() {
     return st == 1 ? GEMM_OK : GEMM_ERR_DEVICE;
 }
 
-int status_of(hipError_t e) {
-    if (e == hipSuccess) return GEMM_OK;
-    (void)hipGetLastError();
-    return GEMM_ERR_LAUNCH;
-}
-
-bool fp8_out(int out_dtype) { return out_dtype == GEMM_OUT_E4M3 || out_dtype == GEMM_OUT_E5M2; }
+namespace {
 
 int run_gemm(int kind, const GemmArgs& a) {
     int st = check_device();

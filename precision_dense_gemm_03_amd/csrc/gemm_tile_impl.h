@@ -178,6 +178,22 @@ __device__ __forceinline__ v4u load_chunk_guarded(const uint8_t* row_ptr, bool r
     return v4u{w[0], w[1], w[2], w[3]};
 }
 
+typedef v4u v4u_any __attribute__((aligned(1)));
+
+// load_chunk_guarded for any alignment: a whole chunk is one load; a chunk
+// that the row's end cuts is the 16 bytes before that end, shifted down (rows
+// shorter than a chunk go element by element).
+template <int ES>
+__device__ __forceinline__ v4u load_chunk_any(const uint8_t* row_ptr, bool row_ok, int64_t col, int64_t limit) {
+    constexpr int VE = 16 / ES;
+    if (!row_ok || col >= limit) return v4u{0u, 0u, 0u, 0u};
+    if (col + VE <= limit) return *reinterpret_cast<const v4u_any*>(row_ptr + col * ES);
+    if (limit < VE) return load_chunk_guarded<ES>(row_ptr, row_ok, col, limit);
+    const v4u v = *reinterpret_cast<const v4u_any*>(row_ptr + (limit - VE) * ES);
+    const unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v) >> (8 * ES * (int)(col + VE - limit));
+    return __builtin_bit_cast(v4u, w);
+}
+
 // Eight FP8 codes starting at element col of a row, zero beyond limit and for
 // rows out of range.
 __device__ __forceinline__ v2i load_codes8_guarded(const uint8_t* row_ptr, bool row_ok, int64_t col, int64_t limit) {
@@ -207,11 +223,24 @@ __device__ __forceinline__ void store_one(void* C, int64_t idx, float y, int efl
 // the exact FP8 mode (ES = 2, GES = 1): FP8 codes are widened to FP16 as they
 // are staged (eflags EPI_A_E5M2 / EPI_B_E5M2 give the operand formats) and
 // summed on the FP16 matrix cores.
-template <int ES, int OUT, int BM, int BN, int BK, int WM, int WN, int FA, int FB, bool BT, int GES = ES>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C, int M, int N, int K,
-    const float* __restrict__ sA, const float* __restrict__ sB, const float* __restrict__ sOut, int tiles_m,
-    int tiles_n, int aligned, int eflags, int kchunk) {
+//
+// UA (the products whose weight depends on the row): operands of any element
+// alignment keep the vector loads (gfx950's global loads take any address),
+// and a row's last partial chunk is read as the 16 bytes that end the row,
+// shifted. Ext: what is added to the products before the store (NoExtra, or
+// LoraExtra of lora_extra.h).
+struct NoExtra {
+    static constexpr bool kActive = false;
+};
+
+// One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N,
+// K range `split` of kchunk.
+template <int ES, int OUT, int BM, int BN, int BK, int WM, int WN, int FA, int FB, bool BT, int GES = ES,
+          bool UA = false, class Ext = NoExtra>
+__device__ __forceinline__ void tile_body(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
+                                          void* __restrict__ C, int M, int N, int K, const float* __restrict__ sA,
+                                          const float* __restrict__ sB, const float* __restrict__ sOut, int m0, int n0,
+                                          int aligned, int eflags, int kchunk, int split, const Ext& ext = Ext{}) {
     using T = Tile<ES, BM, BN, BK, WM, WN, BT>;
     __shared__ __attribute__((aligned(16))) uint8_t smem_raw[2 * T::STAGE];
     LDS_AS uint8_t* smem = (LDS_AS uint8_t*)smem_raw;
@@ -221,14 +250,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
     const int wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
 
-    int tile_m, tile_n;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
-    const int m0 = tile_m * BM;
-    const int n0 = tile_n * BN;
     const bool interior_mn = aligned && (m0 + BM <= M) && (n0 + BN <= N);
-    // Split-K: workgroup row blockIdx.y sums K range [kbeg, kend) (the whole
-    // of K when the launch is not split). kbeg is a multiple of BK.
-    const int split = blockIdx.y;
+    // Split-K: a workgroup sums K range [kbeg, kend) (the whole of K when the
+    // launch is not split). kbeg is a multiple of BK.
     const int kbeg = split * kchunk;
     const int klen = min(K - kbeg, kchunk);
     const int kend = kbeg + klen;
@@ -278,6 +302,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
         if constexpr (kWiden) {
             const v2i w = *reinterpret_cast<const v2i*>(p);
             return widen8_fp8((uint32_t)w.x, (uint32_t)w.y, e5m2);
+        } else if constexpr (UA) {
+            return *reinterpret_cast<const v4u_any*>(p);
         } else {
             return *reinterpret_cast<const v4u*>(p);
         }
@@ -287,6 +313,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
         if constexpr (kWiden) {
             const v2i w = load_codes8_guarded(row_ptr, row_ok, col, limit);
             return widen8_fp8((uint32_t)w.x, (uint32_t)w.y, e5m2);
+        } else if constexpr (UA) {
+            return load_chunk_any<ES>(row_ptr, row_ok, col, limit);
         } else {
             return load_chunk_guarded<ES>(row_ptr, row_ok, col, limit);
         }
@@ -307,7 +335,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
             const int r = min(n0 + b_row + i * T::B_RPP, N - 1) - n0;
             b_offs[i] = (uint32_t)((r * K + b_col * T::VE) * GES);
         } else {
-            const int c = min(n0 + b_col * T::VE, N - T::VE) - n0;
+            const int c = (UA ? max(min(n0 + b_col * T::VE, N - T::VE), 0) : min(n0 + b_col * T::VE, N - T::VE)) - n0;
             b_offs[i] = (uint32_t)(((b_row + i * T::B_RPP) * N + c) * GES);
         }
     }
@@ -467,7 +495,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
         // the K tail and unaligned operands load each chunk with element
         // guards straight into LDS.
         auto fast = [&](int kt) __attribute__((always_inline)) {
-            return aligned && offsets_fit && (kt + 1) * BK <= klen;
+            // (a column chunk that N cuts cannot be re-read from the last whole one)
+            const bool whole = !UA || BT || N % T::VE == 0 || n0 + BN <= N;
+            return aligned && whole && offsets_fit && (kt + 1) * BK <= klen;
         };
         if (fast(0)) {
             load_a(0);
@@ -509,6 +539,29 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
     const float scale = partial ? 1.0f : epilogue_base(sA, sB, sOut, OUT == OUT_E4M3, chan);  // both FP8 outputs
     const int row0 = m0 + wm * T::WTM + 4 * g;
     const int col0 = n0 + wn * T::WTN + j16;
+    if constexpr (Ext::kActive) {
+        // scaled here, added to, stored as it is
+#pragma unroll
+        for (int tm = 0; tm < T::TM; ++tm)
+#pragma unroll
+            for (int tn = 0; tn < T::TN; ++tn)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    acc[tm][tn][r] *= scale;
+                    if (chan) acc[tm][tn][r] *= sA[min(row0 + tm * 16 + r, M - 1)] * sB[min(col0 + tn * 16, N - 1)];
+                }
+        ext.template add16<T::TM, T::TN>(acc, m0 + wm * T::WTM, n0 + wn * T::WTN, M, N);
+#pragma unroll
+        for (int tm = 0; tm < T::TM; ++tm)
+#pragma unroll
+            for (int tn = 0; tn < T::TN; ++tn)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = row0 + tm * 16 + r, col = col0 + tn * 16;
+                    if (row < M && col < N) store_one<OUT>(C, (int64_t)row * N + col, acc[tm][tn][r], eflags);
+                }
+        return;
+    }
     if (interior_mn) {
 #pragma unroll
         for (int tm = 0; tm < T::TM; ++tm)
@@ -536,6 +589,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
                     }
                 }
     }
+}
+
+template <int ES, int OUT, int BM, int BN, int BK, int WM, int WN, int FA, int FB, bool BT, int GES = ES>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_tile_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C, int M, int N, int K,
+    const float* __restrict__ sA, const float* __restrict__ sB, const float* __restrict__ sOut, int tiles_m,
+    int tiles_n, int aligned, int eflags, int kchunk) {
+    int tile_m, tile_n;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
+    tile_body<ES, OUT, BM, BN, BK, WM, WN, FA, FB, BT, GES>(A, B, C, M, N, K, sA, sB, sOut, tile_m * BM, tile_n * BN,
+                                                            aligned, eflags, kchunk, blockIdx.y);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }

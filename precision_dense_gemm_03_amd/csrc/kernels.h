@@ -32,6 +32,24 @@ struct GemmArgs {
     int b_kmajor = 0;
 };
 
+// Products whose weight depends on the row: the arguments of a plain product
+// with M = rows, and the cut of the rows into groups (row_groups.h).
+struct GroupedArgs : GemmArgs {
+    const int32_t* offsets = nullptr;   // device, groups + 1
+    int64_t groups = 0;
+};
+
+// A product with K-major weight plus the low-rank term of each row's adapter.
+struct LoraArgs : GemmArgs {
+    const void* X = nullptr;            // FP16 [M, K]: what the adapters multiply (A itself for FP16)
+    const void* LA = nullptr;           // FP16 [adapters, rank, K]
+    const void* LB = nullptr;           // FP16 [adapters, N, rank]
+    const int32_t* adapter = nullptr;   // device, M: the row's adapter, none outside [0, adapters)
+    const float* lscale = nullptr;      // device, adapters
+    int64_t rank = 0, adapters = 0;
+    float* low = nullptr;               // workspace: [M, rank rounded up to 8]
+};
+
 typedef hipError_t (*GemmLauncher)(const GemmArgs&);
 
 // One entry of the compiled-in configuration table.
@@ -89,6 +107,21 @@ const GemmConfig* select_config_exact(int out_dtype, int64_t M, int64_t N, int64
 
 SplitPlan plan_splitk(int kind, int out_dtype, int64_t M, int64_t N, int64_t K, int fmt_a = 0, int fmt_b = 0,
                       int b_kmajor = 0);
+
+// Products grouped by rows (grouped.cpp chooses the kernel), kind: OperandKind.
+hipError_t launch_grouped(int kind, const GroupedArgs& a);
+// The register-staged tile kernel over row groups: any sizes and alignment.
+hipError_t launch_grouped_tile_f16(const GroupedArgs& a, int bm);
+hipError_t launch_grouped_tile_fp8(const GroupedArgs& a, int bm);
+// C[g] = A[rows of g]^T B[rows of g] for FP16 A[rows, M], B[rows, N]; C F32 or
+// F16 [groups, M, N]. K holds the number of rows.
+hipError_t launch_grouped_wgrad(const GroupedArgs& a);
+// low[i, r] = lscale[a_i] <X[i], LA[a_i, r]>, zero for rows without an adapter
+// and from rank on.
+hipError_t launch_lora_low(const LoraArgs& a);
+hipError_t launch_lora(int kind, const LoraArgs& a);
+hipError_t launch_lora_tile_f16(const LoraArgs& a, int bm);
+hipError_t launch_lora_tile_fp8(const LoraArgs& a, int bm);
 
 // C = epilogue(sum over a.splits slices of a.ws), in slice order.
 hipError_t launch_splitk_reduce(const GemmArgs& a);

@@ -1,0 +1,173 @@
+// The low-rank values of per-row adapters, for gfx950:
+//
+//   low[i, r] = lscale[a_i] sum_k X[i, k] LA[a_i, r, k]      (FP32)
+//
+// zero for rows without an adapter and for r from rank to rank_p (the next
+// multiple of 8); the product kernels add low LB^T (lora_extra.h).
+//
+// Few rows: each usually has its own adapter, so nothing is shared between
+// rows and a wave takes one (i, r): a dot product over K, both sides read in
+// 16-byte pieces, rows * rank waves. More rows: a workgroup takes 16 rows and
+// its 8 waves share out K in tiles of 64 (128 bytes of each row); every
+// adapter present multiplies the block on the matrix cores (LA as the first
+// operand, so a lane ends with one row's four neighbouring values) and its
+// rows keep the result; the waves' sums join in LDS in wave order.
+#include <hip/hip_runtime.h>
+
+#include "device_common.h"
+#include "kernels.h"
+
+namespace libgemm {
+namespace {
+
+typedef v4u any16 __attribute__((aligned(2)));
+
+// Eight halves from k on, zero from K on.
+__device__ __forceinline__ v8h chunk8(const _Float16* row, int k, int K) {
+    if (k + 8 <= K) return __builtin_bit_cast(v8h, *reinterpret_cast<const any16*>(row + k));
+    v8h v;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? row[k + i] : (_Float16)0.0f;
+    return v;
+}
+
+__global__ __launch_bounds__(256) void lora_low_dot_kernel(const _Float16* __restrict__ X,
+                                                           const _Float16* __restrict__ LA,
+                                                           const int32_t* __restrict__ adapter,
+                                                           const float* __restrict__ lscale, int64_t waves, int K,
+                                                           int rank, int rank_p, int adapters,
+                                                           float* __restrict__ low) {
+    const int lane = threadIdx.x & 63;
+    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (w >= waves) return;
+    const int64_t row = w / rank_p;
+    const int r = (int)(w % rank_p);
+    const int a = adapter[row];
+    const bool has = a >= 0 && a < adapters && r < rank;
+    float sum = 0.0f;
+    if (has) {
+        const _Float16* x = X + row * K;
+        const _Float16* l = LA + ((int64_t)a * rank + r) * K;
+        constexpr int U = 8;   // pairs of loads in flight
+        for (int k0 = 8 * lane; k0 < K; k0 += 512 * U) {
+            v8h xv[U], lv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int k = k0 + 512 * u;
+                xv[u] = lv[u] = v8h{0, 0, 0, 0, 0, 0, 0, 0};
+                if (k < K) {
+                    xv[u] = chunk8(x, k, K);
+                    lv[u] = chunk8(l, k, K);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum = __builtin_fmaf((float)xv[u][i], (float)lv[u][i], sum);
+        }
+#pragma unroll
+        for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
+    }
+    if (lane == 0) low[row * rank_p + r] = has ? sum * lscale[a] : 0.0f;
+}
+
+constexpr int kLowWaves = 8;
+
+// RB: blocks of 16 low-rank values; blockIdx.y takes 16 RB of them.
+template <int RB>
+__global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(const _Float16* __restrict__ X,
+                                                                  const _Float16* __restrict__ LA,
+                                                                  const int32_t* __restrict__ adapter,
+                                                                  const float* __restrict__ lscale, int M, int K,
+                                                                  int rank, int rank_p, int adapters,
+                                                                  float* __restrict__ low) {
+    __shared__ v4f red[kLowWaves * RB * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j16 = lane & 15, g = lane >> 4;
+    const int row = blockIdx.x * 16 + j16, r0 = blockIdx.y * 16 * RB;
+    int mine = row < M ? adapter[row] : -1;
+    if (mine < 0 || mine >= adapters) mine = -1;
+    const _Float16* x = X + (int64_t)min(row, M - 1) * K;
+    v4f fin[RB];
+#pragma unroll
+    for (int b = 0; b < RB; ++b) fin[b] = v4f{0.f, 0.f, 0.f, 0.f};
+    const int tiles = (K + 63) / 64;
+    for (uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0) & 0xFFFFu; left;) {
+        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+        left &= ~((uint32_t)__builtin_amdgcn_ballot_w64(mine == a) & 0xFFFFu);
+        const _Float16* la = LA + (int64_t)a * rank * K;
+        v4f cur[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) cur[b] = v4f{0.f, 0.f, 0.f, 0.f};
+        auto load = [&](int t, v8h (&xo)[2], v8h (&lo)[RB][2]) __attribute__((always_inline)) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const int k = 64 * t + 32 * s + 8 * g;
+                xo[s] = chunk8(x, k, K);
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    lo[b][s] = chunk8(la + (int64_t)min(r0 + 16 * b + j16, rank - 1) * K, k, K);
+            }
+        };
+        v8h xo[2], lo[RB][2];
+        if (wave < tiles) load(wave, xo, lo);
+        for (int t = wave; t < tiles; t += kLowWaves) {
+            v8h xn[2], ln[RB][2];
+            if (t + kLowWaves < tiles) load(t + kLowWaves, xn, ln);
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    cur[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo[b][s], xo[s], cur[b], 0, 0, 0);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                xo[s] = xn[s];
+#pragma unroll
+                for (int b = 0; b < RB; ++b) lo[b][s] = ln[b][s];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) fin[b][e] = mine == a ? cur[b][e] : fin[b][e];
+    }
+#pragma unroll
+    for (int b = 0; b < RB; ++b) red[(wave * RB + b) * 64 + lane] = fin[b];
+    __syncthreads();
+    const float scale = mine >= 0 ? lscale[mine] : 0.0f;
+    for (int b = wave; b < RB; b += kLowWaves) {
+        v4f sum = red[b * 64 + lane];
+        for (int w = 1; w < kLowWaves; ++w) sum += red[(w * RB + b) * 64 + lane];
+        const int r = r0 + 16 * b + 4 * g;
+        if (row < M && r < rank_p) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] = mine >= 0 && r + e < rank ? sum[e] * scale : 0.0f;
+            *reinterpret_cast<v4f*>(low + (int64_t)row * rank_p + r) = sum;
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_lora_low(const LoraArgs& a) {
+    const _Float16* X = reinterpret_cast<const _Float16*>(a.X);
+    const _Float16* LA = reinterpret_cast<const _Float16*>(a.LA);
+    const int rank = (int)a.rank, rank_p = (rank + 7) / 8 * 8;
+    if (a.M <= 64) {
+        const int64_t waves = a.M * rank_p;
+        lora_low_dot_kernel<<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(
+            X, LA, a.adapter, a.lscale, waves, (int)a.K, rank, rank_p, (int)a.adapters, a.low);
+        return hipGetLastError();
+    }
+    const unsigned blocks = (unsigned)((a.M + 15) / 16);
+#define LIBGEMM_GO(RB)                                                                                        \
+    lora_low_kernel<RB><<<dim3(blocks, (unsigned)((rank + 16 * RB - 1) / (16 * RB))), 64 * kLowWaves, 0, a.stream>>>( \
+        X, LA, a.adapter, a.lscale, (int)a.M, (int)a.K, rank, rank_p, (int)a.adapters, a.low)
+    if (rank <= 16) LIBGEMM_GO(1);
+    else if (rank <= 32) LIBGEMM_GO(2);
+    else if (rank <= 64) LIBGEMM_GO(4);
+    else LIBGEMM_GO(8);
+#undef LIBGEMM_GO
+    return hipGetLastError();
+}
+
+}  // namespace libgemm
