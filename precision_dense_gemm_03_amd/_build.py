@@ -21,7 +21,8 @@ SOURCES = ["abi.cpp", "selector.cpp", "amax_quant.hip", "amax_quant_channel.hip"
            "gemm_stream.hip", "gemv_kmajor.hip", "gemm_pp.hip", "gemm_pp_mixed.hip",
            "amax_quant_pair.hip", "gemm_ring.hip", "gemm_ring_mixed.hip", "noalloc.hip", "gemm_pp_exact.hip",
            "abi_routed.cpp", "routed.cpp", "routed_tile_f16.hip", "routed_tile_fp8.hip", "lora.hip", "gemm_wgrad.hip",
-           "moe_route.hip", "moe_rows.hip"]
+           "moe_route.hip", "moe_rows.hip", "routed_pp_f16.hip", "routed_pp_fp8.hip", "routed_pp_mixed.hip",
+           "routed_ring_f16.hip", "routed_ring_fp8.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -85,11 +85,12 @@ namespace pp {
 
 // BM_: tile rows, 256 or 192 (three 32-row blocks per wave instead of four:
 // 3000 x 4096 is 16 x 16 tiles of 192 x 256 on 256 CUs, against 12 x 16 tiles
-// of 256 x 256 that leave a quarter of them idle).
+// of 256 x 256 that leave a quarter of them idle); 128 and 64 for the last rows
+// of a row group.
 template <int ES, int BM_ = 256>
 struct Pp {
     static constexpr int BM = BM_, BN = 256;
-    static_assert(BM == 256 || BM == 192, "tile rows: 256 or 192");
+    static_assert(BM % 64 == 0 && BM <= 256, "tile rows: 64, 128, 192 or 256");
     static constexpr int NT = 512;                  // 8 waves
     static constexpr int S = 4;                     // B: LDS ring stages, one K tile each
     static constexpr int AP = 3;                    // A: LDS regions, two K tiles each
@@ -175,44 +176,61 @@ __device__ __forceinline__ void store_elem(void* C, int64_t idx, float y, int ef
 // FP16 MFMA (v_mfma_f32_32x32x16_f16), whose products and sums are exact in
 // FP32. A lane's 32 codes cover k = 32 h .. 32 h + 31; k-step s takes codes
 // 8 s .. 8 s + 7 of both operands, so every product pairs the same k.
-template <int ES, int OUT, int FA, int FB, bool BT, bool EX = false, int BM = 256>
-__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_pp_kernel(
-    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C, int M, int N, int K,
-    const float* __restrict__ sA, const float* __restrict__ sB, const float* __restrict__ sOut, int tiles_m,
-    int tiles_n, int eflags, int vec_out) {
+//
+// RAG (row groups, adapters): tiles that M or N cuts keep the vector stores,
+// masked by row and by 16-byte column piece. Ext: what is added to the
+// products before the store (NoExtra, or LoraExtra of lora_extra.h).
+struct NoExtra {
+    static constexpr bool kActive = false;
+};
+
+// The LDS rings of a workgroup (LIBGEMM_PP_LDS declares them: separate objects,
+// so that bodies of several tile heights in one kernel share them).
+struct PpLds {
+    LDS_AS uint8_t* a[3];
+    LDS_AS uint8_t* b[4];
+};
+
+#define LIBGEMM_PP_LDS(T)                                                                                          \
+    __shared__ __attribute__((aligned(1024))) uint8_t a0[T::A_PAIR], a1[T::A_PAIR], a2[T::A_PAIR];                 \
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[T::B_STAGE], b1[T::B_STAGE], b2[T::B_STAGE], b3[T::B_STAGE]; \
+    const pp::PpLds lds{{(LDS_AS uint8_t*)a0, (LDS_AS uint8_t*)a1, (LDS_AS uint8_t*)a2},                           \
+                        {(LDS_AS uint8_t*)b0, (LDS_AS uint8_t*)b1, (LDS_AS uint8_t*)b2, (LDS_AS uint8_t*)b3}}
+
+// One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N.
+template <int ES, int OUT, int FA, int FB, bool BT, bool EX, int BM, bool RAG = false, class Ext = NoExtra>
+__device__ __forceinline__ void pp_body(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
+                                        void* __restrict__ C, int M, int N, int K, const float* __restrict__ sA,
+                                        const float* __restrict__ sB, const float* __restrict__ sOut, int m0, int n0,
+                                        int eflags, int vec_out, const PpLds& lds, const Ext& ext = Ext{}) {
     using T = Pp<ES, BM>;
     using Op = typename Mfma<ES>::op;
-    __shared__ __attribute__((aligned(1024))) uint8_t a0[T::A_PAIR], a1[T::A_PAIR], a2[T::A_PAIR];
-    __shared__ __attribute__((aligned(1024))) uint8_t b0[T::B_STAGE], b1[T::B_STAGE], b2[T::B_STAGE], b3[T::B_STAGE];
     // Region and stage selection; the index is a compile-time constant wherever
     // it matters (the main loop is unrolled by the ring periods).
     auto region_a = [&](int r) __attribute__((always_inline)) -> LDS_AS uint8_t* {
         switch (r) {
-            case 0: return (LDS_AS uint8_t*)a0;
-            case 1: return (LDS_AS uint8_t*)a1;
-            default: return (LDS_AS uint8_t*)a2;
+            case 0: return lds.a[0];
+            case 1: return lds.a[1];
+            default: return lds.a[2];
         }
     };
     auto stage_b = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
         switch (st) {
-            case 0: return (LDS_AS uint8_t*)b0;
-            case 1: return (LDS_AS uint8_t*)b1;
-            case 2: return (LDS_AS uint8_t*)b2;
-            default: return (LDS_AS uint8_t*)b3;
+            case 0: return lds.b[0];
+            case 1: return lds.b[1];
+            case 2: return lds.b[2];
+            default: return lds.b[3];
         }
     };
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int G = wave >> 2, wj = wave & 3;
-    int tile_m, tile_n;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
-    const int m0 = tile_m * T::BM, n0 = tile_n * T::BN;
     const int nk = (K + T::BK - 1) / T::BK;
     const int nk_full = K / T::BK;
     // the epilogue's multiplier, loaded now (see epilogue_base_early)
-    const bool chan = (eflags & EPI_CHANNEL) != 0;
-    const float scale = epilogue_base_early(sA, sB, sOut, OUT == OUT_E4M3, chan);
+    const bool chan0 = (eflags & EPI_CHANNEL) != 0;
+    const float scale0 = epilogue_base_early(sA, sB, sOut, OUT == OUT_E4M3, chan0);
     const int npf = nk_full / 2;            // K tile pairs whose two tiles are full
     const int KE = K * ES;                  // bytes of one A (or Bt) row
 
@@ -590,8 +608,25 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // 64 wj + 32 j + 8 q + 4 h + e of the tile.
     const int row_t = T::MR * G + lr;          // + 32 i
     const int col_t = 64 * wj + 4 * h;         // + 32 j + 8 q
+    if constexpr (Ext::kActive) {
+        // scaled here, added to, stored as it is
+#pragma unroll
+        for (int i = 0; i < T::MI; ++i) {
+            const float sr = chan0 ? sA[min(m0 + row_t + 32 * i, M - 1)] : 1.0f;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    acc[i][j][r] *= scale0;
+                    if (chan0) acc[i][j][r] *= sr * sB[min(n0 + col_t + 32 * j + 8 * (r >> 2) + (r & 3), N - 1)];
+                }
+        }
+        ext.template add32<T::MI>(acc, m0 + T::MR * G, n0 + 64 * wj, M, N);
+    }
+    const bool chan = !Ext::kActive && chan0;
+    const float scale = Ext::kActive ? 1.0f : scale0;
     // Vector stores need a 16-byte aligned C with 16-byte row pitches (vec_out).
-    const bool interior = vec_out && (m0 + T::BM <= M) && (n0 + T::BN <= N);
+    const bool interior = vec_out && (RAG || ((m0 + T::BM <= M) && (n0 + T::BN <= N)));
     if (!interior) {
 #pragma unroll
         for (int i = 0; i < T::MI; ++i)
@@ -614,8 +649,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = acc[i][j][4 * q + e] * scale;
         if (chan) {
-            const float sr = sA[m0 + row_t + 32 * i];
-            const int col = n0 + col_t + 32 * j + 8 * q;
+            const float sr = sA[RAG ? min(m0 + row_t + 32 * i, M - 1) : m0 + row_t + 32 * i];
+            const int col = RAG ? min(n0 + col_t + 32 * j + 8 * q, N - 4) : n0 + col_t + 32 * j + 8 * q;
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] *= sr * sB[col + e];
         }
@@ -637,9 +672,12 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        *reinterpret_cast<v4f*>(Cf + (int64_t)(m0 + row_t + 32 * i) * N + n0 + col_t + 32 * j +
-                                                8 * q) = val4(i, j, q);
+                    for (int q = 0; q < 4; ++q) {
+                        const v4f y = val4(i, j, q);
+                        if (!RAG || (m0 + row_t + 32 * i < M && n0 + col_t + 32 * j + 8 * q < N))
+                            *reinterpret_cast<v4f*>(Cf + (int64_t)(m0 + row_t + 32 * i) * N + n0 + col_t + 32 * j +
+                                                    8 * q) = y;
+                    }
         };
         if (chan) store_all(run4);
         else store_all(plain4);
@@ -742,8 +780,22 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     for (int p = 0; p < 32 * T::MI / RPI; ++p) {
         const int r = RPI * p + lane / LPR, seg = lane % LPR;
         const v4i v = *(const LDS_AS v4i*)(ep + r * RB + 16 * (seg ^ esw(r)));
+        if (RAG && (m0 + T::MR * G + r >= M || n0 + 64 * wj + seg * (16 / es_out) >= N)) continue;
         *reinterpret_cast<v4i*>(Cb + ((int64_t)(m0 + T::MR * G + r) * N + n0 + 64 * wj) * es_out + 16 * seg) = v;
     }
+}
+
+template <int ES, int OUT, int FA, int FB, bool BT, bool EX = false, int BM = 256>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemm_pp_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C, int M, int N, int K,
+    const float* __restrict__ sA, const float* __restrict__ sB, const float* __restrict__ sOut, int tiles_m,
+    int tiles_n, int eflags, int vec_out) {
+    using T = Pp<ES, BM>;
+    LIBGEMM_PP_LDS(T);
+    int tile_m, tile_n;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
+    pp_body<ES, OUT, FA, FB, BT, EX, BM>(A, B, C, M, N, K, sA, sB, sOut, tile_m * T::BM, tile_n * T::BN, eflags,
+                                         vec_out, lds);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }

@@ -58,7 +58,8 @@
 namespace libgemm {
 namespace ring {
 
-template <int ES, int BM, int BN, bool BT>
+// S_: LDS ring stages, 0 for the most that fit (below).
+template <int ES, int BM, int BN, bool BT, int S_ = 0>
 struct Ring {
     static constexpr int NT = 256;
     static constexpr int ROWB = 128;                          // bytes of every A row per K tile
@@ -72,7 +73,7 @@ struct Ring {
     // LDS ring stages: 8, or as many as fit in 144 KiB (deeper rings measured
     // no faster: the stream is then bound by the memory system, not the
     // number of loads in flight)
-    static constexpr int S = (144 * 1024 / STAGE) < 8 ? (144 * 1024 / STAGE) : 8;
+    static constexpr int S = S_ ? S_ : ((144 * 1024 / STAGE) < 8 ? (144 * 1024 / STAGE) : 8);
     static constexpr int A_INST = A_BYTES / 1024;             // 1 KiB direct loads per stage
     static constexpr int INST = A_INST + B_BYTES / 1024;
     static constexpr int MAX_PER_WAVE = (INST + 3) / 4;       // loads of one wave per stage
@@ -83,6 +84,7 @@ struct Ring {
     static constexpr int WCOLS = WPK / WROWS;                 // ... and along N
     static constexpr int TN = BN / 16 / WCOLS;                // 16-column blocks per wave
     static constexpr int KSUB = ES == 1 ? 1 : 2;              // MFMA k-steps per K tile
+    static constexpr int RED_SLOTS = (KW > 1 ? (KW - 1) * WPK : 1) * 64 * TN;   // (one, unused, when KW == 1)
     static_assert(BM == 16 || BM == 32 || BM == 64, "BM is 16, 32 or 64");
     static_assert(BN == 16 || BN == 32 || BN == 64, "BN is 16, 32 or 64");
     static_assert(WROWS <= WPK && WCOLS * WROWS == WPK && TN * WCOLS * 16 == BN, "wave layout");
@@ -290,28 +292,30 @@ __device__ __forceinline__ void store_elem(void* C, int64_t idx, float y, int ef
     }
 }
 
-template <int ES, int BM, int BN, int OUT, int FA, int FB, bool BT>
-__global__ __launch_bounds__(256) void gemm_ring_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
-                                                        void* __restrict__ C, int M, int N, int K,
-                                                        const float* __restrict__ sA, const float* __restrict__ sB,
-                                                        const float* __restrict__ sOut, int tiles_m, int tiles_n,
-                                                        int eflags, int vec_out) {
-    using T = Ring<ES, BM, BN, BT>;
+// RAG (row groups, adapters): tiles that M or N cuts keep the vector stores,
+// masked. Ext: what is added to the products before the store (NoExtra, or
+// LoraExtra of lora_extra.h).
+struct NoExtra {
+    static constexpr bool kActive = false;
+};
+
+// One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N.
+// The ring: stage st at ring + st * STAGE. Every read of it is an asm group
+// (device_common.h), so the compiler does not need to tell stages apart. red:
+// partial sums of wave groups 1 .. KW-1 (RED_SLOTS of them).
+template <int ES, int BM, int BN, int OUT, int FA, int FB, bool BT, int S_ = 0, bool RAG = false, class Ext = NoExtra>
+__device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
+                                          void* __restrict__ C, int M, int N, int K, const float* __restrict__ sA,
+                                          const float* __restrict__ sB, const float* __restrict__ sOut, int m0, int n0,
+                                          int eflags, int vec_out, uint8_t* ring, v4f* red, const Ext& ext = Ext{}) {
+    using T = Ring<ES, BM, BN, BT, S_>;
     using Op = typename Op16<ES>::type;
-    // The ring: stage st at ring + st * STAGE. Every read of it is an asm group
-    // (device_common.h), so the compiler does not need to tell stages apart.
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
-    // partial sums of wave groups 1 .. KW-1 (one slot when KW == 1, unused)
-    __shared__ v4f red[(T::KW > 1 ? (T::KW - 1) * T::WPK : 1) * 64 * T::TN];
     auto stage = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
         return (LDS_AS uint8_t*)ring + st * T::STAGE;
     };
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    int tile_m, tile_n;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
-    const int m0 = tile_m * BM, n0 = tile_n * BN;
     const int nk = (K + T::BK - 1) / T::BK, nk_full = K / T::BK;
     // the epilogue's multiplier, loaded now (see epilogue_base_early)
     const bool chan = (eflags & EPI_CHANNEL) != 0;
@@ -613,15 +617,27 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(const uint8_t* __restric
 
     // ---- epilogue: lane holds row 16 wr + j16 and columns 16 (TN wc + tn) + 4 g + 0..3 ----
     const int row = m0 + 16 * wr + j16;
-    const bool interior = vec_out && (m0 + BM <= M) && (n0 + BN <= N);
+    const bool interior = vec_out && (RAG || ((m0 + BM <= M) && (n0 + BN <= N)));
+    if constexpr (RAG) {
+        if (row >= M) return;
+    }
 #pragma unroll
     for (int tn = 0; tn < T::TN; ++tn) {
         const int col = n0 + 16 * (T::TN * wc + tn) + 4 * g;
+        if (RAG && col >= N) continue;   // (vec_out: N is a multiple of 4)
         v4f y;
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = acc[tn][e] * scale;
-        if (interior) {
+        if constexpr (Ext::kActive) {
             if (chan) {
+                const float sr = sA[row];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= sr * sB[min(col + e, N - 1)];
+            }
+            ext.add_row4(y, row, col, M, N);
+        }
+        if (interior) {
+            if (chan && !Ext::kActive) {
                 const float sr = sA[row];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] *= sr * sB[col + e];
@@ -642,11 +658,26 @@ __global__ __launch_bounds__(256) void gemm_ring_kernel(const uint8_t* __restric
             for (int e = 0; e < 4; ++e)
                 if (col + e < N) {
                     float v = y[e];
-                    if (chan) v *= sA[row] * sB[col + e];
+                    if (chan && !Ext::kActive) v *= sA[row] * sB[col + e];
                     store_elem<OUT>(C, (int64_t)row * N + col + e, v, eflags);
                 }
         }
     }
+}
+
+template <int ES, int BM, int BN, int OUT, int FA, int FB, bool BT>
+__global__ __launch_bounds__(256) void gemm_ring_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
+                                                        void* __restrict__ C, int M, int N, int K,
+                                                        const float* __restrict__ sA, const float* __restrict__ sB,
+                                                        const float* __restrict__ sOut, int tiles_m, int tiles_n,
+                                                        int eflags, int vec_out) {
+    using T = Ring<ES, BM, BN, BT>;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
+    __shared__ v4f red[T::RED_SLOTS];
+    int tile_m, tile_n;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, tile_m, tile_n);
+    ring_body<ES, BM, BN, OUT, FA, FB, BT>(A, B, C, M, N, K, sA, sB, sOut, tile_m * BM, tile_n * BN, eflags, vec_out,
+                                           ring, red);
 }
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }

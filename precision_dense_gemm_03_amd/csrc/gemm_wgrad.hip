@@ -4,16 +4,271 @@
 //
 // The sum runs over the group's rows, the slow direction of both operands, so
 // both reach the matrix cores through LDS transpose reads (ds_read_b64_tr_b16),
-// as row-major B does in the plain products. One workgroup computes a 128 x
-// 128 tile of one group, 4 waves of 64 x 64, 64 rows at a time, registers
-// ahead of two LDS stages (the layout and padding of gemm_tile_impl.h's
-// row-major B). Rows past the group's end are staged as zeros on both sides
-// (another group's rows may hold NaN); a group without rows gives zeros.
-// Operands of any alignment are read in 16-byte pieces.
+// as row-major B does in the plain products. Rows past the group's end are
+// staged as zeros on both sides (another group's rows may hold NaN); a group
+// without rows gives zeros. Two kernels:
+//
+// wgrad_pp_kernel (16-byte aligned operands): the ping-pong kernel's plan
+// (gemm_pp_impl.h) with A staged like its row-major B. 256 x 256 tiles, 8
+// waves in two groups that take turns at the matrix cores and the LDS, 32 rows
+// per step (16 KiB of each operand), four LDS stages per operand, direct
+// buffer->LDS loads three steps ahead (group 0 loads A, group 1 B).
+//
+// wgrad_tile_kernel (operands of any alignment): 128 x 128 tiles, 4 waves of
+// 64 x 64, 64 rows at a time, registers ahead of two LDS stages (the layout
+// and padding of gemm_tile_impl.h's row-major B).
+//
+// Order of the tiles: the column tiles of all groups, counted through, go
+// round the XCDs, each with all its row tiles, so every XCD gets an equal part
+// of every group and tiles that run together share B's columns.
+#include "gemm_pp_impl.h"
 #include "gemm_tile_impl.h"
 
 namespace libgemm {
 namespace {
+
+struct WgradTile {
+    int group, tm, tn, lo, hi;
+};
+
+// The tile of workgroup bid; group -1: none.
+__device__ __forceinline__ WgradTile wgrad_tile(int bid, const int32_t* __restrict__ offsets, int groups, int rows,
+                                                int tiles_m, int tiles_n) {
+    const int at = bid >> 3, c = (bid & 7) + 8 * (at / tiles_m);
+    WgradTile t{c / tiles_n, at % tiles_m, c % tiles_n, 0, 0};
+    if (t.group >= groups) {
+        t.group = -1;
+        return t;
+    }
+    t.lo = min(max(offsets[t.group], 0), rows);
+    t.hi = max(t.lo, min(max(offsets[t.group + 1], 0), rows));
+    return t;
+}
+
+int64_t wgrad_blocks(int64_t groups, int64_t tiles_m, int64_t tiles_n) {
+    return (groups * tiles_n + 7) / 8 * 8 * tiles_m;
+}
+
+template <int OUT>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void wgrad_pp_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C,
+    const int32_t* __restrict__ offsets, int groups, int rows, int M, int N, int tiles_m, int tiles_n, int vec_out) {
+    constexpr int BK = 32, STAGE = BK * 512, L = 4;   // rows per step, bytes of a stage, loads per wave and step
+    __shared__ __attribute__((aligned(1024))) uint8_t a0[STAGE], a1[STAGE], a2[STAGE], a3[STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t b0[STAGE], b1[STAGE], b2[STAGE], b3[STAGE];
+    auto stage_a = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
+        switch (st) {
+            case 0: return (LDS_AS uint8_t*)a0;
+            case 1: return (LDS_AS uint8_t*)a1;
+            case 2: return (LDS_AS uint8_t*)a2;
+            default: return (LDS_AS uint8_t*)a3;
+        }
+    };
+    auto stage_b = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
+        switch (st) {
+            case 0: return (LDS_AS uint8_t*)b0;
+            case 1: return (LDS_AS uint8_t*)b1;
+            case 2: return (LDS_AS uint8_t*)b2;
+            default: return (LDS_AS uint8_t*)b3;
+        }
+    };
+    const WgradTile w = wgrad_tile(blockIdx.x, offsets, groups, rows, tiles_m, tiles_n);
+    if (w.group < 0) return;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int G = wave >> 2, wj = wave & 3;
+    const int m0 = w.tm * 256, n0 = w.tn * 256;
+    const int K = w.hi - w.lo, nk = (K + BK - 1) / BK, nk_full = K / BK;
+
+    // ---- staging: load i of wave j fills rows 2 (4 j + i) and + 1 of a stage
+    // (512 bytes each, lane / 32 the row, slot lane % 32 holding chunk
+    // slot ^ swz_b(row)); columns past the operand's end read its last chunk ----
+    const int W = G == 0 ? M : N, c0 = G == 0 ? m0 : n0;
+    const uint8_t* src = (G == 0 ? A : B) + (int64_t)w.lo * W * 2;
+    uint32_t off[L];
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        const int r = 2 * (4 * wj + i) + (lane >> 5);
+        const int c = (lane & 31) ^ pp::swz_b<2>(r);
+        off[i] = (uint32_t)(r * W + min(c0 + 8 * c, W - 8)) * 2u;
+    }
+    const uint32_t step_bytes = (uint32_t)BK * (uint32_t)W * 2u;
+    const int64_t end = (int64_t)K * W * 2;
+    auto rsrc_at = [&](int t) __attribute__((always_inline)) {
+        const int64_t at = (int64_t)t * step_bytes;
+        return buffer_rsrc(src + at, end - at);
+    };
+    auto stage_of = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
+        return (G == 0 ? stage_a(st) : stage_b(st)) + wj * 4096;
+    };
+    auto issue_via = [&](__amdgpu_buffer_rsrc_t rs, int kb, int st) __attribute__((always_inline)) {
+        const uint32_t kofs = (uint32_t)kb * step_bytes;
+        if (G == 0) {
+            LDS_AS uint8_t* dst = stage_a(st) + wj * 4096;
+#pragma unroll
+            for (int i = 0; i < L; ++i) buffer_load_lds16(rs, (LDS_AS void*)(dst + i * 1024), off[i], kofs);
+        } else {
+            LDS_AS uint8_t* dst = stage_b(st) + wj * 4096;
+#pragma unroll
+            for (int i = 0; i < L; ++i) buffer_load_lds16(rs, (LDS_AS void*)(dst + i * 1024), off[i], kofs);
+        }
+    };
+    auto issue_partial = [&](int t) __attribute__((always_inline)) {
+        const uint8_t* p = src + (int64_t)t * step_bytes;
+        LDS_AS uint8_t* dst = stage_of(t & 3);
+#pragma unroll 1
+        for (int i = 0; i < L; ++i) {
+            const int r = 2 * (4 * wj + i) + (lane >> 5);
+            v4u v = v4u{0u, 0u, 0u, 0u};
+            if (t * BK + r < K) v = *reinterpret_cast<const v4u*>(p + off[i]);
+            *(LDS_AS v4u*)(dst + i * 1024 + lane * 16) = v;
+        }
+    };
+    auto issue = [&](int t) __attribute__((always_inline)) {
+        if (t < nk_full) issue_via(rsrc_at(t), 0, t & 3);
+        else if (t < nk) issue_partial(t);
+    };
+
+    // ---- operands: transpose reads of rows 16 u + 8 h + 4 q + lane16 / 4,
+    // four columns each (gemm_pp_impl.h, row-major B in FP16) ----
+    const int lr = lane & 31, h = lane >> 5, j16 = lane & 15, half = (lane >> 4) & 1;
+    auto addr = [&](const LDS_AS uint8_t* st, int chunk0, int u, int q) __attribute__((always_inline)) -> uint32_t {
+        const int k = 16 * u + 8 * h + 4 * q + (j16 >> 2);
+        const int chunk = (chunk0 + 2 * half + ((j16 & 3) >> 1)) ^ pp::swz_b<2>(j16 >> 2);
+        return lds_addr(st + k * 512 + chunk * 16 + 8 * (j16 & 1));
+    };
+    auto pair = [](v4s x, v4s y) __attribute__((always_inline)) -> v8h {
+        return __builtin_bit_cast(v8h, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    };
+    v8h opa[2][4], opb[2][2];
+    auto read = [&](const LDS_AS uint8_t* sa, const LDS_AS uint8_t* sb) __attribute__((always_inline)) {
+        v4s t[8];
+        uint32_t ad[8];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) ad[2 * i + q] = addr(sa, 16 * G + 4 * i, u, q);
+            lds_tr16_x8(t, ad);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) opa[u][i] = pair(t[2 * i], t[2 * i + 1]);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) ad[4 * u + 2 * j + q] = addr(sb, 8 * wj + 4 * j, u, q);
+        lds_tr16_x8(t, ad);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) opb[u][j] = pair(t[4 * u + 2 * j], t[4 * u + 2 * j + 1]);
+    };
+
+    v16f acc[4][2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+    // One step: MEM (this group's operand reads, loads three steps ahead, wait
+    // for step t + 1's), barrier, MMA, barrier; the other group is one phase off.
+    // A step past the last full one was staged with ordinary LDS stores, whose
+    // wait (and the wait for everything older) is the full one.
+    __amdgpu_buffer_rsrc_t rs_blk;
+    auto step = [&](int t, int tmod, bool steady) __attribute__((always_inline)) {
+        const int st = steady ? tmod : t & 3;
+        read(stage_a(st), stage_b(st));
+        if (steady) {
+            issue_via(rs_blk, tmod + 3, (tmod + 3) & 3);
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
+        } else {
+            issue(t + 3);
+            // loads of steps t + 2 and t + 3 may stay in flight while they are direct ones
+            const int younger = t + 3 < nk_full ? 2 : (t + 2 < nk_full && t + 3 >= nk ? 1 : 0);
+            if (younger == 2) __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
+            else if (younger == 1) __builtin_amdgcn_s_waitcnt(waitcnt_imm(L, 0));
+            else __builtin_amdgcn_s_waitcnt(0);
+        }
+        asm volatile("s_barrier" ::: "memory");
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) asm volatile("" : "+v"(opa[u][i]));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(opb[u][j]));
+        }
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(opb[u][j], opa[u][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) asm volatile("" : "+v"(acc[i][j]));
+        __builtin_amdgcn_s_setprio(0);
+        asm volatile("s_barrier" ::: "memory");
+    };
+
+    if (nk > 0) {
+#pragma unroll
+        for (int t = 0; t < 3; ++t) issue(t);
+        // step 0 landed: steps 1 and 2 may stay in flight if all three are direct loads
+        if (nk_full >= 3) __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
+        else __builtin_amdgcn_s_waitcnt(0);
+        asm volatile("s_barrier" ::: "memory");
+        if (G == 1) asm volatile("s_barrier" ::: "memory");
+        int t = 0;
+        for (; t + 7 <= nk_full; t += 4) {   // loads steps t + 3 .. t + 6
+            rs_blk = rsrc_at(t);
+            step(t, 0, true);
+            step(t + 1, 1, true);
+            step(t + 2, 2, true);
+            step(t + 3, 3, true);
+        }
+#pragma unroll 1
+        for (; t < nk; ++t) step(t, 0, false);
+        if (G == 0) asm volatile("s_barrier" ::: "memory");
+    }
+
+    // ---- store: block (i, j), value 4 q + e: row 128 G + 32 i + lr, column
+    // 64 wj + 32 j + 8 q + 4 h + e ----
+    const int64_t base = (int64_t)w.group * M * N;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = m0 + 128 * G + 32 * i + lr;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int col = n0 + 64 * wj + 32 * j + 8 * q + 4 * h;
+                if (row >= M || col >= N) continue;
+                const int64_t at = base + (int64_t)row * N + col;
+                if (vec_out) {   // N is a multiple of 8: four columns are in or out together
+                    if constexpr (OUT == OUT_F32) {
+                        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(C) + at) =
+                            v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    } else {
+                        typedef _Float16 v4hh __attribute__((ext_vector_type(4)));
+                        *reinterpret_cast<v4hh*>(reinterpret_cast<_Float16*>(C) + at) =
+                            v4hh{(_Float16)acc[i][j][4 * q], (_Float16)acc[i][j][4 * q + 1],
+                                 (_Float16)acc[i][j][4 * q + 2], (_Float16)acc[i][j][4 * q + 3]};
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) tile::store_one<OUT>(C, at + e, acc[i][j][4 * q + e], 0);
+                }
+            }
+    }
+}
 
 using WT = tile::Tile<2, 128, 128, 64, 2, 2, false>;
 
@@ -26,10 +281,9 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
     __shared__ __attribute__((aligned(16))) uint8_t smem_raw[4 * OP];
     LDS_AS uint8_t* smem = (LDS_AS uint8_t*)smem_raw;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-    int tm, tn;
-    tile_coords(blockIdx.x, groups * tiles_m, tiles_n, tm, tn);
-    const int grp = tm / tiles_m, m0 = (tm % tiles_m) * 128, n0 = tn * 128;
-    const int lo = min(max(offsets[grp], 0), rows), hi = max(lo, min(max(offsets[grp + 1], 0), rows));
+    const WgradTile w = wgrad_tile(blockIdx.x, offsets, groups, rows, tiles_m, tiles_n);
+    if (w.group < 0) return;
+    const int grp = w.group, m0 = w.tm * 128, n0 = w.tn * 128, lo = w.lo, hi = w.hi;
     const int nk = (hi - lo + BK - 1) / BK;
 
     const int srow = tid >> 4, scol = tid & 15;   // staged chunk: rows srow + 16 i, 16-byte column scol
@@ -107,17 +361,35 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
 }  // namespace
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
-    const int64_t tiles_m = (a.M + 127) / 128, tiles_n = (a.N + 127) / 128, blocks = a.groups * tiles_m * tiles_n;
-    if (blocks <= 0) return hipSuccess;
+    if (a.M <= 0 || a.N <= 0 || a.groups <= 0) return hipSuccess;
+    // 16-byte pieces of both operands' rows, and 32-bit offsets over 8 steps
+    const bool pp_ok = pp::aligned16(a.A) && pp::aligned16(a.B) && a.M % 8 == 0 && a.N % 8 == 0 &&
+                       a.M < (1 << 21) && a.N < (1 << 21);
+    const int size = pp_ok ? 256 : 128;
+    const int64_t tiles_m = (a.M + size - 1) / size, tiles_n = (a.N + size - 1) / size;
+    const int64_t blocks = wgrad_blocks(a.groups, tiles_m, tiles_n);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    const int rows = (int)a.K, M = (int)a.M, N = (int)a.N, groups = (int)a.groups;
+    if (pp_ok) {
+        const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
+        const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
+        const int vec_out = pp::aligned16(a.C);
+        if (a.out_dtype == OUT_F32)
+            wgrad_pp_kernel<OUT_F32><<<(unsigned)blocks, 512, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
+                                                                             (int)tiles_m, (int)tiles_n, vec_out);
+        else
+            wgrad_pp_kernel<OUT_F16><<<(unsigned)blocks, 512, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
+                                                                             (int)tiles_m, (int)tiles_n, vec_out);
+        return hipGetLastError();
+    }
     const _Float16* A = reinterpret_cast<const _Float16*>(a.A);
     const _Float16* B = reinterpret_cast<const _Float16*>(a.B);
     if (a.out_dtype == OUT_F32)
-        wgrad_tile_kernel<OUT_F32><<<(unsigned)blocks, 256, 0, a.stream>>>(
-            A, B, a.C, a.offsets, (int)a.groups, (int)a.K, (int)a.M, (int)a.N, (int)tiles_m, (int)tiles_n);
+        wgrad_tile_kernel<OUT_F32><<<(unsigned)blocks, 256, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
+                                                                           (int)tiles_m, (int)tiles_n);
     else
-        wgrad_tile_kernel<OUT_F16><<<(unsigned)blocks, 256, 0, a.stream>>>(
-            A, B, a.C, a.offsets, (int)a.groups, (int)a.K, (int)a.M, (int)a.N, (int)tiles_m, (int)tiles_n);
+        wgrad_tile_kernel<OUT_F16><<<(unsigned)blocks, 256, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
+                                                                           (int)tiles_m, (int)tiles_n);
     return hipGetLastError();
 }
 

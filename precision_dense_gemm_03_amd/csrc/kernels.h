@@ -108,7 +108,7 @@ const GemmConfig* select_config_exact(int out_dtype, int64_t M, int64_t N, int64
 SplitPlan plan_splitk(int kind, int out_dtype, int64_t M, int64_t N, int64_t K, int fmt_a = 0, int fmt_b = 0,
                       int b_kmajor = 0);
 
-// Products grouped by rows (grouped.cpp chooses the kernel), kind: OperandKind.
+// Products grouped by rows (routed.cpp chooses the kernel), kind: OperandKind.
 hipError_t launch_grouped(int kind, const GroupedArgs& a);
 // The register-staged tile kernel over row groups: any sizes and alignment.
 hipError_t launch_grouped_tile_f16(const GroupedArgs& a, int bm);
@@ -122,6 +122,29 @@ hipError_t launch_lora_low(const LoraArgs& a);
 hipError_t launch_lora(int kind, const LoraArgs& a);
 hipError_t launch_lora_tile_f16(const LoraArgs& a, int bm);
 hipError_t launch_lora_tile_fp8(const LoraArgs& a, int bm);
+// The deep-ring kernel over row groups of few rows / with adapters, for
+// operands it takes.
+bool grouped_ring_takes_f16(const GroupedArgs& a);
+bool grouped_ring_takes_fp8(const GroupedArgs& a);
+hipError_t launch_grouped_ring_f16(const GroupedArgs& a);
+hipError_t launch_grouped_ring_fp8(const GroupedArgs& a);
+bool lora_ring_takes_f16(const LoraArgs& a);
+bool lora_ring_takes_fp8(const LoraArgs& a);
+hipError_t launch_lora_ring_f16(const LoraArgs& a);
+hipError_t launch_lora_ring_fp8(const LoraArgs& a);
+// The ping-pong tile kernel over row groups / with adapters: whether it takes
+// the operands (16-byte alignment, 32-bit offsets), and its launches (bm 128 or
+// 256 rows, adapters 192 or 256; pairs with E5M2: 192).
+bool grouped_pp_takes_f16(const GroupedArgs& a);
+bool grouped_pp_takes_fp8(const GroupedArgs& a);
+bool lora_pp_takes_f16(const LoraArgs& a);
+bool lora_pp_takes_fp8(const LoraArgs& a);
+hipError_t launch_grouped_pp_f16(const GroupedArgs& a, int bm);
+hipError_t launch_grouped_pp_e4m3(const GroupedArgs& a, int bm);
+hipError_t launch_grouped_pp_mixed(const GroupedArgs& a);
+hipError_t launch_lora_pp_f16(const LoraArgs& a, int bm);
+hipError_t launch_lora_pp_e4m3(const LoraArgs& a, int bm);
+hipError_t launch_lora_pp_mixed(const LoraArgs& a);
 
 // C = epilogue(sum over a.splits slices of a.ws), in slice order.
 hipError_t launch_splitk_reduce(const GemmArgs& a);

@@ -122,6 +122,69 @@ struct LoraExtra {
             }
         }
     }
+
+    // 32x32 blocks with one row per lane (LB's operand first): acc[i][j] holds
+    // row row0 + 32 i + lane % 32, columns col0 + 32 j + 8 q + 4 (lane / 32) + e
+    // in value 4 q + e.
+    template <int MI>
+    __device__ __forceinline__ void add32(v16f (&acc)[MI][2], int row0, int col0, int M, int N) const {
+        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int row = row0 + 32 * i + lr;
+            const int mine = adapter_of(row, M);
+            const uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0);
+            if (!todo) continue;
+            const float* lrow = low + (int64_t)min(row, M - 1) * rank_p;
+            for (int p0 = 0; p0 < rank_p; p0 += 64) {
+                v8h hi[4], lo[4];
+                const int e = split_piece<4, 2>(lrow, p0, h, hi, lo);
+                for (uint32_t left = todo; left;) {
+                    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+                    left &= ~(uint32_t)__builtin_amdgcn_ballot_w64(mine == a);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int col = min(col0 + 32 * j + lr, N - 1);
+                        v16f sum;
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) sum[r] = 0.0f;
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) {
+                            if (p0 + 16 * s >= rank_p) break;
+                            const v8h b = lb_chunk(a, col, p0 + 8 * (2 * s + h), N);
+                            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, hi[s], sum, 0, 0, 0);
+                            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, lo[s], sum, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            if (mine == a) acc[i][j][r] += __builtin_ldexpf(sum[r], e);
+                    }
+                }
+            }
+        }
+    }
+
+    // Four neighbouring columns of one row, on the vector units: for few rows,
+    // where each usually has its own adapter and a block has nothing to share.
+    __device__ __forceinline__ void add_row4(v4f& y, int row, int col, int M, int N) const {
+        const int a = adapter_of(row, M);
+        if (a < 0) return;
+        const float* lrow = low + (int64_t)row * rank_p;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
+        for (int r0 = 0; r0 < rank_p; r0 += 8) {
+            const v4f l0 = *reinterpret_cast<const v4f*>(lrow + r0), l1 = *reinterpret_cast<const v4f*>(lrow + r0 + 4);
+            v8h b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = lb_chunk(a, min(col + e, N - 1), r0, N);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum[e] = __builtin_fmaf(i < 4 ? l0[i & 3] : l1[i & 3], (float)b[e][i], sum[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] += sum[e];
+    }
 };
 
 }  // namespace libgemm

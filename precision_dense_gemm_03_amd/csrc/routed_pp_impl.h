@@ -1,0 +1,132 @@
+// The ping-pong tile kernel (gemm_pp_impl.h) over row groups, and with the
+// low-rank term of per-row adapters.
+//
+// Grouped: tiles of BM x 256, and with TAILS a group's last rows at the
+// smallest of 64, 128, 192 and 256 rows that holds them (the four bodies share
+// the LDS rings). One workgroup per tile the host cannot rule out
+// (row_groups.h: up to one row of tiles per group more than there are; such a
+// workgroup ends after its look at the offsets). A fixed number of workgroups
+// walking the tiles measured slower: the walk's state cost the main loop its
+// registers (47 spilled per lane with 256 rows).
+#pragma once
+
+#include "gemm_pp_impl.h"
+#include "lora_extra.h"
+#include "row_groups.h"
+
+namespace libgemm {
+namespace routed {
+
+template <int ES, int OUT, int FA, int FB, bool BT, int BM, bool TAILS>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_pp_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C,
+    const int32_t* __restrict__ offsets, int groups, int rows, int N, int K, const float* __restrict__ sA,
+    const float* __restrict__ sB, const float* __restrict__ sOut, int tiles_n, int eflags, int vec_out) {
+    using T = pp::Pp<ES, BM>;
+    LIBGEMM_PP_LDS(T);
+    const RowTile t = find_row_tile<BM>(offsets, groups, rows, blockIdx.x, tiles_n);
+    if (t.m0 >= t.end) return;
+    const int n0 = t.tn * T::BN;
+    if (t.group < 0) {
+        zero_rows<BM, T::BN, OUT == OUT_F32 ? 4 : (OUT == OUT_F16 ? 2 : 1)>(C, t.m0, t.end, n0, N);
+        return;
+    }
+    const bool chan = (eflags & EPI_CHANNEL) != 0;
+    const float* sb = sB ? sB + (chan ? (int64_t)t.group * N : t.group) : nullptr;
+    const uint8_t* b = B + (int64_t)t.group * N * K * ES;
+    const int left = t.end - t.m0;
+    if constexpr (TAILS && BM > 64) {
+        if (left <= 64) {
+            pp::pp_body<ES, OUT, FA, FB, BT, false, 64, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
+                                                              vec_out, lds);
+            return;
+        }
+    }
+    if constexpr (TAILS && BM > 128) {
+        if (left <= 128) {
+            pp::pp_body<ES, OUT, FA, FB, BT, false, 128, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
+                                                               vec_out, lds);
+            return;
+        }
+    }
+    if constexpr (TAILS && BM > 192) {
+        if (left <= 192) {
+            pp::pp_body<ES, OUT, FA, FB, BT, false, 192, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
+                                                               vec_out, lds);
+            return;
+        }
+    }
+    pp::pp_body<ES, OUT, FA, FB, BT, false, BM, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags, vec_out,
+                                                      lds);
+}
+
+// What the ping-pong kernel needs (pp_fits), and a grid that can be launched.
+template <int ES>
+bool grouped_pp_fits(const GroupedArgs& a) {
+    const bool fits = a.b_kmajor ? pp::pp_fits<ES, true, 256>(a) : pp::pp_fits<ES, false, 256>(a);
+    return fits && most_workgroups(a.M, a.groups, 128, (a.N + 255) / 256) <= 0x7FFFFFFF;
+}
+
+template <int ES, int FA, int FB, bool BT, int BM, bool TAILS = true>
+hipError_t launch_grouped_pp(const GroupedArgs& a) {
+    using T = pp::Pp<ES, BM>;
+    const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
+    const unsigned grid = (unsigned)most_workgroups(a.M, a.groups, BM, tiles_n);
+    const int eflags = (a.out_dtype == OUT_E5M2 ? EPI_E5M2 : 0) | (a.channel ? EPI_CHANNEL : 0);
+    const int64_t out_es = a.out_dtype == OUT_F32 ? 4 : (a.out_dtype == OUT_F16 ? 2 : 1);
+    const int vec_out = pp::aligned16(a.C) && (a.N * out_es) % 16 == 0;
+    const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
+    const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
+#define LIBGEMM_GO(OUT)                                                                                       \
+    grouped_pp_kernel<ES, OUT, FA, FB, BT, BM, TAILS><<<grid, T::NT, 0, a.stream>>>(                          \
+        A, B, a.C, a.offsets, (int)a.groups, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, a.sOut, (int)tiles_n,  \
+        eflags, vec_out)
+    if (a.out_dtype == OUT_F32) {
+        LIBGEMM_GO(OUT_F32);
+    } else if (a.out_dtype == OUT_F16) {
+        LIBGEMM_GO(OUT_F16);
+    } else if constexpr (ES == 1) {
+        LIBGEMM_GO(OUT_E4M3);
+    } else {
+        return hipErrorInvalidValue;
+    }
+#undef LIBGEMM_GO
+    return hipGetLastError();
+}
+
+template <int ES, int OUT, int FA, int FB, int BM>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void lora_pp_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C, int M, int N, int K,
+    const float* __restrict__ sA, const float* __restrict__ sB, int tiles_m, int tiles_n, int eflags, int vec_out,
+    LoraExtra ext) {
+    using T = pp::Pp<ES, BM>;
+    LIBGEMM_PP_LDS(T);
+    int tm, tn;
+    tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    pp::pp_body<ES, OUT, FA, FB, true, false, BM, true, LoraExtra>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM, tn * 256,
+                                                                  eflags, vec_out, lds, ext);
+}
+
+template <int ES, int FA, int FB, int BM>
+hipError_t launch_lora_pp(const LoraArgs& a) {
+    const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + 255) / 256;
+    const unsigned grid = (unsigned)(tiles_m * tiles_n);
+    const int eflags = a.channel ? EPI_CHANNEL : 0;
+    const int vec_out = pp::aligned16(a.C) && (a.N * (a.out_dtype == OUT_F32 ? 4 : 2)) % 16 == 0;
+    const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
+    const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
+    const LoraExtra ext{a.low, a.adapter, reinterpret_cast<const _Float16*>(a.LB), (int)a.rank,
+                        (int)((a.rank + 7) / 8 * 8), (int)a.adapters};
+    if (a.out_dtype == OUT_F32)
+        lora_pp_kernel<ES, OUT_F32, FA, FB, BM><<<grid, 512, 0, a.stream>>>(
+            A, B, a.C, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, (int)tiles_m, (int)tiles_n, eflags, vec_out, ext);
+    else if (a.out_dtype == OUT_F16)
+        lora_pp_kernel<ES, OUT_F16, FA, FB, BM><<<grid, 512, 0, a.stream>>>(
+            A, B, a.C, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, (int)tiles_m, (int)tiles_n, eflags, vec_out, ext);
+    else
+        return hipErrorInvalidValue;
+    return hipGetLastError();
+}
+
+}  // namespace routed
+}  // namespace libgemm

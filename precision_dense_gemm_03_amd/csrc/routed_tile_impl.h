@@ -2,7 +2,7 @@
 // row: over row groups, and with the low-rank term of per-row adapters. Its
 // tile body (gemm_tile_impl.h) takes operands of any alignment here, so these
 // kernels serve every size; the faster kernels take what their alignment and
-// shape rules allow (grouped.cpp, lora.cpp).
+// shape rules allow (routed.cpp).
 //
 // Grouped: a fixed number of workgroups walks the tiles (row_groups.h), so
 // that the bound on the tiles the host has to launch for, up to one more row
@@ -22,17 +22,13 @@ template <int ES, int OUT, int BM, int BK, int FA, int FB, bool BT>
 __global__ __launch_bounds__(256) void grouped_tile_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C,
     const int32_t* __restrict__ offsets, int groups, int rows, int N, int K, const float* __restrict__ sA,
-    const float* __restrict__ sB, const float* __restrict__ sOut, int most_tiles, int tiles_n, int eflags) {
+    const float* __restrict__ sB, const float* __restrict__ sOut, int most, int tiles_n, int eflags) {
     constexpr int BN = BM;
-    RowGroups<BM> rg;
-    rg.init(offsets, groups, rows, most_tiles);
     const bool chan = (eflags & EPI_CHANNEL) != 0;
-    const int total = rg.total * tiles_n;
-    for (int id = blockIdx.x; id < total; id += gridDim.x) {
-        int tm, tn;
-        tile_coords(id, rg.total, tiles_n, tm, tn);
-        const RowTile t = rg.find(tm);
-        if (t.m0 >= t.end) continue;
+    for (int id = blockIdx.x; id < most; id += gridDim.x) {   // the grid is a multiple of 8: one XCD's tiles
+        const RowTile t = find_row_tile<BM>(offsets, groups, rows, id, tiles_n);
+        if (t.m0 >= t.end) break;
+        const int tn = t.tn;
         if (t.group < 0) {
             zero_rows<BM, BN, OUT == OUT_F32 ? 4 : (OUT == OUT_F16 ? 2 : 1)>(C, t.m0, t.end, tn * BN, N);
             continue;
@@ -46,9 +42,9 @@ __global__ __launch_bounds__(256) void grouped_tile_kernel(
 template <int ES, int BM, int FA, int FB, bool BT>
 hipError_t launch_grouped_tile(const GroupedArgs& a) {
     constexpr int BK = 128 / ES;
-    const int64_t tiles_n = (a.N + BM - 1) / BM, most = most_row_tiles(a.M, a.groups, BM);
-    if (most * tiles_n > 0x7FFFFFFF - kTileWorkgroups) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)(most * tiles_n < kTileWorkgroups ? most * tiles_n : kTileWorkgroups);
+    const int64_t tiles_n = (a.N + BM - 1) / BM, most = most_workgroups(a.M, a.groups, BM, tiles_n);
+    if (most > 0x7FFFFFFF - kTileWorkgroups) return hipErrorInvalidValue;
+    const unsigned grid = (unsigned)(most < kTileWorkgroups ? most : kTileWorkgroups);
     const int eflags = (a.out_dtype == OUT_E5M2 ? EPI_E5M2 : 0) | (a.channel ? EPI_CHANNEL : 0);
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);

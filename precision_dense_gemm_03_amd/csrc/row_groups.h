@@ -4,10 +4,19 @@
 // offsets[0] and from offsets[G] on belong to no group. The host knows only
 // rows and G, so every wave finds its tile itself: the rows form G + 2
 // segments (the first and the last belong to no group), segment s has
-// ceil(size / BM) tiles, and a tile's segment comes from a running sum of
-// those, 64 segments at a time across the wave's lanes. No tile crosses a
-// segment's end. Offsets are clamped to [0, rows]: whatever they hold, no
-// address leaves the operands.
+// ceil(size / BM) rows of tiles, and no tile crosses a segment's end. Offsets
+// are clamped to [0, rows]: whatever they hold, no address leaves the operands.
+//
+// Order. A segment's rows of tiles are cut into equal shares of at most
+// kTallest, and a column of a share (those tiles all read one 256-column piece
+// of the weight) is what one XCD takes: the columns, counted through all
+// segments, go round the 8 XCDs. So each piece of a weight is read into one
+// L2, once per share, by tiles that run together; every XCD gets an equal part
+// of every group, whatever the groups' sizes; and the rows of A, which all
+// XCDs read, are the smaller operand. Consecutive workgroups go round the
+// XCDs, so workgroup b takes the (b / 8)th tile of XCD b % 8. (All the groups'
+// last, partly filled rows of tiles after all others, to level the load with
+// short tiles, measured 5 to 10 % slower: they read the weights again alone.)
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -16,75 +25,92 @@
 namespace libgemm {
 
 struct RowTile {
-    int group;   // -1: rows of no group
+    int group;   // -1: rows of no group; -2: no tile left
     int m0;      // first row
     int end;     // end of the segment's rows
+    int tn;      // column tile
 };
 
+constexpr int kTallest = 6;
+
+// Sum over this lane and those below it (row shifts, then row broadcasts).
+__device__ __forceinline__ int wave_running_sum(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
+    return v;
+}
+
+// The tile of workgroup bid, the same in every lane of the wave: 64 segments
+// at a time, one per lane, running sums for the columns before each segment
+// and this XCD's tiles up to it, and a ballot for the segment.
 template <int BM>
-struct RowGroups {
-    const int32_t* offsets;
-    int groups, rows, lane;
-    int lo, hi, sum;   // the last scanned 64 segments: this lane's rows, tiles up to and including it
-    int total;         // tiles of all segments
-
-    __device__ __forceinline__ int edge(int i) const { return min(max(offsets[i], 0), rows); }
-
-    // Scans segments base .. base + 63; returns their number of tiles.
-    __device__ __forceinline__ int scan(int base) {
+__device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ offsets, int groups, int rows, int bid,
+                                                 int tiles_n) {
+    const int lane = threadIdx.x & 63, x = bid & 7;
+    int at = bid >> 3;      // tiles of this XCD still to pass over
+    int columns = 0;        // of the segments before this 64, modulo 8
+    for (int base = 0; base < groups + 2; base += 64) {
         const int s = base + lane;
-        lo = hi = 0;
+        int lo = 0, hi = 0;
         if (s <= groups + 1) {
-            lo = s == 0 ? 0 : edge(s - 1);
-            hi = s == groups + 1 ? rows : edge(s);
+            lo = s == 0 ? 0 : min(max(offsets[s - 1], 0), rows);
+            hi = s == groups + 1 ? rows : min(max(offsets[s], 0), rows);
             hi = max(lo, hi);
         }
-        sum = (int)(((int64_t)hi - lo + BM - 1) / BM);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int u = __shfl_up(sum, d);
-            if (lane >= d) sum += u;
-        }
-        return __builtin_amdgcn_readlane(sum, 63);
-    }
-
-    // limit: the most tiles offsets in order can give (the host's bound).
-    __device__ __forceinline__ void init(const int32_t* off, int n, int r, int limit) {
-        offsets = off;
-        groups = n;
-        rows = r;
-        lane = threadIdx.x & 63;
-        int64_t t = 0;
-        for (int base = 0; base < groups + 2; base += 64) t += scan(base);
-        total = (int)min(t, (int64_t)limit);
-    }
-
-    // The tile tm in [0, total), the same in every lane of the wave.
-    __device__ __forceinline__ RowTile find(int tm) {
-        int before = 0;
-        RowTile r{-1, 0, 0};
-        for (int base = 0; base < groups + 2; base += 64) {
-            const int here = groups + 2 <= 64 ? __builtin_amdgcn_readlane(sum, 63) : scan(base);
-            if (tm < before + here) {
-                const int at = __popcll(__builtin_amdgcn_ballot_w64(sum <= tm - before));   // its lane
-                const int first = at ? __builtin_amdgcn_readlane(sum, at - 1) : 0;
-                const int s = base + at;
-                r.group = s >= 1 && s <= groups ? s - 1 : -1;
-                r.m0 = __builtin_amdgcn_readlane(lo, at) + (tm - before - first) * BM;
-                r.end = __builtin_amdgcn_readlane(hi, at);
-                break;
+        const uint32_t tall = ((uint32_t)(hi - lo) + BM - 1) / BM;
+        const uint32_t shares = (tall + kTallest - 1) / kTallest;
+        const uint32_t low = shares ? tall / shares : 0, more = tall - low * shares;   // `more` shares of low + 1 rows
+        const int mine = (int)shares * tiles_n;
+        const int upto = wave_running_sum(mine & 7);   // counts modulo 8 place the columns
+        const int j0 = (x - columns - upto + (mine & 7)) & 7;   // first column of this XCD
+        const int big = (int)more * tiles_n;
+        const int n_big = big > j0 ? (big - j0 + 7) >> 3 : 0;
+        const int n_all = mine > j0 ? (mine - j0 + 7) >> 3 : 0;
+        const int tiles = n_big * (int)(low + 1) + (n_all - n_big) * (int)low;
+        const int sum = wave_running_sum(tiles);
+        const int here = __builtin_amdgcn_readlane(sum, 63);
+        if (at < here) {
+            const int l = __popcll(__builtin_amdgcn_ballot_w64(sum <= at));   // the segment's lane
+            int i = at - (l ? __builtin_amdgcn_readlane(sum, l - 1) : 0);
+            const int q_low = __builtin_amdgcn_readlane((int)low, l), q_more = __builtin_amdgcn_readlane((int)more, l);
+            const int q_big = __builtin_amdgcn_readlane(n_big, l);
+            int column, row;
+            if (i < q_big * (q_low + 1)) {
+                column = i / (q_low + 1);
+                row = i - column * (q_low + 1);
+            } else {
+                i -= q_big * (q_low + 1);
+                column = i / q_low;
+                row = i - column * q_low;
+                column += q_big;
             }
-            before += here;
+            const int j = __builtin_amdgcn_readlane(j0, l) + 8 * column;
+            const int share = j / tiles_n;
+            row += share * q_low + min(share, q_more);
+            const int seg = base + l;
+            RowTile r;
+            r.group = seg >= 1 && seg <= groups ? seg - 1 : -1;
+            r.m0 = __builtin_amdgcn_readlane(lo, l) + row * BM;
+            r.end = __builtin_amdgcn_readlane(hi, l);
+            r.tn = j - share * tiles_n;
+            return r;
         }
-        return r;
+        at -= here;
+        columns += __builtin_amdgcn_readlane(upto, 63);
     }
-};
+    return RowTile{-2, 0, 0, 0};
+}
 
-// The most tiles of BM rows that G groups in order can give: each nonempty
-// segment adds at most BM - 1 padded rows.
-inline int64_t most_row_tiles(int64_t rows, int64_t groups, int bm) {
+// Workgroups that cover every tile that offsets in order can give: all rows of
+// tiles, of which each nonempty segment pads at most one, and for each of them
+// one column more than its eighth.
+inline int64_t most_workgroups(int64_t rows, int64_t groups, int bm, int64_t tiles_n) {
     const int64_t segs = groups + 2 < rows ? groups + 2 : rows;
-    return (rows + segs * (bm - 1)) / bm;
+    return (rows + segs * (bm - 1)) / bm * ((tiles_n + 7) / 8 * 8 + 8);
 }
 
 // Zeros in columns [n0, n0 + BN) of rows [m0, min(end, m0 + BM)): the rows of no group.
