@@ -224,14 +224,21 @@ def _check(status: int, what: str):
         raise GemmError(status, what)
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(stream):
     if stream is None:
-        return _torch().cuda.current_stream().cuda_stream
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -796,6 +803,8 @@ def amax_quantize_fp8_pair_bt(xa, xb, fmt=FMT_E4M3, pow2=False, amax=None, scale
 
 def _need(t, dtype, shape, what):
     """Checks an argument's type and shape (None in shape: any size)."""
+    if t.dtype is dtype and t.shape == shape:   # the common case, one comparison
+        return
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
     if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):

@@ -621,7 +621,7 @@ __device__ __forceinline__ void pp_body(const uint8_t* __restrict__ A, const uin
                     if (chan0) acc[i][j][r] *= sr * sB[min(n0 + col_t + 32 * j + 8 * (r >> 2) + (r & 3), N - 1)];
                 }
         }
-        ext.template add32<T::MI>(acc, m0 + T::MR * G, n0 + 64 * wj, M, N);
+        ext.template add_tile<T::MI>(acc, lds, m0, n0, G, wj, M, N);
     }
     const bool chan = !Ext::kActive && chan0;
     const float scale = Ext::kActive ? 1.0f : scale0;

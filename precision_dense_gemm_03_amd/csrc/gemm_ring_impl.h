@@ -294,9 +294,18 @@ __device__ __forceinline__ void store_elem(void* C, int64_t idx, float y, int ef
 
 // RAG (row groups, adapters): tiles that M or N cuts keep the vector stores,
 // masked. Ext: what is added to the products before the store (NoExtra, or
-// LoraExtra of lora_extra.h).
+// LoraExtra of lora_extra.h), or with kStores what stores them.
 struct NoExtra {
-    static constexpr bool kActive = false;
+    static constexpr bool kActive = false, kStores = false;
+};
+
+template <class Ext, bool ACTIVE = Ext::kActive>
+struct ExtPiece {
+    typedef int type;
+};
+template <class Ext>
+struct ExtPiece<Ext, true> {
+    typedef typename Ext::Piece type;
 };
 
 // One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N.
@@ -570,6 +579,14 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
         }
     };
 
+    const int row = m0 + 16 * wr + j16;
+    auto col_of = [&](int tn) __attribute__((always_inline)) { return n0 + 16 * (T::TN * wc + tn) + 4 * g; };
+    typename ExtPiece<Ext>::type piece[T::TN];
+    if constexpr (Ext::kActive) {
+#pragma unroll
+        for (int tn = 0; tn < T::TN; ++tn) ext.prefetch(piece[tn], row, col_of(tn), kg, M, N);
+    }
+
     // this wave's loads per stage (MAX_PER_WAVE or one fewer)
     const bool full_share = loads_of<T::INST>(wave) == T::MAX_PER_WAVE;
 
@@ -601,6 +618,19 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
         }
     }
 
+    if constexpr (Ext::kActive) {   // scaled here (each group its part), added to, stored as it is
+#pragma unroll
+        for (int tn = 0; tn < T::TN; ++tn) {
+            acc[tn] *= scale;
+            if (chan) {
+                const float sr = sA[min(row, M - 1)];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[tn][e] *= sr * sB[min(col_of(tn) + e, N - 1)];
+            }
+            ext.add_row4(acc[tn], piece[tn], row, col_of(tn), kg, T::KW, N);
+        }
+    }
+
     // ---- wave groups 1 .. KW-1 hand their partial sums to group 0 ----
     if constexpr (T::KW > 1) {
         if (kg > 0) {
@@ -616,26 +646,21 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
     }
 
     // ---- epilogue: lane holds row 16 wr + j16 and columns 16 (TN wc + tn) + 4 g + 0..3 ----
-    const int row = m0 + 16 * wr + j16;
     const bool interior = vec_out && (RAG || ((m0 + BM <= M) && (n0 + BN <= N)));
     if constexpr (RAG) {
         if (row >= M) return;
     }
 #pragma unroll
     for (int tn = 0; tn < T::TN; ++tn) {
-        const int col = n0 + 16 * (T::TN * wc + tn) + 4 * g;
+        const int col = col_of(tn);
+        if constexpr (Ext::kStores) {
+            ext.store4(acc[tn], row, col);
+            continue;
+        }
         if (RAG && col >= N) continue;   // (vec_out: N is a multiple of 4)
         v4f y;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = acc[tn][e] * scale;
-        if constexpr (Ext::kActive) {
-            if (chan) {
-                const float sr = sA[row];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] *= sr * sB[min(col + e, N - 1)];
-            }
-            ext.add_row4(y, row, col, M, N);
-        }
+        for (int e = 0; e < 4; ++e) y[e] = Ext::kActive ? acc[tn][e] : acc[tn][e] * scale;
         if (interior) {
             if (chan && !Ext::kActive) {
                 const float sr = sA[row];

@@ -5,16 +5,29 @@
 // zero for rows without an adapter and for r from rank to rank_p (the next
 // multiple of 8); the product kernels add low LB^T (lora_extra.h).
 //
-// Few rows: each usually has its own adapter, so nothing is shared between
-// rows and a wave takes one (i, r): a dot product over K, both sides read in
-// 16-byte pieces, rows * rank waves. More rows: a workgroup takes 16 rows and
-// its 8 waves share out K in tiles of 64 (128 bytes of each row); every
-// adapter present multiplies the block on the matrix cores (LA as the first
-// operand, so a lane ends with one row's four neighbouring values) and its
-// rows keep the result; the waves' sums join in LDS in wave order.
+// Three kernels:
+//
+// Few rows (lora_low_dot_kernel): each usually has its own adapter, so nothing
+// is shared between rows and a wave takes one (i, r): a dot product over K, both
+// sides read in 16-byte pieces, rows * rank waves.
+//
+// More rows, 16-byte aligned (lora_low_ring_kernel): 16 rows against 16, 32 or
+// 64 of an adapter's rows on the deep-ring kernel, whose direct loads take whole
+// lines of both and run far ahead: the call is bound by moving X and, for each
+// 16 rows again, LA into the compute units (4096 rows, K 4096, rank 64: 640 KB
+// each). A block's adapters are shared out over kLowParts workgroups, one pass
+// each; an adapter's pass stores its own rows.
+//
+// Any alignment (lora_low_kernel): a workgroup takes 16 rows and its 8 waves
+// share out K in tiles of 64, straight from memory to the matrix cores; every
+// adapter present multiplies the block (LA as the first operand, so a lane ends
+// with one row's four neighbouring values) and its rows keep the result; the
+// waves' sums join in LDS in wave order. Its loads take a line per lane: 41 us
+// for the sizes above.
 #include <hip/hip_runtime.h>
 
 #include "device_common.h"
+#include "gemm_ring_impl.h"
 #include "kernels.h"
 
 namespace libgemm {
@@ -69,6 +82,58 @@ __global__ __launch_bounds__(256) void lora_low_dot_kernel(const _Float16* __res
         for (int s = 32; s; s >>= 1) sum += __shfl_xor(sum, s);
     }
     if (lane == 0) low[row * rank_p + r] = has ? sum * lscale[a] : 0.0f;
+}
+
+// Stores the low-rank values of the rows whose adapter is `a`.
+struct LowStore {
+    static constexpr bool kActive = false, kStores = true;
+    float* low;
+    const int32_t* adapter;
+    float scale;
+    int a, rank, rank_p;
+    __device__ __forceinline__ void store4(v4f y, int row, int col) const {
+        if (col >= rank_p || adapter[row] != a) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = col + e < rank ? y[e] * scale : 0.0f;
+        *reinterpret_cast<v4f*>(low + (int64_t)row * rank_p + col) = y;
+    }
+};
+
+constexpr int kLowParts = 4;
+
+template <int BN>
+__global__ __launch_bounds__(256) void lora_low_ring_kernel(const uint8_t* __restrict__ X,
+                                                            const uint8_t* __restrict__ LA,
+                                                            const int32_t* __restrict__ adapter,
+                                                            const float* __restrict__ lscale, int M, int K, int rank,
+                                                            int rank_p, int adapters, float* __restrict__ low) {
+    using T = ring::Ring<2, 16, BN, true>;
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
+    __shared__ v4f red[T::RED_SLOTS];
+    const int lane = threadIdx.x & 63, m0 = blockIdx.x * 16, n0 = blockIdx.y * BN;
+    int mine = -1;
+    if (lane < 16 && m0 + lane < M) {
+        mine = adapter[m0 + lane];
+        if (mine < 0 || mine >= adapters) mine = -1;
+    }
+    if (blockIdx.z == 0) {   // rows without an adapter: zeros
+        const uint32_t none = (uint32_t)__builtin_amdgcn_ballot_w64(mine < 0);
+        for (int i = threadIdx.x; i < 16 * BN; i += 256) {
+            const int r = i / BN, c = n0 + i % BN;
+            if (((none >> r) & 1) && m0 + r < M && c < rank_p) low[(int64_t)(m0 + r) * rank_p + c] = 0.0f;
+        }
+    }
+    int part = 0;
+    for (uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0); left; part = (part + 1) % kLowParts) {
+        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
+        left &= ~(uint32_t)__builtin_amdgcn_ballot_w64(mine == a);
+        if (part != (int)blockIdx.z) continue;
+        const LowStore store{low, adapter, lscale[a], a, rank, rank_p};
+        ring::ring_body<2, 16, BN, OUT_F32, 0, 0, true, 0, true, LowStore>(
+            X, LA + (int64_t)a * rank * K * 2, low, M, rank, K, nullptr, nullptr, nullptr, m0, n0, 0, 0, ring, red,
+            store);
+        __syncthreads();
+    }
 }
 
 constexpr int kLowWaves = 8;
@@ -159,6 +224,19 @@ hipError_t launch_lora_low(const LoraArgs& a) {
         return hipGetLastError();
     }
     const unsigned blocks = (unsigned)((a.M + 15) / 16);
+    const bool ring_ok = ring::aligned16(a.X) && ring::aligned16(a.LA) && a.K % 8 == 0 && a.K < (1 << 24);
+    if (ring_ok) {
+        const unsigned parts = (unsigned)(a.adapters < kLowParts ? a.adapters : kLowParts);
+#define LIBGEMM_GO(BN)                                                                                      \
+    lora_low_ring_kernel<BN><<<dim3(blocks, (unsigned)((rank + BN - 1) / BN), parts), 256, 0, a.stream>>>(  \
+        (const uint8_t*)a.X, (const uint8_t*)a.LA, a.adapter, a.lscale, (int)a.M, (int)a.K, rank, rank_p,   \
+        (int)a.adapters, a.low)
+        if (rank <= 16) LIBGEMM_GO(16);
+        else if (rank <= 32) LIBGEMM_GO(32);
+        else LIBGEMM_GO(64);
+#undef LIBGEMM_GO
+        return hipGetLastError();
+    }
 #define LIBGEMM_GO(RB)                                                                                        \
     lora_low_kernel<RB><<<dim3(blocks, (unsigned)((rank + 16 * RB - 1) / (16 * RB))), 64 * kLowWaves, 0, a.stream>>>( \
         X, LA, a.adapter, a.lscale, (int)a.M, (int)a.K, rank, rank_p, (int)a.adapters, a.low)

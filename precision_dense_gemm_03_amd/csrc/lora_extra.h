@@ -21,7 +21,7 @@
 namespace libgemm {
 
 struct LoraExtra {
-    static constexpr bool kActive = true;
+    static constexpr bool kActive = true, kStores = false;
     const float* low;         // [rows, rank_p], zero from rank on
     const int32_t* adapter;   // [rows]
     const _Float16* LB;       // [adapters, N, rank]
@@ -44,22 +44,21 @@ struct LoraExtra {
         return v;
     }
 
-    // This lane's STEPS chunks of a row's piece [p0, p0 + 64) as hi and lo
-    // operands; chunk s is 8 (GROUPS s + g) values into the piece, and the
-    // lanes that share the row differ in lane bits 64 / GROUPS and up. Returns
-    // the piece's exponent.
-    template <int STEPS, int GROUPS>
-    __device__ __forceinline__ int split_piece(const float* row, int p0, int g, v8h (&hi)[STEPS],
-                                               v8h (&lo)[STEPS]) const {
+    // STEPS chunks of 8 values of a row, from r0 on and `step` apart, as hi and
+    // lo halves; the lanes lane ^ d, d = first_d, 2 first_d, .. below end_d, hold
+    // the rest of the row's piece. Returns the piece's exponent.
+    template <int STEPS>
+    __device__ __forceinline__ int split_chunks(const float* row, int r0, int step, int first_d, int end_d,
+                                                v8h (&hi)[STEPS], v8h (&lo)[STEPS]) const {
         float v[STEPS][8];
         float m = 0.0f;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const int r0 = p0 + 8 * (GROUPS * s + g);
+            const int r = r0 + step * s;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v4f t = v4f{0.f, 0.f, 0.f, 0.f};
-                if (r0 < rank_p) t = *reinterpret_cast<const v4f*>(row + r0 + 4 * h);
+                if (r < rank_p) t = *reinterpret_cast<const v4f*>(row + r + 4 * h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[s][4 * h + i] = t[i];
@@ -67,8 +66,7 @@ struct LoraExtra {
                 }
             }
         }
-#pragma unroll
-        for (int d = 64 / GROUPS; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        for (int d = first_d; d < end_d; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
         const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) - 15 : 0;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
@@ -96,7 +94,7 @@ struct LoraExtra {
             const float* lrow = low + (int64_t)min(row, M - 1) * rank_p;
             for (int p0 = 0; p0 < rank_p; p0 += 64) {
                 v8h hi[2], lo[2];
-                const int e = split_piece<2, 4>(lrow, p0, g, hi, lo);
+                const int e = split_chunks<2>(lrow, p0 + 8 * g, 32, 16, 64, hi, lo);
                 for (uint32_t left = todo; left;) {
                     const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
                     const uint32_t rows = (uint32_t)__builtin_amdgcn_ballot_w64(mine == a) & 0xFFFFu;
@@ -123,64 +121,129 @@ struct LoraExtra {
         }
     }
 
-    // 32x32 blocks with one row per lane (LB's operand first): acc[i][j] holds
-    // row row0 + 32 i + lane % 32, columns col0 + 32 j + 8 q + 4 (lane / 32) + e
-    // in value 4 q + e.
-    template <int MI>
-    __device__ __forceinline__ void add32(v16f (&acc)[MI][2], int row0, int col0, int M, int N) const {
-        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int row = row0 + 32 * i + lr;
-            const int mine = adapter_of(row, M);
-            const uint32_t todo = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0);
-            if (!todo) continue;
-            const float* lrow = low + (int64_t)min(row, M - 1) * rank_p;
-            for (int p0 = 0; p0 < rank_p; p0 += 64) {
+    // A 256-column tile of the ping-pong kernel (its acc, LDS regions and wave
+    // layout: acc[i][j] holds row MR G + 32 i + lane % 32, columns 64 wj + 32 j +
+    // 8 q + 4 (lane / 32) + e in value 4 q + e). After the K loop the LDS is
+    // free: the tile's low-rank values go there split, once for all waves (hi
+    // in region a[0], lo in a[1], 128 bytes of a row's piece each; the row's
+    // exponent and adapter in a[2]), then for each adapter of the tile its 256
+    // rows of LB (b[0], b[1]). So the wait for memory is one per adapter, and
+    // the accumulators, which leave few registers, meet operands from LDS.
+    // (Operands straight from memory, a wave for itself: 27 us of 137 for 4096
+    // rows, N = K = 4096, rank 64.)
+    template <int MI, class Lds>
+    __device__ __forceinline__ void add_tile(v16f (&acc)[MI][2], const Lds& lds, int m0, int n0, int G, int wj, int M,
+                                             int N) const {
+        constexpr int BM = 64 * MI, MR = 32 * MI;
+        const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, h = lane >> 5;
+        LDS_AS int* ids = (LDS_AS int*)lds.a[2];
+        LDS_AS int* exps = ids + BM;
+        auto slot = [](int r, int c) __attribute__((always_inline)) -> int {
+            return r * 128 + ((c ^ ((r & 7) ^ ((r >> 3) & 1))) << 4);
+        };
+        const int srow = tid >> 1, half = tid & 1;   // staging: 32 values of a row (of low, of LB) per thread
+        if (tid < BM) ids[tid] = adapter_of(m0 + tid, M);
+        for (int p0 = 0; p0 < rank_p; p0 += 64) {
+            if (srow < BM) {
                 v8h hi[4], lo[4];
-                const int e = split_piece<4, 2>(lrow, p0, h, hi, lo);
-                for (uint32_t left = todo; left;) {
-                    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-                    left &= ~(uint32_t)__builtin_amdgcn_ballot_w64(mine == a);
+                const int e =
+                    split_chunks<4>(low + (int64_t)min(m0 + srow, M - 1) * rank_p, p0 + 32 * half, 8, 1, 2, hi, lo);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    *(LDS_AS v8h*)(lds.a[0] + slot(srow, 4 * half + q)) = hi[q];
+                    *(LDS_AS v8h*)(lds.a[1] + slot(srow, 4 * half + q)) = lo[q];
+                }
+                if (half == 0) exps[srow] = e;
+            }
+            __syncthreads();
+            // the tile's adapters, one after another (every wave goes through the same list)
+            int id[(BM + 63) / 64];
+#pragma unroll
+            for (int k = 0; k < (BM + 63) / 64; ++k) id[k] = ids[64 * k + lane];
+            for (;;) {
+                int a = -1;
+#pragma unroll
+                for (int k = 0; k < (BM + 63) / 64; ++k) {
+                    const uint64_t some = __builtin_amdgcn_ballot_w64(id[k] >= 0);
+                    if (a < 0 && some) a = __builtin_amdgcn_readlane(id[k], __builtin_ctzll(some));
+                }
+                if (a < 0) break;
+#pragma unroll
+                for (int k = 0; k < (BM + 63) / 64; ++k) id[k] = id[k] == a ? -1 : id[k];
+                LDS_AS uint8_t* lb = srow < 128 ? lds.b[0] : lds.b[1];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *(LDS_AS v8h*)(lb + slot(srow & 127, 4 * half + q)) =
+                        lb_chunk(a, min(n0 + srow, N - 1), p0 + 32 * half + 8 * q, N);
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < MI; ++i) {
+                    const int r = MR * G + 32 * i + lr;
+                    const bool mine = ids[r] == a;
+                    if (__builtin_amdgcn_ballot_w64(mine) == 0) continue;
+                    const int e = exps[r];
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const int col = min(col0 + 32 * j + lr, N - 1);
+                        const int c = 64 * (wj & 1) + 32 * j + lr;
+                        const LDS_AS uint8_t* b = (wj < 2 ? lds.b[0] : lds.b[1]);
                         v16f sum;
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) sum[r] = 0.0f;
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) {
-                            if (p0 + 16 * s >= rank_p) break;
-                            const v8h b = lb_chunk(a, col, p0 + 8 * (2 * s + h), N);
-                            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, hi[s], sum, 0, 0, 0);
-                            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(b, lo[s], sum, 0, 0, 0);
+                        for (int x = 0; x < 16; ++x) sum[x] = 0.0f;
+                        for (int s = 0; s < 4 && p0 + 16 * s < rank_p; ++s) {
+                            const v8h bo = *(const LDS_AS v8h*)(b + slot(c, 2 * s + h));
+                            const v8h ho = *(const LDS_AS v8h*)(lds.a[0] + slot(r, 2 * s + h));
+                            const v8h lw = *(const LDS_AS v8h*)(lds.a[1] + slot(r, 2 * s + h));
+                            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(bo, ho, sum, 0, 0, 0);
+                            sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(bo, lw, sum, 0, 0, 0);
                         }
 #pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            if (mine == a) acc[i][j][r] += __builtin_ldexpf(sum[r], e);
+                        for (int x = 0; x < 16; ++x)
+                            if (mine) acc[i][j][x] += __builtin_ldexpf(sum[x], e);
                     }
                 }
+                __syncthreads();
             }
+            __syncthreads();   // the next piece (or the stores' staging) overwrites the LDS
         }
     }
 
-    // Four neighbouring columns of one row, on the vector units: for few rows,
-    // where each usually has its own adapter and a block has nothing to share.
-    __device__ __forceinline__ void add_row4(v4f& y, int row, int col, int M, int N) const {
-        const int a = adapter_of(row, M);
-        if (a < 0) return;
-        const float* lrow = low + (int64_t)row * rank_p;
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-        for (int r0 = 0; r0 < rank_p; r0 += 8) {
-            const v4f l0 = *reinterpret_cast<const v4f*>(lrow + r0), l1 = *reinterpret_cast<const v4f*>(lrow + r0 + 4);
-            v8h b[4];
+    // Few rows: each usually has its own adapter and a block has nothing to
+    // share, so the term goes through the vector units, four neighbouring
+    // columns of one row per lane, a row's low-rank values in pieces of 8 that
+    // the waves holding the block's partial sums share out (wave group kg of KW
+    // takes pieces kg, kg + KW, ...). A lane's first piece is fetched before
+    // the K loop, whose length hides LB's way from memory.
+    struct Piece {
+        int adapter;
+        v4f l[2];
+        v8h b[4];
+    };
+
+    __device__ __forceinline__ void fetch(Piece& p, int row, int col, int r0, int N) const {
+        const float* lrow = low + (int64_t)row * rank_p + r0;
+        p.l[0] = *reinterpret_cast<const v4f*>(lrow);
+        p.l[1] = *reinterpret_cast<const v4f*>(lrow + 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) b[e] = lb_chunk(a, min(col + e, N - 1), r0, N);
+        for (int e = 0; e < 4; ++e) p.b[e] = lb_chunk(p.adapter, min(col + e, N - 1), r0, N);
+    }
+
+    __device__ __forceinline__ void prefetch(Piece& p, int row, int col, int kg, int M, int N) const {
+        p.adapter = adapter_of(row, M);
+        if (p.adapter >= 0 && 8 * kg < rank_p) fetch(p, row, col, 8 * kg, N);
+    }
+
+    __device__ __forceinline__ void add_row4(v4f& y, Piece& p, int row, int col, int kg, int KW, int N) const {
+        if (p.adapter < 0 || 8 * kg >= rank_p) return;
+        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int r0 = 8 * kg;;) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum[e] = __builtin_fmaf(i < 4 ? l0[i & 3] : l1[i & 3], (float)b[e][i], sum[e]);
+                for (int i = 0; i < 8; ++i)
+                    sum[e] = __builtin_fmaf(p.l[i >> 2][i & 3], (float)p.b[e][i], sum[e]);
+            r0 += 8 * KW;
+            if (r0 >= rank_p) break;
+            fetch(p, row, col, r0, N);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] += sum[e];

@@ -1,9 +1,11 @@
 // Rows to their experts and back, for gfx950: the gather of the tokens' rows
 // in expert order, the weighted sum of the experts' outputs (combine) and its
 // gradient. All are bound by bytes: each row is read and written in 16-byte
-// units, a row by 8 to 256 lanes (the smallest power of two that covers it, a
-// whole workgroup where few rows would leave compute units idle), the k rows
-// of a token in flight together. Rows may start at any element: the units are
+// units, a row by 8 to 256 lanes (the smallest of 8, 16, 32, 64 and 256 that
+// covers it), the k rows of a token in flight together, two units of each
+// where a row has that many. 8192 tokens of 8 rows of 4096 halves: 103 us
+// (5.9 TB/s); a wave per token 117 to 138, without the non-temporal hint 110.
+// Rows may start at any element: the units are
 // plain 16-byte accesses at element alignment, which gfx950's vector memory
 // takes, and a row's last partial unit goes element by element.
 //
@@ -66,6 +68,32 @@ __device__ __forceinline__ void store_values(T* p, const float (&v)[N]) {
     }
 }
 
+// 16384 tokens of 2048 halves to 131072 rows: 144 us, 7.4 TB/s of reads and
+// writes together (each token is read again for each of its 8 experts, from
+// beyond the L2s). Rows picked by ranges of tokens, one range per XCD and L2,
+// measured 272 us: the writes then scatter.
+// The row of this lane, in a scalar register where whole waves share it.
+template <int LPR>
+__device__ __forceinline__ int64_t lane_row() {
+    if constexpr (LPR >= kRowThreads) return blockIdx.x;
+    const int sub = threadIdx.x / LPR;
+    return (int64_t)blockIdx.x * (kRowThreads / LPR) + (LPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
+}
+
+// Rows j0 .. j0 + KB - 1 of a token: each one's offset in z, -1 where there is
+// none, and its weight. (No load hangs on a condition: they go out together.)
+template <int KB, int LPR>
+__device__ __forceinline__ void fetch_rows(const int32_t* __restrict__ row, const float* __restrict__ weight, int j0,
+                                           int K, int64_t rows, int64_t width, int64_t (&at)[KB], float (&w)[KB]) {
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+        const int jj = min(j0 + j, K - 1);
+        const int64_t r = row[jj];
+        w[j] = weight ? weight[jj] : 1.0f;
+        at[j] = j0 + j < K && r >= 0 && r < rows ? r * width : -1;
+    }
+}
+
 template <int LPR>
 __global__ __launch_bounds__(kRowThreads) void moe_gather_kernel(const uint8_t* __restrict__ x,
                                                                  const int32_t* __restrict__ token,
@@ -73,7 +101,7 @@ __global__ __launch_bounds__(kRowThreads) void moe_gather_kernel(const uint8_t* 
                                                                  int64_t rows, int64_t row_bytes) {
     constexpr int U = 4;   // units in flight per lane
     const int l = threadIdx.x % LPR;
-    const int64_t r = (int64_t)blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
+    const int64_t r = lane_row<LPR>();
     if (r >= rows) return;
     const int64_t t = token[r];
     const bool has = t >= 0 && t < tokens;
@@ -103,7 +131,7 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_kernel(const ZT* __re
                                                                   int64_t width) {
     constexpr int N = Unit<ZT>::N;
     const int l = threadIdx.x % LPR;
-    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
+    const int64_t t = lane_row<LPR>();
     if (t >= T) return;
     const int32_t* rt = row + t * K;
     const float* wt = weight ? weight + t * K : nullptr;
@@ -113,37 +141,40 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_kernel(const ZT* __re
     int64_t at[KB];
     float w[KB];
     auto fetch = [&](int j0) __attribute__((always_inline)) {
-#pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            int64_t r = -1;
-            w[j] = 0.0f;
-            if (j0 + j < K) {
-                r = rt[j0 + j];
-                w[j] = wt ? wt[j0 + j] : 1.0f;
-            }
-            at[j] = r >= 0 && r < rows ? r * width : -1;
-        }
+        fetch_rows<KB, LPR>(rt, wt, j0, K, rows, width, at, w);
     };
     fetch(0);
-    for (int64_t u = l; u < units; u += LPR) {
-        float acc[N];
+    // UN units of each row at once
+    auto sum_units = [&](int64_t u, auto un) __attribute__((always_inline)) {
+        constexpr int UN = decltype(un)::value;
+        float acc[UN][N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+        for (int x = 0; x < UN; ++x)
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[x][i] = 0.0f;
         for (int j0 = 0; j0 < K; j0 += KB) {
             if (!once) fetch(j0);
-            Unit<ZT> v[KB];
+            Unit<ZT> v[UN][KB];
 #pragma unroll
-            for (int j = 0; j < KB; ++j)
-                if (at[j] >= 0) v[j] = load_unit(z + at[j] + u * N);
+            for (int x = 0; x < UN; ++x)
 #pragma unroll
-            for (int j = 0; j < KB; ++j)
-                if (at[j] >= 0) {
+                for (int j = 0; j < KB; ++j)
+                    if (at[j] >= 0) v[x][j] = load_unit(z + at[j] + (u + x * LPR) * N);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) acc[i] = __builtin_fmaf(w[j], (float)v[j].e[i], acc[i]);
-                }
+            for (int x = 0; x < UN; ++x)
+#pragma unroll
+                for (int j = 0; j < KB; ++j)
+                    if (at[j] >= 0) {
+#pragma unroll
+                        for (int i = 0; i < N; ++i) acc[x][i] = __builtin_fmaf(w[j], (float)v[x][j].e[i], acc[x][i]);
+                    }
         }
-        store_values<YT, N>(yt + u * N, acc);
-    }
+#pragma unroll
+        for (int x = 0; x < UN; ++x) store_values<YT, N>(yt + (u + x * LPR) * N, acc[x]);
+    };
+    int64_t u = l;
+    for (; u + LPR < units; u += 2 * LPR) sum_units(u, std::integral_constant<int, 2>{});
+    if (u < units) sum_units(u, std::integral_constant<int, 1>{});
     for (int64_t c = units * N + l; c < width; c += LPR) {
         float acc = 0.0f;
         for (int j0 = 0; j0 < K; j0 += KB) {
@@ -164,23 +195,16 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_backward_kernel(
     constexpr int N = Unit<ET>::N;
     __shared__ float part[LPR > 64 ? kRowThreads / 64 * KB : 1];
     const int l = threadIdx.x % LPR;
-    const int64_t t = (int64_t)blockIdx.x * (kRowThreads / LPR) + threadIdx.x / LPR;
+    const int64_t t = lane_row<LPR>();
     if (t >= T) return;   // LPR > 64: the whole workgroup or none of it
     const ET* dyt = dy + t * width;
     const int64_t units = width / N;
     for (int j0 = 0; j0 < K; j0 += KB) {
         int64_t at[KB];
         float w[KB], dot[KB];
+        fetch_rows<KB, LPR>(row + t * K, weight + t * K, j0, K, rows, width, at, w);
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-            int64_t r = -1;
-            w[j] = dot[j] = 0.0f;
-            if (j0 + j < K) {
-                r = row[t * K + j0 + j];
-                w[j] = weight[t * K + j0 + j];
-            }
-            at[j] = r >= 0 && r < rows ? r * width : -1;
-        }
+        for (int j = 0; j < KB; ++j) dot[j] = 0.0f;
         for (int64_t u = l; u < units; u += LPR) {
             const Unit<ET> d = load_unit_cached(dyt + u * N);
             Unit<ET> v[KB];
@@ -234,11 +258,10 @@ __global__ __launch_bounds__(kRowThreads) void moe_combine_backward_kernel(
     }
 }
 
-// Lanes of a row of `units` units: the smallest power of two from 8 to 64 that
-// covers it; 256 for long rows when there are too few rows for one wave each
-// to fill the chip (1024 SIMDs, two waves each).
-int lanes_for(int64_t units, int64_t rows) {
-    if (units > 64) return rows < 2048 ? 256 : 64;
+// Lanes of a row of `units` units: the smallest of 8, 16, 32, 64 and 256 that
+// covers it (64 up to 128 units: two each).
+int lanes_for(int64_t units) {
+    if (units > 128) return 256;
     for (int l = 8; l < 64; l *= 2)
         if (units <= l) return l;
     return 64;
@@ -268,7 +291,7 @@ hipError_t with_batch(int64_t K, F f) {
 template <typename ZT, typename YT>
 hipError_t combine(const void* z, const int32_t* row, const float* weight, void* y, int64_t T, int64_t K, int64_t rows,
                    int64_t width, hipStream_t stream) {
-    const int lpr = lanes_for((width + Unit<ZT>::N - 1) / Unit<ZT>::N, T);
+    const int lpr = lanes_for((width + Unit<ZT>::N - 1) / Unit<ZT>::N);
     return with_batch(K, [&](auto kb) {
         return with_lanes(lpr, [&](auto lanes) {
             constexpr int L = decltype(lanes)::value;
@@ -282,7 +305,7 @@ hipError_t combine(const void* z, const int32_t* row, const float* weight, void*
 template <typename ET>
 hipError_t combine_backward(const void* dy, const void* z, const int32_t* row, const float* weight, void* dz,
                             float* dw, int64_t T, int64_t K, int64_t rows, int64_t width, hipStream_t stream) {
-    const int lpr = lanes_for((width + Unit<ET>::N - 1) / Unit<ET>::N, T);
+    const int lpr = lanes_for((width + Unit<ET>::N - 1) / Unit<ET>::N);
     return with_batch(K, [&](auto kb) {
         return with_lanes(lpr, [&](auto lanes) {
             constexpr int L = decltype(lanes)::value;
@@ -298,7 +321,7 @@ hipError_t combine_backward(const void* dy, const void* z, const int32_t* row, c
 hipError_t launch_moe_gather(const void* x, const int32_t* token, void* y, int64_t tokens, int64_t rows,
                              int64_t row_bytes, hipStream_t stream) {
     if (rows == 0 || row_bytes == 0) return hipSuccess;
-    return with_lanes(lanes_for((row_bytes + 15) / 16, rows), [&](auto lanes) {
+    return with_lanes(lanes_for((row_bytes + 15) / 16), [&](auto lanes) {
         constexpr int L = decltype(lanes)::value;
         moe_gather_kernel<L><<<blocks_for(rows, L), kRowThreads, 0, stream>>>(
             (const uint8_t*)x, token, (uint8_t*)y, tokens, rows, row_bytes);
