@@ -20,7 +20,9 @@
 //
 // Order of the tiles: the column tiles of all groups, counted through, go
 // round the XCDs, each with all its row tiles, so every XCD gets an equal part
-// of every group and tiles that run together share B's columns.
+// of every group and tiles that run together share B's columns. A tile takes
+// as long as its group has rows, so up to 64 groups come in the order of their
+// sizes, the largest first, and the short ones level the end.
 #include "gemm_pp_impl.h"
 #include "gemm_tile_impl.h"
 
@@ -39,6 +41,16 @@ __device__ __forceinline__ WgradTile wgrad_tile(int bid, const int32_t* __restri
     if (t.group >= groups) {
         t.group = -1;
         return t;
+    }
+    if (groups <= 64) {
+        const int lane = threadIdx.x & 63;
+        int size = -1, before = 0;   // groups ahead of this lane's
+        if (lane < groups) size = min(max(offsets[lane + 1], 0), rows) - min(max(offsets[lane], 0), rows);
+        for (int e = 0; e < groups; ++e) {
+            const int other = __builtin_amdgcn_readlane(size, e);
+            before += other > size || (other == size && e < lane) ? 1 : 0;
+        }
+        t.group = __builtin_ctzll(__builtin_amdgcn_ballot_w64(lane < groups && before == t.group));
     }
     t.lo = min(max(offsets[t.group], 0), rows);
     t.hi = max(t.lo, min(max(offsets[t.group + 1], 0), rows));
@@ -98,35 +110,43 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
         const int64_t at = (int64_t)t * step_bytes;
         return buffer_rsrc(src + at, end - at);
     };
-    auto stage_of = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
-        return (G == 0 ? stage_a(st) : stage_b(st)) + wj * 4096;
-    };
-    auto issue_via = [&](__amdgpu_buffer_rsrc_t rs, int kb, int st) __attribute__((always_inline)) {
-        const uint32_t kofs = (uint32_t)kb * step_bytes;
+    auto issue_offs = [&](__amdgpu_buffer_rsrc_t rs, const uint32_t (&o)[L], uint32_t kofs, int st)
+        __attribute__((always_inline)) {
         if (G == 0) {
             LDS_AS uint8_t* dst = stage_a(st) + wj * 4096;
 #pragma unroll
-            for (int i = 0; i < L; ++i) buffer_load_lds16(rs, (LDS_AS void*)(dst + i * 1024), off[i], kofs);
+            for (int i = 0; i < L; ++i) buffer_load_lds16(rs, (LDS_AS void*)(dst + i * 1024), o[i], kofs);
         } else {
             LDS_AS uint8_t* dst = stage_b(st) + wj * 4096;
 #pragma unroll
-            for (int i = 0; i < L; ++i) buffer_load_lds16(rs, (LDS_AS void*)(dst + i * 1024), off[i], kofs);
+            for (int i = 0; i < L; ++i) buffer_load_lds16(rs, (LDS_AS void*)(dst + i * 1024), o[i], kofs);
         }
     };
-    auto issue_partial = [&](int t) __attribute__((always_inline)) {
-        const uint8_t* p = src + (int64_t)t * step_bytes;
-        LDS_AS uint8_t* dst = stage_of(t & 3);
-#pragma unroll 1
-        for (int i = 0; i < L; ++i) {
-            const int r = 2 * (4 * wj + i) + (lane >> 5);
-            v4u v = v4u{0u, 0u, 0u, 0u};
-            if (t * BK + r < K) v = *reinterpret_cast<const v4u*>(p + off[i]);
-            *(LDS_AS v4u*)(dst + i * 1024 + lane * 16) = v;
-        }
+    auto issue_via = [&](__amdgpu_buffer_rsrc_t rs, int kb, int st) __attribute__((always_inline)) {
+        issue_offs(rs, off, (uint32_t)kb * step_bytes, st);
     };
+    // The partial last step loads like the others, its rows past the end from
+    // the group's last row; clear() puts zeros over those once they have landed.
     auto issue = [&](int t) __attribute__((always_inline)) {
-        if (t < nk_full) issue_via(rsrc_at(t), 0, t & 3);
-        else if (t < nk) issue_partial(t);
+        if (t < nk_full) {
+            issue_via(rsrc_at(t), 0, t & 3);
+        } else if (t < nk) {
+            const int last = K - 1 - t * BK;
+            uint32_t o[L];
+#pragma unroll
+            for (int i = 0; i < L; ++i) {
+                const int r = 2 * (4 * wj + i) + (lane >> 5);
+                o[i] = off[i] - (uint32_t)max(r - last, 0) * (uint32_t)W * 2u;
+            }
+            issue_offs(rsrc_at(t), o, 0, t & 3);
+        }
+    };
+    auto clear = [&](int t) __attribute__((always_inline)) {
+        LDS_AS uint8_t* dst = (G == 0 ? stage_a(t & 3) : stage_b(t & 3)) + wj * 4096;
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+            if (t * BK + 2 * (4 * wj + i) + (lane >> 5) >= K)
+                *(LDS_AS v4u*)(dst + i * 1024 + lane * 16) = v4u{0u, 0u, 0u, 0u};
     };
 
     // ---- operands: transpose reads of rows 16 u + 8 h + 4 q + lane16 / 4,
@@ -177,8 +197,6 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 
     // One step: MEM (this group's operand reads, loads three steps ahead, wait
     // for step t + 1's), barrier, MMA, barrier; the other group is one phase off.
-    // A step past the last full one was staged with ordinary LDS stores, whose
-    // wait (and the wait for everything older) is the full one.
     __amdgpu_buffer_rsrc_t rs_blk;
     auto step = [&](int t, int tmod, bool steady) __attribute__((always_inline)) {
         const int st = steady ? tmod : t & 3;
@@ -188,11 +206,18 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
         } else {
             issue(t + 3);
-            // loads of steps t + 2 and t + 3 may stay in flight while they are direct ones
-            const int younger = t + 3 < nk_full ? 2 : (t + 2 < nk_full && t + 3 >= nk ? 1 : 0);
-            if (younger == 2) __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
-            else if (younger == 1) __builtin_amdgcn_s_waitcnt(waitcnt_imm(L, 0));
-            else __builtin_amdgcn_s_waitcnt(0);
+            // step t + 1 must have landed; steps t + 2 and t + 3, where there are any, may be in flight
+            if (t + 1 == nk_full && nk > nk_full) {
+                __builtin_amdgcn_s_waitcnt(0);
+                clear(t + 1);
+                __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            } else if (t + 3 < nk) {
+                __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
+            } else if (t + 2 < nk) {
+                __builtin_amdgcn_s_waitcnt(waitcnt_imm(L, 0));
+            } else {
+                __builtin_amdgcn_s_waitcnt(0);
+            }
         }
         asm volatile("s_barrier" ::: "memory");
 #pragma unroll
@@ -221,9 +246,16 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     if (nk > 0) {
 #pragma unroll
         for (int t = 0; t < 3; ++t) issue(t);
-        // step 0 landed: steps 1 and 2 may stay in flight if all three are direct loads
-        if (nk_full >= 3) __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
-        else __builtin_amdgcn_s_waitcnt(0);
+        // step 0 must have landed; steps 1 and 2 may be in flight
+        if (nk >= 3) {
+            __builtin_amdgcn_s_waitcnt(waitcnt_imm(2 * L, 0));
+        } else {
+            __builtin_amdgcn_s_waitcnt(0);
+            if (nk_full == 0) {
+                clear(0);
+                __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+            }
+        }
         asm volatile("s_barrier" ::: "memory");
         if (G == 1) asm volatile("s_barrier" ::: "memory");
         int t = 0;
@@ -242,31 +274,55 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // ---- store: block (i, j), value 4 q + e: row 128 G + 32 i + lr, column
     // 64 wj + 32 j + 8 q + 4 h + e ----
     const int64_t base = (int64_t)w.group * M * N;
+    if (!vec_out) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = m0 + 128 * G + 32 * i + lr;
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int col = n0 + 64 * wj + 32 * j + 8 * q + 4 * h;
-                if (row >= M || col >= N) continue;
-                const int64_t at = base + (int64_t)row * N + col;
-                if (vec_out) {   // N is a multiple of 8: four columns are in or out together
+                for (int x = 0; x < 16; ++x) {
+                    const int row = m0 + 128 * G + 32 * i + lr, col = n0 + 64 * wj + 32 * j + 8 * (x >> 2) + 4 * h + (x & 3);
+                    if (row < M && col < N) tile::store_one<OUT>(C, base + (int64_t)row * N + col, acc[i][j][x], 0);
+                }
+        return;
+    }
+    // Through LDS (a wave's own stage array, free after the last barrier), so
+    // that a store writes whole lines of C's rows: 16-byte chunk c of row r sits
+    // at slot c ^ (r % chunks of a row). FP32 in two halves of 64 rows.
+    constexpr int ES = OUT == OUT_F32 ? 4 : 2, RB = 64 * ES, CH = RB / 16, HALVES = OUT == OUT_F32 ? 2 : 1;
+    constexpr int ROWS = 128 / HALVES;
+    LDS_AS uint8_t* ep = wave < 4 ? stage_a(wave) : stage_b(wave - 4);
+    auto swz = [](int r) __attribute__((always_inline)) -> int { return ES == 4 ? r & 15 : (r >> 1) & 7; };
+    uint8_t* Cb = reinterpret_cast<uint8_t*>(C) + base * ES;
+#pragma unroll
+    for (int half = 0; half < HALVES; ++half) {
+#pragma unroll
+        for (int ii = 0; ii < 4 / HALVES; ++ii)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int i = half * (4 / HALVES) + ii, r = 32 * ii + lr;
+                    const int cb = (32 * j + 8 * q + 4 * h) * ES;
+                    LDS_AS uint8_t* p = ep + r * RB + ((((cb >> 4) ^ swz(r)) << 4) | (cb & 15));
                     if constexpr (OUT == OUT_F32) {
-                        *reinterpret_cast<v4f*>(reinterpret_cast<float*>(C) + at) =
+                        *(LDS_AS v4f*)p =
                             v4f{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
                     } else {
                         typedef _Float16 v4hh __attribute__((ext_vector_type(4)));
-                        *reinterpret_cast<v4hh*>(reinterpret_cast<_Float16*>(C) + at) =
-                            v4hh{(_Float16)acc[i][j][4 * q], (_Float16)acc[i][j][4 * q + 1],
-                                 (_Float16)acc[i][j][4 * q + 2], (_Float16)acc[i][j][4 * q + 3]};
+                        const v4hh hv = {(_Float16)acc[i][j][4 * q], (_Float16)acc[i][j][4 * q + 1],
+                                         (_Float16)acc[i][j][4 * q + 2], (_Float16)acc[i][j][4 * q + 3]};
+                        *(LDS_AS v2i*)p = __builtin_bit_cast(v2i, hv);
                     }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) tile::store_one<OUT>(C, at + e, acc[i][j][4 * q + e], 0);
                 }
-            }
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(63, 0));
+#pragma unroll
+        for (int p = 0; p < ROWS * CH / 64; ++p) {
+            const int r = p * (64 / CH) + lane / CH, seg = lane % CH;
+            const v4i v = *(const LDS_AS v4i*)(ep + r * RB + 16 * (seg ^ swz(r)));
+            const int row = m0 + 128 * G + half * ROWS + r, col = n0 + 64 * wj + seg * (16 / ES);
+            if (row < M && col < N) *reinterpret_cast<v4i*>(Cb + ((int64_t)row * N + col) * ES) = v;
+        }
     }
 }
 
