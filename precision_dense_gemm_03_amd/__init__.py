@@ -802,23 +802,26 @@ def amax_quantize_fp8_pair_bt(xa, xb, fmt=FMT_E4M3, pow2=False, amax=None, scale
 # ------------------------------------ products whose weight depends on the row
 
 def _need(t, dtype, shape, what):
-    """Checks an argument's type and shape (None in shape: any size)."""
-    if t.dtype is dtype and t.shape == shape:   # the common case, one comparison
+    """Checks an argument's type and shape (an int in place of the shape: that many dimensions, of any size)."""
+    if t.dtype is dtype and (t.dim() if shape.__class__ is int else t.shape) == shape:
         return
     if t.dtype != dtype:
         raise ValueError(f"{what} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and w != h for w, h in zip(shape, t.shape)):
-        raise ValueError(f"{what} must have shape {tuple('any' if w is None else w for w in shape)}, "
-                         f"not {tuple(t.shape)}")
+    raise ValueError(f"{what} must have {shape} dimensions, not shape {tuple(t.shape)}" if isinstance(shape, int) else
+                     f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
-def _scratch(nbytes, device, stream):
-    """Workspace of one call, kept by the allocator until the call's stream is past it."""
+def _new(shape, dtype, device, stream, zero=False):
+    """An output or workspace of a call on `stream`: allocated (and cleared) on that stream, so that neither memory
+    another stream is still using nor a clear on another stream meets the call."""
     torch = _torch()
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if stream is not None and nbytes:
-        ws.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return ws
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return make(shape, dtype=dtype, device=device)
 
 
 def _grouped_dims(A, B, offsets, C, bt):
@@ -927,7 +930,7 @@ def _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream):
     _need(adapter, torch.int32, (rows,), "adapter")
     _need(lscale, torch.float32, (adapters,), "lscale")
     if workspace is None:
-        workspace = _scratch(lora_workspace_size(rows, rank), X.device, stream)
+        workspace = _new(lora_workspace_size(rows, rank), torch.uint8, X.device, stream)
     return rows, K, rank, adapters, workspace
 
 
@@ -977,7 +980,7 @@ def moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=N
     token[tokens * topk]). Equal logits go to the lower index; -inf and NaN are never chosen (expert and row -1,
     weight 0). renorm: weights sum to 1 over the chosen experts, else they are the softmax over all."""
     torch = _torch()
-    _need(logits, torch.float32, (None, None), "logits")
+    _need(logits, torch.float32, 2, "logits")
     T, E = logits.shape
     topk = int(topk)
     dev = logits.device
@@ -986,7 +989,7 @@ def moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=N
 
     def out(t, dtype, shape, what):
         if t is None:
-            return torch.empty(shape, dtype=dtype, device=dev)
+            return _new(shape, dtype, dev, stream)
         _need(t, dtype, shape, what)
         return t
 
@@ -997,7 +1000,7 @@ def moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=N
     token = out(token, torch.int32, (T * topk,), "token")
     if workspace is None:
         n = moe_route_workspace_size(T, E)
-        workspace = _scratch(n, dev, stream) if n else None
+        workspace = _new(n, torch.uint8, dev, stream) if n else None
     _check(lib().moe_route_f32(_ptr(logits), T, E, topk, 1 if renorm else 0, _ptr(expert), _ptr(weight),
                                _ptr(offsets), _ptr(row), _ptr(token), *_ws_args(workspace), _stream_handle(stream)),
            "moe_route_f32")
@@ -1007,14 +1010,15 @@ def moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=N
 def moe_route_backward_f32(logits, expert, weight, dweight, renorm=True, dlogits=None, stream=None):
     """dlogits[tokens, experts] of moe_route_f32's weights, from dweight[tokens, topk]."""
     torch = _torch()
-    _need(logits, torch.float32, (None, None), "logits")
+    _need(logits, torch.float32, 2, "logits")
     T, E = logits.shape
-    _need(expert, torch.int32, (T, None), "expert")
+    _need(expert, torch.int32, 2, "expert")
     K = expert.shape[1]
+    _need(expert, torch.int32, (T, K), "expert")
     _need(weight, torch.float32, (T, K), "weight")
     _need(dweight, torch.float32, (T, K), "dweight")
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+        dlogits = _new((T, E), torch.float32, logits.device, stream)
     _need(dlogits, torch.float32, (T, E), "dlogits")
     _check(lib().moe_route_backward_f32(_ptr(logits), _ptr(expert), _ptr(weight), _ptr(dweight), T, E, K,
                                         1 if renorm else 0, _ptr(dlogits), _stream_handle(stream)),
@@ -1028,10 +1032,10 @@ def moe_gather(x, token, y=None, stream=None):
     torch = _torch()
     if x.dim() != 2:
         raise ValueError("x must be [tokens, width]")
-    _need(token, torch.int32, (None,), "token")
+    _need(token, torch.int32, 1, "token")
     rows = token.shape[0]
     if y is None:
-        y = torch.empty((rows, x.shape[1]), dtype=x.dtype, device=x.device)
+        y = _new((rows, x.shape[1]), x.dtype, x.device, stream)
     _need(y, x.dtype, (rows, x.shape[1]), "y")
     _check(lib().moe_gather(_ptr(x), _ptr(token), _ptr(y), x.shape[0], rows, x.shape[1], x.element_size(),
                             _stream_handle(stream)), "moe_gather")
@@ -1055,12 +1059,12 @@ def moe_combine(z, row, weight, y=None, stream=None):
     zt = _float_dtype(z, "z")
     if z.dim() != 2:
         raise ValueError("z must be [rows, width]")
-    _need(row, torch.int32, (None, None), "row")
+    _need(row, torch.int32, 2, "row")
     T, K = row.shape
     if weight is not None:
         _need(weight, torch.float32, (T, K), "weight")
     if y is None:
-        y = torch.empty((T, z.shape[1]), dtype=z.dtype, device=z.device)
+        y = _new((T, z.shape[1]), z.dtype, z.device, stream)
     yt = _float_dtype(y, "y")
     _need(y, y.dtype, (T, z.shape[1]), "y")
     _check(lib().moe_combine(_ptr(z), zt, _ptr(row), _ptr(weight), _ptr(y), yt, T, K, z.shape[0], z.shape[1],
@@ -1074,16 +1078,16 @@ def moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None)
     zeros."""
     torch = _torch()
     dt = _float_dtype(z, "z")
-    _need(row, torch.int32, (None, None), "row")
+    _need(row, torch.int32, 2, "row")
     T, K = row.shape
     _need(weight, torch.float32, (T, K), "weight")
-    _need(z, z.dtype, (None, None), "z")
+    _need(z, z.dtype, 2, "z")
     _need(dy, z.dtype, (T, z.shape[1]), "dy")
     if dZ is None:
-        dZ = torch.zeros_like(z)
+        dZ = _new(tuple(z.shape), z.dtype, z.device, stream, zero=True)
     _need(dZ, z.dtype, tuple(z.shape), "dZ")
     if dweight is None:
-        dweight = torch.empty((T, K), dtype=torch.float32, device=z.device)
+        dweight = _new((T, K), torch.float32, z.device, stream)
     _need(dweight, torch.float32, (T, K), "dweight")
     _check(lib().moe_combine_backward(_ptr(dy), _ptr(z), dt, _ptr(row), _ptr(weight), _ptr(dZ), _ptr(dweight), T, K,
                                       z.shape[0], z.shape[1], _stream_handle(stream)), "moe_combine_backward")
