@@ -70,7 +70,9 @@ int grouped_common(int kind, const void* A, int fmt_a, const void* B, int fmt_b,
     return run_grouped(kind, a);
 }
 
-int64_t lora_low_bytes(int64_t rows, int64_t rank) { return rows * ((rank + 7) / 8 * 8) * 4; }
+int64_t lora_low_bytes(int64_t rows, int64_t rank) {
+    return lora_most_slices(rows, rank) * rows * ((rank + 7) / 8 * 8) * 4;
+}
 
 int lora_common(int kind, const void* A, int fmt_a, const void* Bt, int fmt_b, const float* sA, const float* sB,
                 const void* X, const void* LA, const void* LB, const int32_t* adapter, const float* lscale, void* C,
@@ -83,7 +85,7 @@ int lora_common(int kind, const void* A, int fmt_a, const void* Bt, int fmt_b, c
     if (!dim_ok(rows) || !dim_ok(N) || !dim_ok(K) || !dim_ok(rank) || !dim_ok(adapters)) return GEMM_ERR_DIM;
     if (rank > kMaxDim - 7) return GEMM_ERR_DIM;
     if (!bytes_ok(rows, K, 2) || !bytes_ok(K, N, es) || !bytes_ok(rows, N, os) || !bytes3_ok(rank, K, adapters, 2) ||
-        !bytes3_ok(rank, N, adapters, 2) || !bytes_ok(rows, rank + 7, 4))
+        !bytes3_ok(rank, N, adapters, 2) || !bytes_ok(rows, rank + 7, 32))
         return GEMM_ERR_DIM;
     if (rows == 0 || N == 0) return GEMM_OK;
     if (!C) return GEMM_ERR_NULL;
@@ -186,7 +188,7 @@ int gemm_f16_grouped_wgrad(const void* A, const void* B, const int32_t* offsets,
 }
 
 int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank) {
-    if (!dim_ok(rows) || !dim_ok(rank) || rank > kMaxDim - 7 || !bytes_ok(rows, rank + 7, 4)) return GEMM_ERR_DIM;
+    if (!dim_ok(rows) || !dim_ok(rank) || rank > kMaxDim - 7 || !bytes_ok(rows, rank + 7, 32)) return GEMM_ERR_DIM;
     return lora_low_bytes(rows, rank);
 }
 

@@ -311,12 +311,14 @@ struct ExtPiece<Ext, true> {
 // One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N.
 // The ring: stage st at ring + st * STAGE. Every read of it is an asm group
 // (device_common.h), so the compiler does not need to tell stages apart. red:
-// partial sums of wave groups 1 .. KW-1 (RED_SLOTS of them).
+// partial sums of wave groups 1 .. KW-1 (RED_SLOTS of them). pitch: elements
+// from one row of A, and of Bt, to the next (0: K).
 template <int ES, int BM, int BN, int OUT, int FA, int FB, bool BT, int S_ = 0, bool RAG = false, class Ext = NoExtra>
 __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                           void* __restrict__ C, int M, int N, int K, const float* __restrict__ sA,
                                           const float* __restrict__ sB, const float* __restrict__ sOut, int m0, int n0,
-                                          int eflags, int vec_out, uint8_t* ring, v4f* red, const Ext& ext = Ext{}) {
+                                          int eflags, int vec_out, uint8_t* ring, v4f* red, const Ext& ext = Ext{},
+                                          int pitch = 0) {
     using T = Ring<ES, BM, BN, BT, S_>;
     using Op = typename Op16<ES>::type;
     auto stage = [&](int st) __attribute__((always_inline)) -> LDS_AS uint8_t* {
@@ -329,6 +331,7 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
     // the epilogue's multiplier, loaded now (see epilogue_base_early)
     const bool chan = (eflags & EPI_CHANNEL) != 0;
     const float scale = epilogue_base_early(sA, sB, sOut, OUT == OUT_E4M3, chan);
+    const int P = pitch ? pitch : K;
     const int k0p = nk_full * T::BK;                 // first k of the partial tile (when nk > nk_full)
 
     // ---- this wave's direct loads: 1 KiB load j = wave + 4 i of every stage ----
@@ -352,9 +355,9 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
             const int r = 8 * jj + (lane >> 3);
             const int c = (lane & 7) ^ swz_row(r);
             const int rr = j < T::A_INST ? min(m0 + r, M - 1) - m0 : min(n0 + r, N - 1) - n0;
-            goff[i] = (uint32_t)(rr * K * ES + c * 16);
+            goff[i] = (uint32_t)(rr * P * ES + c * 16);
             dead[i] = k0p + c * T::VE >= K;
-            goffp[i] = dead[i] ? (uint32_t)(rr * K * ES) : goff[i];
+            goffp[i] = dead[i] ? (uint32_t)(rr * P * ES) : goff[i];
         } else {
             const int r = (1024 / T::BNB) * (j - T::A_INST) + lane / T::CPR;
             const int c = (lane % T::CPR) ^ swz_b<ES, T::CPR>(r);
@@ -364,8 +367,8 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
             goffp[i] = dead[i] ? (uint32_t)((K - 1 - k0p) * N * ES + col * ES) : goff[i];
         }
     }
-    const uint8_t* a_src = A + (int64_t)m0 * K * ES;
-    const uint8_t* b_src = BT ? B + (int64_t)n0 * K * ES : B + (int64_t)n0 * ES;
+    const uint8_t* a_src = A + (int64_t)m0 * P * ES;
+    const uint8_t* b_src = BT ? B + (int64_t)n0 * P * ES : B + (int64_t)n0 * ES;
     const int64_t b_step = BT ? (int64_t)T::ROWB : (int64_t)T::BK * N * ES;
 
     auto issue = [&](int kt, int st, bool partial) __attribute__((always_inline)) {

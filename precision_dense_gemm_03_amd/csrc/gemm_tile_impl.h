@@ -219,6 +219,10 @@ __device__ __forceinline__ void store_one(void* C, int64_t idx, float y, int efl
     }
 }
 
+// Tiles that the kernels of unaligned operands (UA) hold in registers ahead of
+// the LDS, by tile rows.
+constexpr int kAhead64 = 2, kAhead128 = 1;
+
 // GES: bytes per element of A and B in global memory. GES == ES except for
 // the exact FP8 mode (ES = 2, GES = 1): FP8 codes are widened to FP16 as they
 // are staged (eflags EPI_A_E5M2 / EPI_B_E5M2 give the operand formats) and
@@ -489,15 +493,110 @@ __device__ __forceinline__ void tile_body(const uint8_t* __restrict__ A, const u
 
     const bool offsets_fit = (int64_t)BM * K * GES < (1ll << 31) &&
                              (BT ? (int64_t)BN * K * GES : (int64_t)BK * N * GES) < (1ll << 31);
-    if (nk > 0) {
+    if constexpr (UA) {
+        // D tiles in registers ahead of the LDS, so that a tile has D times the
+        // work of one to arrive in. Every load goes out without a condition (a
+        // branch around one would make the compiler wait for all of them): past
+        // K and N addresses are clamped into the matrix, and what they bring is
+        // put right on the way to the LDS. There, chunks of A (and of Bt) that K
+        // cuts, the 16 bytes before its end, are shifted down, those past it are
+        // zeros, as are rows of a row-major B past K (its last row); column
+        // chunks of it that N cuts are shifted too. Only operands narrower than
+        // a chunk take the element-wise path.
+        constexpr int D = BM <= 64 ? kAhead64 : kAhead128, U = D < 2 ? 2 : D;   // U: tiles unrolled
+        const bool wide = offsets_fit && K >= T::VE && (BT || N >= T::VE);
+        const int nk_full = klen / BK;
+        const bool cut = !BT && n0 + BN > N && N % T::VE != 0;
+        auto shifted = [](v4u v, int elements) __attribute__((always_inline)) -> v4u {
+            if (elements >= T::VE) return v4u{0u, 0u, 0u, 0u};
+            return __builtin_bit_cast(v4u, __builtin_bit_cast(unsigned __int128, v) >> (8 * GES * elements));
+        };
+        const uint8_t* a_base = A + (int64_t)m0 * K * GES;
+        const uint8_t* b_base = BT ? B + (int64_t)n0 * K * GES : B;
+        uint32_t a_row_at[T::CA], b_row_at[T::CB];   // bytes to this thread's rows (row-major B: unused)
+#pragma unroll
+        for (int i = 0; i < T::CA; ++i) a_row_at[i] = (uint32_t)(min(a_row + i * T::A_RPP, M - 1 - m0) * K * GES);
+#pragma unroll
+        for (int i = 0; i < T::CB; ++i) b_row_at[i] = BT ? (uint32_t)(min(b_row + i * T::B_RPP, N - 1 - n0) * K * GES) : 0u;
+        const int b_col_at = BT ? 0 : max(min(n0 + b_col * T::VE, N - T::VE), 0);
+        v4u qa[D][T::CA], qb[D][T::CB];
+        auto fetch = [&](int kt, int set) __attribute__((always_inline)) {
+            const int k0 = min(kt, nk - 1) * BK;   // past the last tile: that one again, unused
+            const uint32_t ca = (uint32_t)(min(k0 + a_col * T::VE, K - T::VE) * GES);
+#pragma unroll
+            for (int i = 0; i < T::CA; ++i) qa[set][i] = gload(a_base + (a_row_at[i] + ca), a_e5m2);
+            if constexpr (BT) {
+                const uint32_t cb = (uint32_t)(min(k0 + b_col * T::VE, K - T::VE) * GES);
+#pragma unroll
+                for (int i = 0; i < T::CB; ++i) qb[set][i] = gload(b_base + (b_row_at[i] + cb), b_e5m2);
+            } else {
+                const uint8_t* pb = b_base + (int64_t)k0 * N * GES;
+                const int last = K - 1 - k0;
+#pragma unroll
+                for (int i = 0; i < T::CB; ++i)
+                    qb[set][i] = gload(pb + (uint32_t)((min(b_row + i * T::B_RPP, last) * N + b_col_at) * GES), b_e5m2);
+            }
+        };
+        auto put = [&](int kt, int stage, int set) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < T::CA; ++i) ra[i] = qa[set][i];
+#pragma unroll
+            for (int i = 0; i < T::CB; ++i) rb[i] = qb[set][i];
+            if (kt >= nk_full) {
+                const int a_past = max(0, kt * BK + a_col * T::VE + T::VE - K);
+                const int b_past = max(0, kt * BK + b_col * T::VE + T::VE - K);
+#pragma unroll
+                for (int i = 0; i < T::CA; ++i) ra[i] = shifted(ra[i], a_past);
+#pragma unroll
+                for (int i = 0; i < T::CB; ++i) {
+                    if (BT) rb[i] = shifted(rb[i], b_past);
+                    else if (kt * BK + b_row + i * T::B_RPP >= K) rb[i] = v4u{0u, 0u, 0u, 0u};
+                }
+            }
+            if (cut) {
+                const int past = max(0, n0 + b_col * T::VE + T::VE - N);
+#pragma unroll
+                for (int i = 0; i < T::CB; ++i) rb[i] = shifted(rb[i], past);
+            }
+            store_a(stage);
+            store_b(stage);
+        };
+        Op bop[T::KS][T::TN];
+        if (!wide) {
+#pragma unroll 1
+            for (int kt = 0; kt < nk; ++kt) {
+                guarded_to_lds(kt, 0);
+                __syncthreads();
+                read_b(0, bop);
+                mma_tile(0, bop);
+                __syncthreads();
+            }
+        } else if (nk > 0) {
+#pragma unroll
+            for (int u = 0; u < D; ++u) fetch(u, u);
+            put(0, 0, 0);
+            fetch(D, 0);
+            __syncthreads();
+            for (int k0 = 0; k0 < nk; k0 += U) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {   // tile k0 + u, in LDS stage u % 2
+                    if (k0 + u >= nk) break;
+                    read_b(u & 1, bop);
+                    mma_tile(u & 1, bop);
+                    if (k0 + u + 1 >= nk) break;
+                    put(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
+                    fetch(k0 + u + 1 + D, (u + 1) % D);
+                    __syncthreads();
+                }
+            }
+        }
+    } else if (nk > 0) {
         Op bop[T::KS][T::TN];
         // Tile kt+1 is fetched into registers while tile kt is multiplied;
         // the K tail and unaligned operands load each chunk with element
         // guards straight into LDS.
         auto fast = [&](int kt) __attribute__((always_inline)) {
-            // (a column chunk that N cuts cannot be re-read from the last whole one)
-            const bool whole = !UA || BT || N % T::VE == 0 || n0 + BN <= N;
-            return aligned && whole && offsets_fit && (kt + 1) * BK <= klen;
+            return aligned && offsets_fit && (kt + 1) * BK <= klen;
         };
         if (fast(0)) {
             load_a(0);

@@ -23,6 +23,9 @@
 // of every group and tiles that run together share B's columns. A tile takes
 // as long as its group has rows, so up to 64 groups come in the order of their
 // sizes, the largest first, and the short ones level the end.
+#include <cstdlib>
+#include <cstring>
+
 #include "gemm_pp_impl.h"
 #include "gemm_tile_impl.h"
 
@@ -326,90 +329,132 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
 }
 
-using WT = tile::Tile<2, 128, 128, 64, 2, 2, false>;
-
-template <int OUT>
+// TS: tile rows and columns, 128 or 64.
+template <int OUT, int TS>
 __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restrict__ A,
                                                          const _Float16* __restrict__ B, void* __restrict__ C,
                                                          const int32_t* __restrict__ offsets, int groups, int rows,
                                                          int M, int N, int tiles_m, int tiles_n) {
+    using WT = tile::Tile<2, TS, TS, 64, 2, 2, false>;
     constexpr int BK = 64, OP = WT::B_BYTES;   // one operand's stage
+    constexpr int CPR = TS / 8, RPP = 256 / CPR, NC = BK / RPP;   // chunks of a row, rows of a pass, passes
+    constexpr int WS = TS / 2, TB = TS / 32;   // a wave's rows and columns, in blocks of 16
     __shared__ __attribute__((aligned(16))) uint8_t smem_raw[4 * OP];
     LDS_AS uint8_t* smem = (LDS_AS uint8_t*)smem_raw;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
     const WgradTile w = wgrad_tile(blockIdx.x, offsets, groups, rows, tiles_m, tiles_n);
     if (w.group < 0) return;
-    const int grp = w.group, m0 = w.tm * 128, n0 = w.tn * 128, lo = w.lo, hi = w.hi;
+    const int grp = w.group, m0 = w.tm * TS, n0 = w.tn * TS, lo = w.lo, hi = w.hi;
     const int nk = (hi - lo + BK - 1) / BK;
 
-    const int srow = tid >> 4, scol = tid & 15;   // staged chunk: rows srow + 16 i, 16-byte column scol
-    v4u ra[4], rb[4];
-    const bool inner = m0 + 128 <= M && n0 + 128 <= N;
-    auto load = [&](int kt) __attribute__((always_inline)) {
+    const int srow = tid / CPR, scol = tid % CPR;   // staged chunk: rows srow + RPP i, 16-byte column scol
+    constexpr int D = TS == 64 ? 4 : 1, U = D < 2 ? 2 : D;   // steps in registers ahead of the LDS; steps unrolled
+    v4u ra[D][NC], rb[D][NC];
+    // Loads go out without conditions: rows past the group's end are its last
+    // row and column chunks past the operand's end the last whole one (M, N of
+    // at least 8); store() clears the one and shifts the other down.
+    const int ca = m0 + 8 * scol, cb = n0 + 8 * scol, past_a = ca + 8 - M, past_b = cb + 8 - N;
+    const bool cut = (m0 + TS > M && M % 8 != 0) || (n0 + TS > N && N % 8 != 0);
+    const _Float16* src_a = A + (int64_t)lo * M + max(min(ca, M - 8), 0);
+    const _Float16* src_b = B + (int64_t)lo * N + max(min(cb, N - 8), 0);
+    const int last = hi - lo - 1;
+    auto load = [&](int kt, int set) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = lo + kt * BK + srow + 16 * i;
-            const uint8_t* pa = reinterpret_cast<const uint8_t*>(A + (int64_t)r * M);
-            const uint8_t* pb = reinterpret_cast<const uint8_t*>(B + (int64_t)r * N);
-            if (inner && (kt + 1) * BK <= hi - lo) {
-                ra[i] = *reinterpret_cast<const tile::v4u_any*>(pa + 2 * (m0 + 8 * scol));
-                rb[i] = *reinterpret_cast<const tile::v4u_any*>(pb + 2 * (n0 + 8 * scol));
-            } else {
-                ra[i] = tile::load_chunk_any<2>(pa, r < hi, m0 + 8 * scol, M);
-                rb[i] = tile::load_chunk_any<2>(pb, r < hi, n0 + 8 * scol, N);
-            }
+        for (int i = 0; i < NC; ++i) {
+            const int64_t r = min(kt * BK + srow + RPP * i, last);
+            ra[set][i] = *reinterpret_cast<const tile::v4u_any*>(src_a + r * M);
+            rb[set][i] = *reinterpret_cast<const tile::v4u_any*>(src_b + r * N);
         }
     };
-    auto store = [&](int st) __attribute__((always_inline)) {
+    auto shifted = [](v4u v, int elements) __attribute__((always_inline)) -> v4u {
+        if (elements <= 0) return v;
+        if (elements >= 8) return v4u{0u, 0u, 0u, 0u};
+        return __builtin_bit_cast(v4u, __builtin_bit_cast(unsigned __int128, v) >> (16 * elements));
+    };
+    auto store = [&](int kt, int st, int set) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = WT::b_row(srow + 16 * i) + scol * 16;
-            *(LDS_AS v4u*)(smem + 2 * st * OP + at) = ra[i];
-            *(LDS_AS v4u*)(smem + (2 * st + 1) * OP + at) = rb[i];
+        for (int i = 0; i < NC; ++i) {
+            v4u a = ra[set][i], b = rb[set][i];
+            if (cut) {
+                a = shifted(a, past_a);
+                b = shifted(b, past_b);
+            }
+            if (kt * BK + srow + RPP * i > last) a = b = v4u{0u, 0u, 0u, 0u};
+            const int at = WT::b_row(srow + RPP * i) + scol * 16;
+            *(LDS_AS v4u*)(smem + 2 * st * OP + at) = a;
+            *(LDS_AS v4u*)(smem + (2 * st + 1) * OP + at) = b;
+        }
+    };
+    // (M or N below 8) element by element, straight to the LDS
+    auto narrow = [&](int kt) __attribute__((always_inline)) {
+#pragma unroll 1
+        for (int i = 0; i < NC; ++i) {
+            const int r = kt * BK + srow + RPP * i, at = WT::b_row(srow + RPP * i) + scol * 16;
+            const uint8_t* pa = reinterpret_cast<const uint8_t*>(A + (int64_t)(lo + r) * M);
+            const uint8_t* pb = reinterpret_cast<const uint8_t*>(B + (int64_t)(lo + r) * N);
+            *(LDS_AS v4u*)(smem + at) = tile::load_chunk_any<2>(pa, r <= last, ca, M);
+            *(LDS_AS v4u*)(smem + OP + at) = tile::load_chunk_any<2>(pb, r <= last, cb, N);
         }
     };
     const int g = lane >> 4, j16 = lane & 15;
     const int in = WT::b_row(8 * g + (j16 >> 2)) + 8 * (j16 & 3);   // + 2 * column
-    v4f acc[4][4];
+    v4f acc[TB][TB];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < TB; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    if (nk > 0) {
-        load(0);
-        store(0);
-        __syncthreads();
-        for (int kt = 0; kt < nk; ++kt) {
-            if (kt + 1 < nk) load(kt + 1);
-            const LDS_AS uint8_t* as = smem + 2 * (kt & 1) * OP + in + 2 * 64 * wm;
-            const LDS_AS uint8_t* bs = smem + (2 * (kt & 1) + 1) * OP + in + 2 * 64 * wn;
+    auto multiply = [&](int st) __attribute__((always_inline)) {
+        const LDS_AS uint8_t* as = smem + 2 * st * OP + in + 2 * WS * wm;
+        const LDS_AS uint8_t* bs = smem + (2 * st + 1) * OP + in + 2 * WS * wn;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                v8h bo[4];
+        for (int ks = 0; ks < 2; ++ks) {
+            v8h bo[TB];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    bo[j] = tile::Operand<2>::read_b(bs + WT::b_row(32 * ks) + 32 * j, WT::SB);
+            for (int j = 0; j < TB; ++j) bo[j] = tile::Operand<2>::read_b(bs + WT::b_row(32 * ks) + 32 * j, WT::SB);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const v8h ao = tile::Operand<2>::read_b(as + WT::b_row(32 * ks) + 32 * i, WT::SB);
+            for (int i = 0; i < TB; ++i) {
+                const v8h ao = tile::Operand<2>::read_b(as + WT::b_row(32 * ks) + 32 * i, WT::SB);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ao, bo[j], acc[i][j], 0, 0, 0);
-                }
+                for (int j = 0; j < TB; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ao, bo[j], acc[i][j], 0, 0, 0);
             }
-            if (kt + 1 < nk) store((kt + 1) & 1);
+        }
+    };
+    if (M < 8 || N < 8) {
+#pragma unroll 1
+        for (int kt = 0; kt < nk; ++kt) {
+            narrow(kt);
             __syncthreads();
+            multiply(0);
+            __syncthreads();
+        }
+    } else if (nk > 0) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) load(u, u);
+        store(0, 0, 0);
+        load(D, 0);
+        __syncthreads();
+        for (int k0 = 0; k0 < nk; k0 += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {   // step k0 + u, in LDS stage u % 2
+                if (k0 + u >= nk) break;
+                multiply(u & 1);
+                if (k0 + u + 1 >= nk) break;
+                store(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
+                load(k0 + u + 1 + D, (u + 1) % D);
+                __syncthreads();
+            }
         }
     }
     const int64_t base = (int64_t)grp * M * N;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < TB; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < TB; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int row = m0 + 64 * wm + 16 * i + 4 * g + r, col = n0 + 64 * wn + 16 * j + j16;
+                const int row = m0 + WS * wm + 16 * i + 4 * g + r, col = n0 + WS * wn + 16 * j + j16;
                 if (row < M && col < N) tile::store_one<OUT>(C, base + (int64_t)row * N + col, acc[i][j][r], 0);
             }
 }
@@ -421,31 +466,37 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
     // 16-byte pieces of both operands' rows, and 32-bit offsets over 8 steps
     const bool pp_ok = pp::aligned16(a.A) && pp::aligned16(a.B) && a.M % 8 == 0 && a.N % 8 == 0 &&
                        a.M < (1 << 21) && a.N < (1 << 21);
-    const int size = pp_ok ? 256 : 128;
+    int size = pp_ok ? 256 : 128;
+    if (const char* env = std::getenv("LIBGEMM_CONFIG")) {
+        if (pp_ok && std::strcmp(env, "wgrad_pp") == 0) size = 256;
+        if (std::strcmp(env, "wgrad_tile_128") == 0) size = 128;
+        if (std::strcmp(env, "wgrad_tile_64") == 0) size = 64;
+    }
     const int64_t tiles_m = (a.M + size - 1) / size, tiles_n = (a.N + size - 1) / size;
     const int64_t blocks = wgrad_blocks(a.groups, tiles_m, tiles_n);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const int rows = (int)a.K, M = (int)a.M, N = (int)a.N, groups = (int)a.groups;
-    if (pp_ok) {
-        const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
-        const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
-        const int vec_out = pp::aligned16(a.C);
-        if (a.out_dtype == OUT_F32)
-            wgrad_pp_kernel<OUT_F32><<<(unsigned)blocks, 512, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
-                                                                             (int)tiles_m, (int)tiles_n, vec_out);
-        else
-            wgrad_pp_kernel<OUT_F16><<<(unsigned)blocks, 512, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
-                                                                             (int)tiles_m, (int)tiles_n, vec_out);
-        return hipGetLastError();
+    const int rows = (int)a.K, M = (int)a.M, N = (int)a.N, groups = (int)a.groups, vec_out = pp::aligned16(a.C);
+#define LIBGEMM_PP(OUT)                                                                                    \
+    wgrad_pp_kernel<OUT><<<(unsigned)blocks, 512, 0, a.stream>>>((const uint8_t*)a.A, (const uint8_t*)a.B, a.C, \
+                                                                 a.offsets, groups, rows, M, N, (int)tiles_m,   \
+                                                                 (int)tiles_n, vec_out)
+#define LIBGEMM_TILE(OUT, TS)                                                                                       \
+    wgrad_tile_kernel<OUT, TS><<<(unsigned)blocks, 256, 0, a.stream>>>((const _Float16*)a.A, (const _Float16*)a.B, \
+                                                                       a.C, a.offsets, groups, rows, M, N,          \
+                                                                       (int)tiles_m, (int)tiles_n)
+    const bool f32 = a.out_dtype == OUT_F32;
+    if (size == 256) {
+        if (f32) LIBGEMM_PP(OUT_F32);
+        else LIBGEMM_PP(OUT_F16);
+    } else if (size == 128) {
+        if (f32) LIBGEMM_TILE(OUT_F32, 128);
+        else LIBGEMM_TILE(OUT_F16, 128);
+    } else {
+        if (f32) LIBGEMM_TILE(OUT_F32, 64);
+        else LIBGEMM_TILE(OUT_F16, 64);
     }
-    const _Float16* A = reinterpret_cast<const _Float16*>(a.A);
-    const _Float16* B = reinterpret_cast<const _Float16*>(a.B);
-    if (a.out_dtype == OUT_F32)
-        wgrad_tile_kernel<OUT_F32><<<(unsigned)blocks, 256, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
-                                                                           (int)tiles_m, (int)tiles_n);
-    else
-        wgrad_tile_kernel<OUT_F16><<<(unsigned)blocks, 256, 0, a.stream>>>(A, B, a.C, a.offsets, groups, rows, M, N,
-                                                                           (int)tiles_m, (int)tiles_n);
+#undef LIBGEMM_PP
+#undef LIBGEMM_TILE
     return hipGetLastError();
 }
 

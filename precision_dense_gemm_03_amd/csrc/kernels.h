@@ -47,7 +47,8 @@ struct LoraArgs : GemmArgs {
     const int32_t* adapter = nullptr;   // device, M: the row's adapter, none outside [0, adapters)
     const float* lscale = nullptr;      // device, adapters
     int64_t rank = 0, adapters = 0;
-    float* low = nullptr;               // workspace: [M, rank rounded up to 8]
+    float* low = nullptr;               // workspace: slices of [M, rank rounded up to 8]
+    int low_slices = 1;                 // parts of the low-rank values, which the products add up
 };
 
 typedef hipError_t (*GemmLauncher)(const GemmArgs&);
@@ -118,7 +119,12 @@ hipError_t launch_grouped_tile_fp8(const GroupedArgs& a, int bm);
 hipError_t launch_grouped_wgrad(const GroupedArgs& a);
 // low[i, r] = lscale[a_i] <X[i], LA[a_i, r]>, zero for rows without an adapter
 // and from rank on.
+// in a.low_slices parts, each the sum over a slice of K.
 hipError_t launch_lora_low(const LoraArgs& a);
+// Slices that launch_lora_low can use: the most for these rows and rank (what
+// the workspace holds), and those for a call.
+int lora_most_slices(int64_t rows, int64_t rank);
+int lora_low_slices(const LoraArgs& a);
 hipError_t launch_lora(int kind, const LoraArgs& a);
 hipError_t launch_lora_tile_f16(const LoraArgs& a, int bm);
 hipError_t launch_lora_tile_fp8(const LoraArgs& a, int bm);

@@ -16,7 +16,8 @@
 // lines of both and run far ahead: the call is bound by moving X and, for each
 // 16 rows again, LA into the compute units (4096 rows, K 4096, rank 64: 640 KB
 // each). A block's adapters are shared out over kLowParts workgroups, one pass
-// each; an adapter's pass stores its own rows.
+// each; an adapter's pass stores its own rows. Where the blocks leave compute
+// units idle, K is cut into slices, each with its own array of sums.
 //
 // Any alignment (lora_low_kernel): a workgroup takes 16 rows and its 8 waves
 // share out K in tiles of 64, straight from memory to the matrix cores; every
@@ -99,24 +100,27 @@ struct LowStore {
     }
 };
 
-constexpr int kLowParts = 4;
+constexpr int kLowParts = 4, kLowDotRows = 64;
 
 template <int BN>
 __global__ __launch_bounds__(256) void lora_low_ring_kernel(const uint8_t* __restrict__ X,
                                                             const uint8_t* __restrict__ LA,
                                                             const int32_t* __restrict__ adapter,
                                                             const float* __restrict__ lscale, int M, int K, int rank,
-                                                            int rank_p, int adapters, float* __restrict__ low) {
+                                                            int rank_p, int adapters, int parts, int kslice,
+                                                            float* __restrict__ low) {
     using T = ring::Ring<2, 16, BN, true>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
     __shared__ v4f red[T::RED_SLOTS];
     const int lane = threadIdx.x & 63, m0 = blockIdx.x * 16, n0 = blockIdx.y * BN;
+    const int z = blockIdx.z / parts, mypart = blockIdx.z - z * parts, k0 = z * kslice;
+    low += (int64_t)z * M * rank_p;
     int mine = -1;
     if (lane < 16 && m0 + lane < M) {
         mine = adapter[m0 + lane];
         if (mine < 0 || mine >= adapters) mine = -1;
     }
-    if (blockIdx.z == 0) {   // rows without an adapter: zeros
+    if (mypart == 0) {   // rows without an adapter: zeros
         const uint32_t none = (uint32_t)__builtin_amdgcn_ballot_w64(mine < 0);
         for (int i = threadIdx.x; i < 16 * BN; i += 256) {
             const int r = i / BN, c = n0 + i % BN;
@@ -124,14 +128,14 @@ __global__ __launch_bounds__(256) void lora_low_ring_kernel(const uint8_t* __res
         }
     }
     int part = 0;
-    for (uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0); left; part = (part + 1) % kLowParts) {
+    for (uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0); left; part = part + 1 == parts ? 0 : part + 1) {
         const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
         left &= ~(uint32_t)__builtin_amdgcn_ballot_w64(mine == a);
-        if (part != (int)blockIdx.z) continue;
+        if (part != mypart) continue;
         const LowStore store{low, adapter, lscale[a], a, rank, rank_p};
         ring::ring_body<2, 16, BN, OUT_F32, 0, 0, true, 0, true, LowStore>(
-            X, LA + (int64_t)a * rank * K * 2, low, M, rank, K, nullptr, nullptr, nullptr, m0, n0, 0, 0, ring, red,
-            store);
+            X + (int64_t)k0 * 2, LA + ((int64_t)a * rank * K + k0) * 2, low, M, rank, min(kslice, K - k0), nullptr, nullptr,
+            nullptr, m0, n0, 0, 0, ring, red, store, K);
         __syncthreads();
     }
 }
@@ -211,26 +215,52 @@ __global__ __launch_bounds__(64 * kLowWaves) void lora_low_kernel(const _Float16
     }
 }
 
+constexpr int kLowMostSlices = 8, kLowSliceK = 512;
+
+bool low_ring_ok(const LoraArgs& a) {
+    return a.M > kLowDotRows && ring::aligned16(a.X) && ring::aligned16(a.LA) && a.K % 8 == 0 && a.K < (1 << 24);
+}
+
+// K of a slice: whole K tiles of the ring kernel.
+int64_t low_slice_k(int64_t K, int slices) { return ((K + slices - 1) / slices + 63) / 64 * 64; }
+
 }  // namespace
+
+// Two workgroups per compute unit, of at least kLowSliceK of K each.
+int lora_most_slices(int64_t rows, int64_t rank) {
+    if (rows <= kLowDotRows || rank <= 0) return 1;
+    const int64_t blocks = (rows + 15) / 16 * ((rank + 63) / 64), s = 512 / blocks;
+    return s < 1 ? 1 : (s > kLowMostSlices ? kLowMostSlices : (int)s);
+}
+
+int lora_low_slices(const LoraArgs& a) {
+    if (!low_ring_ok(a)) return 1;
+    const int64_t most = lora_most_slices(a.M, a.rank);
+    int64_t s = a.K / kLowSliceK < most ? a.K / kLowSliceK : most;
+    if (s <= 1) return 1;
+    const int64_t per = low_slice_k(a.K, (int)s);
+    return (int)((a.K + per - 1) / per);   // none of them empty
+}
 
 hipError_t launch_lora_low(const LoraArgs& a) {
     const _Float16* X = reinterpret_cast<const _Float16*>(a.X);
     const _Float16* LA = reinterpret_cast<const _Float16*>(a.LA);
     const int rank = (int)a.rank, rank_p = (rank + 7) / 8 * 8;
-    if (a.M <= 64) {
+    if (a.M <= kLowDotRows) {
         const int64_t waves = a.M * rank_p;
         lora_low_dot_kernel<<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(
             X, LA, a.adapter, a.lscale, waves, (int)a.K, rank, rank_p, (int)a.adapters, a.low);
         return hipGetLastError();
     }
     const unsigned blocks = (unsigned)((a.M + 15) / 16);
-    const bool ring_ok = ring::aligned16(a.X) && ring::aligned16(a.LA) && a.K % 8 == 0 && a.K < (1 << 24);
-    if (ring_ok) {
+    if (low_ring_ok(a)) {
         const unsigned parts = (unsigned)(a.adapters < kLowParts ? a.adapters : kLowParts);
+        const unsigned slices = (unsigned)a.low_slices;
+        const int kslice = (int)low_slice_k(a.K, a.low_slices);
 #define LIBGEMM_GO(BN)                                                                                      \
-    lora_low_ring_kernel<BN><<<dim3(blocks, (unsigned)((rank + BN - 1) / BN), parts), 256, 0, a.stream>>>(  \
+    lora_low_ring_kernel<BN><<<dim3(blocks, (unsigned)((rank + BN - 1) / BN), parts * slices), 256, 0, a.stream>>>( \
         (const uint8_t*)a.X, (const uint8_t*)a.LA, a.adapter, a.lscale, (int)a.M, (int)a.K, rank, rank_p,   \
-        (int)a.adapters, a.low)
+        (int)a.adapters, (int)parts, kslice, a.low)
         if (rank <= 16) LIBGEMM_GO(16);
         else if (rank <= 32) LIBGEMM_GO(32);
         else LIBGEMM_GO(64);

@@ -22,11 +22,20 @@ namespace libgemm {
 
 struct LoraExtra {
     static constexpr bool kActive = true, kStores = false;
-    const float* low;         // [rows, rank_p], zero from rank on
+    const float* low;         // slices of [rows, rank_p], zero from rank on
     const int32_t* adapter;   // [rows]
     const _Float16* LB;       // [adapters, N, rank]
     int rank, rank_p;         // rank_p: rank rounded up to a multiple of 8
     int adapters;
+    int slices;               // low is the sum of this many arrays, low_step values apart
+    int64_t low_step;
+
+    // Four of a row's low-rank values, the slices added in order.
+    __device__ __forceinline__ v4f low4(const float* p) const {
+        v4f v = *reinterpret_cast<const v4f*>(p);
+        for (int s = 1; s < slices; ++s) v += *reinterpret_cast<const v4f*>(p + s * low_step);
+        return v;
+    }
 
     __device__ __forceinline__ int adapter_of(int row, int M) const {
         const int a = row < M ? adapter[row] : -1;
@@ -58,7 +67,7 @@ struct LoraExtra {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 v4f t = v4f{0.f, 0.f, 0.f, 0.f};
-                if (r < rank_p) t = *reinterpret_cast<const v4f*>(row + r + 4 * h);
+                if (r < rank_p) t = low4(row + r + 4 * h);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     v[s][4 * h + i] = t[i];
@@ -221,8 +230,8 @@ struct LoraExtra {
 
     __device__ __forceinline__ void fetch(Piece& p, int row, int col, int r0, int N) const {
         const float* lrow = low + (int64_t)row * rank_p + r0;
-        p.l[0] = *reinterpret_cast<const v4f*>(lrow);
-        p.l[1] = *reinterpret_cast<const v4f*>(lrow + 4);
+        p.l[0] = low4(lrow);
+        p.l[1] = low4(lrow + 4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) p.b[e] = lb_chunk(p.adapter, min(col + e, N - 1), r0, N);
     }

@@ -16,10 +16,11 @@ constexpr int64_t kCus = 256;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-bool named(const char* name) {
+// Whether the environment names this kernel (looked up once per call).
+struct Named {
     const char* env = std::getenv("LIBGEMM_CONFIG");
-    return env && std::strcmp(env, name) == 0;
-}
+    bool operator()(const char* name) const { return env && std::strcmp(env, name) == 0; }
+};
 
 // Time in us that a grouped kernel is expected to take; the host knows the rows
 // and the number of groups, not the sizes, so it assumes half a row of tiles
@@ -59,6 +60,7 @@ hipError_t launch_grouped(int kind, const GroupedArgs& a) {
     };
     auto ring = [&] { return f16 ? launch_grouped_ring_f16(a) : launch_grouped_ring_fp8(a); };
     auto tile = [&](int bm) { return f16 ? launch_grouped_tile_f16(a, bm) : launch_grouped_tile_fp8(a, bm); };
+    const Named named;
     if (pp_ok && named("grouped_pp_256")) return pp(256);
     if (pp_ok && named("grouped_pp_128")) return pp(128);
     if (ring_ok && named("grouped_ring")) return ring();
@@ -82,7 +84,9 @@ hipError_t launch_grouped(int kind, const GroupedArgs& a) {
     return tile(a.M >= 64 * a.groups ? 128 : 64);
 }
 
-hipError_t launch_lora(int kind, const LoraArgs& a) {
+hipError_t launch_lora(int kind, const LoraArgs& call) {
+    LoraArgs a = call;
+    a.low_slices = lora_low_slices(a);
     const hipError_t e = launch_lora_low(a);
     if (e != hipSuccess) return e;
     const bool f16 = kind == KIND_F16, mixed = a.fmt_a || a.fmt_b;
@@ -93,6 +97,7 @@ hipError_t launch_lora(int kind, const LoraArgs& a) {
     };
     auto ring = [&] { return f16 ? launch_lora_ring_f16(a) : launch_lora_ring_fp8(a); };
     auto tile = [&](int bm) { return f16 ? launch_lora_tile_f16(a, bm) : launch_lora_tile_fp8(a, bm); };
+    const Named named;
     if (pp_ok && named("lora_pp_256")) return pp(256);
     if (pp_ok && named("lora_pp_192")) return pp(192);
     if (ring_ok && named("lora_ring")) return ring();

@@ -116,7 +116,7 @@ hipError_t launch_lora_pp(const LoraArgs& a) {
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
     const LoraExtra ext{a.low, a.adapter, reinterpret_cast<const _Float16*>(a.LB), (int)a.rank,
-                        (int)((a.rank + 7) / 8 * 8), (int)a.adapters};
+                        (int)((a.rank + 7) / 8 * 8), (int)a.adapters, a.low_slices, a.M * ((a.rank + 7) / 8 * 8)};
     if (a.out_dtype == OUT_F32)
         lora_pp_kernel<ES, OUT_F32, FA, FB, BM><<<grid, 512, 0, a.stream>>>(
             A, B, a.C, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, (int)tiles_m, (int)tiles_n, eflags, vec_out, ext);

@@ -78,7 +78,7 @@ __global__ __launch_bounds__(256) void lora_tile_kernel(const uint8_t* __restric
 
 inline LoraExtra extra_of(const LoraArgs& a) {
     return LoraExtra{a.low, a.adapter, reinterpret_cast<const _Float16*>(a.LB), (int)a.rank,
-                     (int)((a.rank + 7) / 8 * 8), (int)a.adapters};
+                     (int)((a.rank + 7) / 8 * 8), (int)a.adapters, a.low_slices, a.M * ((a.rank + 7) / 8 * 8)};
 }
 
 template <int ES, int BM, int FA, int FB>
