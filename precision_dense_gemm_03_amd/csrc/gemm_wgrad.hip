@@ -6,7 +6,7 @@
 // both reach the matrix cores through LDS transpose reads (ds_read_b64_tr_b16),
 // as row-major B does in the plain products. Rows past the group's end are
 // staged as zeros on both sides (another group's rows may hold NaN); a group
-// without rows gives zeros. Two kernels:
+// without rows gives zeros. Two kernels, in three tile sizes:
 //
 // wgrad_pp_kernel (16-byte aligned operands): the ping-pong kernel's plan
 // (gemm_pp_impl.h) with A staged like its row-major B. 256 x 256 tiles, 8
@@ -14,9 +14,13 @@
 // per step (16 KiB of each operand), four LDS stages per operand, direct
 // buffer->LDS loads three steps ahead (group 0 loads A, group 1 B).
 //
-// wgrad_tile_kernel (operands of any alignment): 128 x 128 tiles, 4 waves of
-// 64 x 64, 64 rows at a time, registers ahead of two LDS stages (the layout
-// and padding of gemm_tile_impl.h's row-major B).
+// wgrad_tile_kernel (operands of any alignment): 128 x 128 or 64 x 64 tiles, 4
+// waves, 64 rows at a time, one (128) or four (64) steps in registers ahead of
+// two LDS stages (the layout and padding of gemm_tile_impl.h's row-major B).
+// A product of few tiles is bound by the steps one tile takes one after
+// another, so the smaller tile wins there: 1819 rows in 23 groups, 304 x 208:
+// 9.5 us with 64, 15.3 with 128, 19.5 ping-pong; 8192 rows in 8 groups, 2048 x
+// 4096 into FP32: ping-pong, 172 us, 0.80 PFLOP/s.
 //
 // Order of the tiles: the column tiles of all groups, counted through, go
 // round the XCDs, each with all its row tiles, so every XCD gets an equal part
@@ -466,7 +470,33 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
     // 16-byte pieces of both operands' rows, and 32-bit offsets over 8 steps
     const bool pp_ok = pp::aligned16(a.A) && pp::aligned16(a.B) && a.M % 8 == 0 && a.N % 8 == 0 &&
                        a.M < (1 << 21) && a.N < (1 << 21);
-    int size = pp_ok ? 256 : 128;
+    // Estimated us, fits to measured times of 90 shapes (choosing by them costs
+    // 2 % over the fastest of each shape; the ping-pong kernel wherever it is
+    // possible 24 %): tiles over compute units, `more` for the uneven end, no
+    // less than `least` for one alone, per_k ns for each of a group's rows, and C
+    // stored at no more than tb TB/s.
+    struct Cost {
+        int size;
+        double per_k, least, more, tb, fixed;
+    };
+    static constexpr Cost costs[] = {{256, 36.8, 0.56, 0.08, 4.8, 9.8},
+                                     {128, 14.8, 1.48, 0.04, 3.2, 6.2},
+                                     {64, 5.4, 1.50, 0.05, 2.2, 5.6}};
+    int size = 0;
+    double least = 0.0;
+    const double live = (double)(a.K < a.groups ? (a.K > 0 ? a.K : 1) : a.groups);
+    for (const Cost& c : costs) {
+        if (c.size == 256 && !pp_ok) continue;
+        const double tiles = (double)a.groups * (double)((a.M + c.size - 1) / c.size) * (double)((a.N + c.size - 1) / c.size);
+        double rounds = tiles / 256.0 + c.more;
+        if (rounds < c.least) rounds = c.least;
+        const double t = rounds * (double)a.K / live * c.per_k * 1e-3 + c.fixed +
+                         (double)a.groups * (double)a.M * (double)a.N * (a.out_dtype == OUT_F32 ? 4.0 : 2.0) / (c.tb * 1e6);
+        if (!size || t < least) {
+            size = c.size;
+            least = t;
+        }
+    }
     if (const char* env = std::getenv("LIBGEMM_CONFIG")) {
         if (pp_ok && std::strcmp(env, "wgrad_pp") == 0) size = 256;
         if (std::strcmp(env, "wgrad_tile_128") == 0) size = 128;

@@ -134,6 +134,24 @@ bool grouped_ring_takes_f16(const GroupedArgs& a);
 bool grouped_ring_takes_fp8(const GroupedArgs& a);
 hipError_t launch_grouped_ring_f16(const GroupedArgs& a);
 hipError_t launch_grouped_ring_fp8(const GroupedArgs& a);
+// The deep ring's tiles for adapters, and the one that the plain product's rule
+// picks: the fewest bytes a compute unit streams (in 128-byte rows of A and B
+// per K tile), ties to the larger tile.
+constexpr int kLoraRingShapes[][2] = {{16, 16}, {16, 32}, {16, 64}, {32, 32}, {32, 64}, {64, 64}};
+inline int lora_ring_shape(int64_t M, int64_t N, int64_t* cost) {
+    int pick = -1, at = 0;
+    for (const auto& c : kLoraRingShapes) {
+        const int64_t tiles = ((M + c[0] - 1) / c[0]) * ((N + c[1] - 1) / c[1]);
+        const int64_t bytes = ((tiles + 255) / 256) * (c[0] + c[1]);
+        if (pick < 0 || bytes < *cost ||
+            (bytes == *cost && c[0] * c[1] > kLoraRingShapes[pick][0] * kLoraRingShapes[pick][1])) {
+            pick = at;
+            *cost = bytes;
+        }
+        ++at;
+    }
+    return pick;
+}
 bool lora_ring_takes_f16(const LoraArgs& a);
 bool lora_ring_takes_fp8(const LoraArgs& a);
 hipError_t launch_lora_ring_f16(const LoraArgs& a);

@@ -22,30 +22,98 @@ struct Named {
     bool operator()(const char* name) const { return env && std::strcmp(env, name) == 0; }
 };
 
-// Time in us that a grouped kernel is expected to take; the host knows the rows
-// and the number of groups, not the sizes, so it assumes half a row of tiles
-// padded in each group that can have a row. A tile costs per_k ns per element
-// of K (half as much again less when a compute unit runs one of two), `slots`
-// run at once, and the weights stream at no more than tb TB/s. Measured on
-// [rows, 2048] x [2048, 2048] in 32 groups of 2 to 256 rows and on 16384 x
-// 12288 x 4096 in 16 groups.
+// Estimated times in us. The constants are fits to measured times of every
+// kernel on 60 to 110 shapes per table, from 1 to 16384 rows, with weights that
+// come from beyond the caches; choosing by them costs 1 to 3 % over choosing
+// the fastest of each shape after the fact (fixed bounds on rows per group
+// cost 5 to 12 %). Terms that are the same for every kernel are left out.
+//
+// Grouped: the host knows the rows and the number of groups, not the sizes,
+// and assumes half a row of tiles padded in each group that can have a row.
+// Tiles over compute units, and `more` for the uneven end, but no less than
+// `least` (one tile alone), take per_k ns each per element of K; the weights
+// stream at no more than tb TB/s.
 struct Cost {
     int bm, bn;
-    int64_t slots;
-    double per_k, tb, fixed;
+    double per_k, least, more, tb, fixed;
 };
 
 double estimate(const Cost& c, const GroupedArgs& a, int64_t es) {
     const double live = (double)(a.groups < a.M ? a.groups : a.M);
     double rows_t = (double)a.M / c.bm + 0.5 * live;
     if (rows_t < live) rows_t = live;
-    const double tiles = rows_t * (double)ceil_div(a.N, c.bn);
-    double rounds = tiles / (double)c.slots;
-    if (rounds < 1.0) rounds = c.slots > kCus && tiles <= (double)kCus ? 0.6 : 1.0;
-    else rounds += 0.3;   // the last round is seldom full
+    double rounds = rows_t * (double)ceil_div(a.N, c.bn) / (double)kCus + c.more;
+    if (rounds < c.least) rounds = c.least;
     const double compute = rounds * (double)a.K * c.per_k * 1e-3;
     const double stream = live * (double)a.N * (double)a.K * (double)es / (c.tb * 1e6);
     return (compute > stream ? compute : stream) + c.fixed;
+}
+
+enum { PP_256, PP_128, RING, TILE_128, TILE_64, N_GROUPED };
+
+// [FP16, FP8][row-major, K-major]. K-major weights that nothing shares stream
+// fastest in the deep ring's whole lines; row-major FP8 comes in 64-byte pieces.
+constexpr Cost kGrouped[2][2][N_GROUPED] = {
+    {{{256, 256, 32.7, 0.21, 0.35, 3.4, 9.0},
+      {128, 256, 28.0, 0.43, 0.04, 3.7, 9.0},
+      {64, 64, 7.9, 0.48, 0.08, 5.9, 5.4},
+      {128, 128, 20.3, 0.60, 0.03, 5.1, 7.7},
+      {64, 64, 5.9, 1.15, 0.64, 4.7, 4.9}},
+     {{256, 256, 14.1, 0.30, 1.04, 2.5, 9.0},
+      {128, 256, 27.6, 0.62, 0.08, 3.6, 7.3},
+      {64, 64, 5.2, 0.62, 0.02, 6.7, 6.0},
+      {128, 128, 11.2, 1.10, 0.03, 4.3, 6.3},
+      {64, 64, 4.6, 1.46, 0.01, 4.7, 4.4}}},
+    {{{256, 256, 12.3, 0.24, 0.57, 5.2, 9.0},
+      {128, 256, 20.1, 0.19, 0.24, 7.5, 9.0},
+      {64, 64, 5.6, 0.31, 0.02, 5.4, 9.0},
+      {128, 128, 9.4, 0.24, 0.53, 4.3, 9.0},
+      {64, 64, 3.9, 0.14, 0.35, 6.6, 6.9}},
+     {{256, 256, 11.5, 0.14, 0.96, 5.5, 9.0},
+      {128, 256, 14.1, 0.13, 0.53, 6.1, 9.0},
+      {64, 64, 2.7, 0.28, 0.09, 7.5, 9.0},
+      {128, 128, 8.6, 0.41, 0.33, 5.8, 9.0},
+      {64, 64, 2.4, 0.16, 0.78, 4.8, 6.9}}}};
+
+// Adapters: the sizes are known. 256-column tiles come in whole rounds; the
+// low-rank term costs `term` us a round and 32 of rank; the deep ring's rounds
+// are the bytes of its chosen tile (ring_cost, 64 x 64: 128) and its term us
+// per million of rows x columns x rank.
+struct LoraCost {
+    int bm, bn;
+    double per_k, least, more, term, fixed;
+};
+
+enum { L_PP_256, L_PP_192, L_RING, L_TILE_128, L_TILE_64, N_LORA };
+
+constexpr LoraCost kLora[2][N_LORA] = {{{256, 256, 30.3, 0, 0, 1.4, 18.0},
+                                        {192, 256, 21.1, 0, 0, 4.0, 18.0},
+                                        {0, 0, 8.3, 0.32, 0, 0.40, 9.9},
+                                        {128, 128, 10.8, 0.21, 1.16, 2.1, 18.0},
+                                        {64, 64, 4.9, 1.49, 0.09, 0.64, 13.0}},
+                                       {{256, 256, 21.8, 0, 0, 0.15, 18.0},
+                                        {192, 256, 16.0, 0, 0, 4.0, 18.0},
+                                        {0, 0, 5.1, 0.20, 0, 0.45, 12.9},
+                                        {128, 128, 8.6, 0.96, 0.01, 4.0, 18.0},
+                                        {64, 64, 3.1, 1.46, 0.48, 0.23, 12.9}}};
+
+double estimate(int which, const LoraCost& c, const LoraArgs& a, int64_t ring_cost) {
+    const double k = (double)a.K * 1e-3;
+    if (which == L_RING) {
+        double rounds = (double)ring_cost / 128.0;
+        if (rounds < c.least) rounds = c.least;
+        return rounds * k * c.per_k + c.fixed + (double)a.M * (double)a.N * (double)a.rank * c.term * 1e-6;
+    }
+    const int64_t tiles = ceil_div(a.M, c.bm) * ceil_div(a.N, c.bn);
+    double rounds;
+    if (c.bn == 256) {
+        rounds = (double)ceil_div(tiles, kCus);
+    } else {
+        rounds = (double)tiles / (double)kCus + c.more;
+        if (rounds < c.least) rounds = c.least;
+    }
+    const double share = tiles > kCus ? (double)tiles / (double)kCus : 1.0;
+    return rounds * k * c.per_k + c.fixed + share * (double)ceil_div(a.rank, 32) * c.term;
 }
 
 }  // namespace
@@ -66,22 +134,24 @@ hipError_t launch_grouped(int kind, const GroupedArgs& a) {
     if (ring_ok && named("grouped_ring")) return ring();
     if (named("grouped_tile_128")) return tile(128);
     if (named("grouped_tile_64")) return tile(64);
-    // The ping-pong kernel's 64-byte pieces of K-major rows stream a weight
-    // that nothing shares at 3.9 TB/s (row-major 5.5), the deep ring's whole
-    // lines at 5.8; row-major FP8 comes in 64-byte pieces there (2.6).
-    const Cost c_pp = f16 ? Cost{256, 256, 256, 26.0, bt ? 3.9 : 5.5, 8.0} : Cost{256, 256, 256, 13.0, bt ? 3.9 : 5.5, 8.0};
-    const Cost c_ring = f16 ? Cost{64, 64, 512, 10.4, bt ? 5.8 : 5.0, 4.0} : Cost{64, 64, 512, 6.3, bt ? 5.8 : 2.6, 4.0};
-    const Cost c_tile = f16 ? Cost{128, 128, 512, 17.7, bt ? 4.2 : 4.6, 4.0} : Cost{128, 128, 512, 12.0, bt ? 4.2 : 2.3, 4.0};
-    const int64_t es = f16 ? 2 : 1;
-    const double t_pp = pp_ok ? estimate(c_pp, a, es) : 1e30;
-    const double t_ring = ring_ok ? estimate(c_ring, a, es) : 1e30;
-    const double t_tile = estimate(c_tile, a, es);
-    // Groups of 96 to 191 rows on average take tiles of 128 rows (dgrad of 32
-    // groups, 5003 x 1416 x 2048: 79 against 88 us with 256; at 64 rows on
-    // average 94 against 79, at 256 134 against 115).
-    if (t_pp <= t_ring && t_pp <= t_tile) return pp(a.M >= 96 * a.groups && a.M < 192 * a.groups ? 128 : 256);
-    if (t_ring <= t_tile) return ring();
-    return tile(a.M >= 64 * a.groups ? 128 : 64);
+    int best = -1;
+    double least = 0.0;
+    for (int i = 0; i < N_GROUPED; ++i) {
+        if ((i == PP_256 || i == PP_128) && (!pp_ok || (i == PP_128 && mixed))) continue;   // (mixed formats: one height)
+        if (i == RING && !ring_ok) continue;
+        const double t = estimate(kGrouped[f16 ? 0 : 1][bt ? 1 : 0][i], a, f16 ? 2 : 1);
+        if (best < 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    switch (best) {
+        case PP_256: return pp(256);
+        case PP_128: return pp(128);
+        case RING: return ring();
+        case TILE_128: return tile(128);
+        default: return tile(64);
+    }
 }
 
 hipError_t launch_lora(int kind, const LoraArgs& call) {
@@ -103,15 +173,27 @@ hipError_t launch_lora(int kind, const LoraArgs& call) {
     if (ring_ok && named("lora_ring")) return ring();
     if (named("lora_tile_128")) return tile(128);
     if (named("lora_tile_64")) return tile(64);
-    // The plain product's rules (selector.cpp): the deep ring up to 256 rows;
-    // 256-column tiles from 3/4 of the compute units, 192 rows high when that
-    // leaves each unit fewer rows; 128 or 64 square below.
-    if (a.M <= 256 && ring_ok) return ring();
-    const int64_t tn = ceil_div(a.N, 256), tiles256 = ceil_div(a.M, 256) * tn, tiles192 = ceil_div(a.M, 192) * tn;
-    const double useful = (double)a.M * (double)a.N;
-    if (pp_ok && tiles256 <= 0x7FFFFFFF && tiles256 >= kCus * 3 / 4 && useful >= 0.75 * 65536.0 * (double)tiles256)
-        return pp(ceil_div(tiles192, kCus) * 192 < ceil_div(tiles256, kCus) * 256 ? 192 : 256);
-    return tile(ceil_div(a.M, 128) * ceil_div(a.N, 128) >= kCus ? 128 : 64);
+    int64_t cost = 0;
+    lora_ring_shape(a.M, a.N, &cost);
+    int best = -1;
+    double least = 0.0;
+    for (int i = 0; i < N_LORA; ++i) {
+        if ((i == L_PP_256 || i == L_PP_192) && !pp_ok) continue;
+        if (i == L_PP_256 && mixed) continue;   // (mixed formats: one height)
+        if (i == L_RING && !ring_ok) continue;
+        const double t = estimate(i, kLora[f16 ? 0 : 1][i], a, cost);
+        if (best < 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    switch (best) {
+        case L_PP_256: return pp(256);
+        case L_PP_192: return pp(192);
+        case L_RING: return ring();
+        case L_TILE_128: return tile(128);
+        default: return tile(64);
+    }
 }
 
 }  // namespace libgemm

@@ -118,31 +118,13 @@ hipError_t launch_lora_ring(const LoraArgs& a) {
     return hipGetLastError();
 }
 
-// The tile sizes of the plain deep-ring kernel, chosen by its rule: the fewest
-// bytes a compute unit streams, ties to the larger tile.
 template <int ES, int FA, int FB>
 hipError_t launch_lora_ring_any(const LoraArgs& a) {
-    struct Shape {
-        int bm, bn;
-        hipError_t (*launch)(const LoraArgs&);
-    };
-    static const Shape shapes[] = {{16, 16, launch_lora_ring<ES, FA, FB, 16, 16>},
-                                   {16, 32, launch_lora_ring<ES, FA, FB, 16, 32>},
-                                   {16, 64, launch_lora_ring<ES, FA, FB, 16, 64>},
-                                   {32, 32, launch_lora_ring<ES, FA, FB, 32, 32>},
-                                   {32, 64, launch_lora_ring<ES, FA, FB, 32, 64>},
-                                   {64, 64, launch_lora_ring<ES, FA, FB, 64, 64>}};
-    const Shape* pick = nullptr;
-    int64_t best = 0;
-    for (const Shape& c : shapes) {
-        const int64_t tiles = ((a.M + c.bm - 1) / c.bm) * ((a.N + c.bn - 1) / c.bn);
-        const int64_t cost = ((tiles + 255) / 256) * (c.bm + c.bn);
-        if (!pick || cost < best || (cost == best && c.bm * c.bn > pick->bm * pick->bn)) {
-            pick = &c;
-            best = cost;
-        }
-    }
-    return pick->launch(a);
+    static hipError_t (*const launch[])(const LoraArgs&) = {
+        launch_lora_ring<ES, FA, FB, 16, 16>, launch_lora_ring<ES, FA, FB, 16, 32>, launch_lora_ring<ES, FA, FB, 16, 64>,
+        launch_lora_ring<ES, FA, FB, 32, 32>, launch_lora_ring<ES, FA, FB, 32, 64>, launch_lora_ring<ES, FA, FB, 64, 64>};
+    int64_t cost = 0;
+    return launch[lora_ring_shape(a.M, a.N, &cost)](a);   // in kLoraRingShapes' order
 }
 
 }  // namespace routed
