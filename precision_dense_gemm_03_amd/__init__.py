@@ -811,6 +811,14 @@ def _need(t, dtype, shape, what):
                      f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
 
 
+def _arg(t, dtype, shape, what):
+    """_need and _ptr in one."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():   # the common case
+        return t.data_ptr()
+    _need(t, dtype, shape, what)
+    return _ptr(t)
+
+
 def _new(shape, dtype, device, stream, zero=False):
     """An output or workspace of a call on `stream`: allocated (and cleared) on that stream, so that neither memory
     another stream is still using nor a clear on another stream meets the call."""
@@ -925,13 +933,11 @@ def _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream):
     if LA.dim() != 3 or LB.dim() != 3:
         raise ValueError("LA[adapters, rank, K] and LB[adapters, N, rank] are needed")
     adapters, rank = LA.shape[0], LA.shape[1]
-    _need(LA, torch.float16, (adapters, rank, K), "LA")
-    _need(LB, torch.float16, (adapters, N, rank), "LB")
-    _need(adapter, torch.int32, (rows,), "adapter")
-    _need(lscale, torch.float32, (adapters,), "lscale")
+    args = (_arg(LA, torch.float16, (adapters, rank, K), "LA"), _arg(LB, torch.float16, (adapters, N, rank), "LB"),
+            _arg(adapter, torch.int32, (rows,), "adapter"), _arg(lscale, torch.float32, (adapters,), "lscale"))
     if workspace is None:
         workspace = _new(lora_workspace_size(rows, rank), torch.uint8, X.device, stream)
-    return rows, K, rank, adapters, workspace
+    return rows, K, rank, adapters, args, workspace
 
 
 def gemm_f16_lora_bt(A, Bt, LA, LB, adapter, lscale, C, workspace=None, stream=None):
@@ -942,9 +948,8 @@ def gemm_f16_lora_bt(A, Bt, LA, LB, adapter, lscale, C, workspace=None, stream=N
     if A.dtype != torch.float16 or Bt.dtype != torch.float16:
         raise ValueError("gemm_f16_lora_bt takes float16 operands")
     M, N, K = _dims_bt(A, Bt, C)
-    rows, K, rank, adapters, ws = _lora_dims(A, N, LA, LB, adapter, lscale, workspace, stream)
-    _check(lib().gemm_f16_lora_bt(_ptr(A), _ptr(Bt), _ptr(LA), _ptr(LB), _ptr(adapter), _ptr(lscale), _ptr(C),
-                                  _out_dtype(C), rows, N, K, rank, adapters, *_ws_args(ws), _stream_handle(stream)),
+    rows, K, rank, adapters, low, ws = _lora_dims(A, N, LA, LB, adapter, lscale, workspace, stream)
+    _check(lib().gemm_f16_lora_bt(_ptr(A), _ptr(Bt), *low, _ptr(C), _out_dtype(C), rows, N, K, rank, adapters, *_ws_args(ws), _stream_handle(stream)),
            "gemm_f16_lora_bt")
     return C
 
@@ -958,9 +963,8 @@ def gemm_fp8_lora_bt(A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C,
     _need(sA, torch.float32, (M,), "sA")
     _need(sB, torch.float32, (N,), "sB")
     _need(X, torch.float16, (M, K), "X")
-    rows, K, rank, adapters, ws = _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream)
-    _check(lib().gemm_fp8_lora_bt(_ptr(A), int(fmt_a), _ptr(Bt), int(fmt_b), _ptr(sA), _ptr(sB), _ptr(X), _ptr(LA),
-                                  _ptr(LB), _ptr(adapter), _ptr(lscale), _ptr(C), _out_dtype(C), rows, N, K, rank,
+    rows, K, rank, adapters, low, ws = _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream)
+    _check(lib().gemm_fp8_lora_bt(_ptr(A), int(fmt_a), _ptr(Bt), int(fmt_b), _ptr(sA), _ptr(sB), _ptr(X), *low, _ptr(C), _out_dtype(C), rows, N, K, rank,
                                   adapters, *_ws_args(ws), _stream_handle(stream)), "gemm_fp8_lora_bt")
     return C
 
@@ -987,23 +991,25 @@ def moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=N
     if topk < 1 or topk > E:
         raise ValueError(f"topk must be between 1 and the {E} experts, not {topk}")
 
-    def out(t, dtype, shape, what):
-        if t is None:
-            return _new(shape, dtype, dev, stream)
-        _need(t, dtype, shape, what)
-        return t
-
-    expert = out(expert, torch.int32, (T, topk), "expert")
-    weight = out(weight, torch.float32, (T, topk), "weight")
-    offsets = out(offsets, torch.int32, (E + 1,), "offsets")
-    row = out(row, torch.int32, (T, topk), "row")
-    token = out(token, torch.int32, (T * topk,), "token")
+    i32, f32 = torch.int32, torch.float32
+    if expert is None:
+        expert = _new((T, topk), i32, dev, stream)
+    if weight is None:
+        weight = _new((T, topk), f32, dev, stream)
+    if offsets is None:
+        offsets = _new((E + 1,), i32, dev, stream)
+    if row is None:
+        row = _new((T, topk), i32, dev, stream)
+    if token is None:
+        token = _new((T * topk,), i32, dev, stream)
+    per = (T, topk)
+    outs = (_arg(expert, i32, per, "expert"), _arg(weight, f32, per, "weight"), _arg(offsets, i32, (E + 1,), "offsets"),
+            _arg(row, i32, per, "row"), _arg(token, i32, (T * topk,), "token"))
     if workspace is None:
         n = moe_route_workspace_size(T, E)
         workspace = _new(n, torch.uint8, dev, stream) if n else None
-    _check(lib().moe_route_f32(_ptr(logits), T, E, topk, 1 if renorm else 0, _ptr(expert), _ptr(weight),
-                               _ptr(offsets), _ptr(row), _ptr(token), *_ws_args(workspace), _stream_handle(stream)),
-           "moe_route_f32")
+    _check(lib().moe_route_f32(_ptr(logits), T, E, topk, 1 if renorm else 0, *outs, *_ws_args(workspace),
+                               _stream_handle(stream)), "moe_route_f32")
     return expert, weight, offsets, row, token
 
 
@@ -1036,8 +1042,9 @@ def moe_gather(x, token, y=None, stream=None):
     rows = token.shape[0]
     if y is None:
         y = _new((rows, x.shape[1]), x.dtype, x.device, stream)
-    _need(y, x.dtype, (rows, x.shape[1]), "y")
-    _check(lib().moe_gather(_ptr(x), _ptr(token), _ptr(y), x.shape[0], rows, x.shape[1], x.element_size(),
+    tokens, width = x.shape
+    py = _arg(y, x.dtype, (rows, width), "y")
+    _check(lib().moe_gather(_ptr(x), _ptr(token), py, tokens, rows, width, x.element_size(),
                             _stream_handle(stream)), "moe_gather")
     return y
 
@@ -1061,13 +1068,13 @@ def moe_combine(z, row, weight, y=None, stream=None):
         raise ValueError("z must be [rows, width]")
     _need(row, torch.int32, 2, "row")
     T, K = row.shape
-    if weight is not None:
-        _need(weight, torch.float32, (T, K), "weight")
+    rows, width = z.shape
+    pw = None if weight is None else _arg(weight, torch.float32, (T, K), "weight")
     if y is None:
-        y = _new((T, z.shape[1]), z.dtype, z.device, stream)
+        y = _new((T, width), z.dtype, z.device, stream)
     yt = _float_dtype(y, "y")
-    _need(y, y.dtype, (T, z.shape[1]), "y")
-    _check(lib().moe_combine(_ptr(z), zt, _ptr(row), _ptr(weight), _ptr(y), yt, T, K, z.shape[0], z.shape[1],
+    py = _arg(y, y.dtype, (T, width), "y")
+    _check(lib().moe_combine(_ptr(z), zt, _ptr(row), pw, py, yt, T, K, rows, width,
                              _stream_handle(stream)), "moe_combine")
     return y
 
@@ -1080,15 +1087,15 @@ def moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None)
     dt = _float_dtype(z, "z")
     _need(row, torch.int32, 2, "row")
     T, K = row.shape
-    _need(weight, torch.float32, (T, K), "weight")
+    pw = _arg(weight, torch.float32, (T, K), "weight")
     _need(z, z.dtype, 2, "z")
-    _need(dy, z.dtype, (T, z.shape[1]), "dy")
+    rows, width = z.shape
+    pdy = _arg(dy, z.dtype, (T, width), "dy")
     if dZ is None:
-        dZ = _new(tuple(z.shape), z.dtype, z.device, stream, zero=True)
-    _need(dZ, z.dtype, tuple(z.shape), "dZ")
+        dZ = _new((rows, width), z.dtype, z.device, stream, zero=True)
     if dweight is None:
         dweight = _new((T, K), torch.float32, z.device, stream)
-    _need(dweight, torch.float32, (T, K), "dweight")
-    _check(lib().moe_combine_backward(_ptr(dy), _ptr(z), dt, _ptr(row), _ptr(weight), _ptr(dZ), _ptr(dweight), T, K,
-                                      z.shape[0], z.shape[1], _stream_handle(stream)), "moe_combine_backward")
+    pdz, pdw = _arg(dZ, z.dtype, (rows, width), "dZ"), _arg(dweight, torch.float32, (T, K), "dweight")
+    _check(lib().moe_combine_backward(pdy, _ptr(z), dt, _ptr(row), pw, pdz, pdw, T, K, rows, width,
+                                      _stream_handle(stream)), "moe_combine_backward")
     return dZ, dweight

@@ -312,8 +312,9 @@ struct ExtPiece<Ext, true> {
 // The ring: stage st at ring + st * STAGE. Every read of it is an asm group
 // (device_common.h), so the compiler does not need to tell stages apart. red:
 // partial sums of wave groups 1 .. KW-1 (RED_SLOTS of them). pitch: elements
-// from one row of A, and of Bt, to the next (0: K).
-template <int ES, int BM, int BN, int OUT, int FA, int FB, bool BT, int S_ = 0, bool RAG = false, class Ext = NoExtra>
+// from one row of A, and of Bt, to the next (0: K). P_: K tiles per barrier (below).
+template <int ES, int BM, int BN, int OUT, int FA, int FB, bool BT, int S_ = 0, bool RAG = false, class Ext = NoExtra,
+          int P_ = 1>
 __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                           void* __restrict__ C, int M, int N, int K, const float* __restrict__ sA,
                                           const float* __restrict__ sB, const float* __restrict__ sOut, int m0, int n0,
@@ -593,6 +594,43 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
     // this wave's loads per stage (MAX_PER_WAVE or one fewer)
     const bool full_share = loads_of<T::INST>(wave) == T::MAX_PER_WAVE;
 
+    if constexpr (P_ > 1) {
+        // P_ K tiles per barrier: wait for the P_ tiles from t on, barrier (which
+        // retires the P_ before them), refill those stages, and each wave group
+        // multiplies its tiles of the P_. A small tile's step is all waiting and
+        // issuing (256 workgroups of 16 x 16 over 4096 of K: 15 us with a
+        // barrier for each of the 64 tiles, of which three waves in four only
+        // pass by), so fewer, larger steps are what makes it faster.
+        static_assert(P_ % T::KW == 0 && T::S % P_ == 0 && T::S >= 2 * P_, "whole steps");
+#pragma unroll
+        for (int p = 0; p < T::S - P_; ++p)
+            if (p < nk) issue(p, p, p >= nk_full);
+        for (int t0 = 0; t0 < nk; t0 += T::S) {
+#pragma unroll
+            for (int u = 0; u < T::S; u += P_) {
+                const int t = t0 + u;
+                if (t >= nk) break;
+                // tiles t + P .. t + S - P - 1, where there are any, may be in flight
+                const int after = max(0, min(T::S - 2 * P_, nk - t - P_));
+                if (full_share) wait_loads<T::MAX_PER_WAVE, T::S - 2 * P_>(after);
+                else wait_loads<(T::MAX_PER_WAVE > 1 ? T::MAX_PER_WAVE - 1 : 1), T::S - 2 * P_>(after);
+                asm volatile("s_barrier" ::: "memory");
+                if (nk > nk_full && t + P_ >= nk) {  // the partial last tile is among them
+                    zero_dead(u + nk_full - t);
+                    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+                    asm volatile("s_barrier" ::: "memory");
+                }
+#pragma unroll
+                for (int p = 0; p < P_; ++p) {
+                    const int nt = t + T::S - P_ + p;
+                    if (nt < nk) issue(nt, (u + T::S - P_ + p) % T::S, nt >= nk_full);
+                }
+#pragma unroll
+                for (int p = 0; p < P_; p += T::KW)
+                    if (t + p + kg < nk) compute(u + p + kg);
+            }
+        }
+    } else {
     // ---- prologue: tiles 0 .. S-2 ----
 #pragma unroll
     for (int p = 0; p < T::S - 1; ++p)
@@ -619,6 +657,7 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
             if (nt < nk) issue(nt, (u + T::S - 1) % T::S, nt >= nk_full);
             if (T::KW == 1 || t % T::KW == kg) compute(u);
         }
+    }
     }
 
     if constexpr (Ext::kActive) {   // scaled here (each group its part), added to, stored as it is

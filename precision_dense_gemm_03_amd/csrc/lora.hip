@@ -11,13 +11,17 @@
 // is shared between rows and a wave takes one (i, r): a dot product over K, both
 // sides read in 16-byte pieces, rows * rank waves.
 //
-// More rows, 16-byte aligned (lora_low_ring_kernel): 16 rows against 16, 32 or
-// 64 of an adapter's rows on the deep-ring kernel, whose direct loads take whole
-// lines of both and run far ahead: the call is bound by moving X and, for each
-// 16 rows again, LA into the compute units (4096 rows, K 4096, rank 64: 640 KB
-// each). A block's adapters are shared out over kLowParts workgroups, one pass
-// each; an adapter's pass stores its own rows. Where the blocks leave compute
-// units idle, K is cut into slices, each with its own array of sums.
+// More rows, 16-byte aligned (lora_low_ring_kernel): 16 rows (from 2048 rows on:
+// 64) against 16, 32 or 64 of an adapter's rows on the deep-ring kernel, whose
+// direct loads take whole lines of both and run far ahead: the call is bound by
+// moving X and, for each block of rows again, LA into the compute units (4096
+// rows, K 4096, rank 64: 640 KB to each unit in blocks of 16, 256 KB of 64). A
+// block's adapters are shared out over kLowParts workgroups, one pass each; an
+// adapter's pass stores its own rows. Where the blocks leave compute units
+// idle, K is cut into slices, each with its own array of sums; every tile of
+// the product then adds them up, so tall blocks use two at most (4096 x 4096 x
+// 4096, rank 64: the two launches take 167 us with one slice, 159 with two or
+// four; 8192 x 4096 x 2048, rank 32: 163, 162 and 169).
 //
 // Any alignment (lora_low_kernel): a workgroup takes 16 rows and its 8 waves
 // share out K in tiles of 64, straight from memory to the matrix cores; every
@@ -100,40 +104,42 @@ struct LowStore {
     }
 };
 
-constexpr int kLowParts = 4, kLowDotRows = 64;
+constexpr int kLowParts = 4, kLowDotRows = 64, kLowTallRows = 2048;
 
-template <int BN>
+template <int BM, int BN>
 __global__ __launch_bounds__(256) void lora_low_ring_kernel(const uint8_t* __restrict__ X,
                                                             const uint8_t* __restrict__ LA,
                                                             const int32_t* __restrict__ adapter,
                                                             const float* __restrict__ lscale, int M, int K, int rank,
                                                             int rank_p, int adapters, int parts, int kslice,
                                                             float* __restrict__ low) {
-    using T = ring::Ring<2, 16, BN, true>;
+    // K tiles per barrier and stages (LDS for two workgroups per compute unit)
+    constexpr int P = BM + BN <= 48 ? 4 : 2, S = BM + BN <= 48 ? 12 : (BM + BN <= 80 ? 6 : 4);
+    using T = ring::Ring<2, BM, BN, true, S>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
     __shared__ v4f red[T::RED_SLOTS];
-    const int lane = threadIdx.x & 63, m0 = blockIdx.x * 16, n0 = blockIdx.y * BN;
+    const int lane = threadIdx.x & 63, m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
     const int z = blockIdx.z / parts, mypart = blockIdx.z - z * parts, k0 = z * kslice;
     low += (int64_t)z * M * rank_p;
     int mine = -1;
-    if (lane < 16 && m0 + lane < M) {
+    if (lane < BM && m0 + lane < M) {
         mine = adapter[m0 + lane];
         if (mine < 0 || mine >= adapters) mine = -1;
     }
     if (mypart == 0) {   // rows without an adapter: zeros
-        const uint32_t none = (uint32_t)__builtin_amdgcn_ballot_w64(mine < 0);
-        for (int i = threadIdx.x; i < 16 * BN; i += 256) {
+        const uint64_t none = __builtin_amdgcn_ballot_w64(mine < 0);
+        for (int i = threadIdx.x; i < BM * BN; i += 256) {
             const int r = i / BN, c = n0 + i % BN;
             if (((none >> r) & 1) && m0 + r < M && c < rank_p) low[(int64_t)(m0 + r) * rank_p + c] = 0.0f;
         }
     }
     int part = 0;
-    for (uint32_t left = (uint32_t)__builtin_amdgcn_ballot_w64(mine >= 0); left; part = part + 1 == parts ? 0 : part + 1) {
-        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-        left &= ~(uint32_t)__builtin_amdgcn_ballot_w64(mine == a);
+    for (uint64_t left = __builtin_amdgcn_ballot_w64(mine >= 0); left; part = part + 1 == parts ? 0 : part + 1) {
+        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(left));
+        left &= ~__builtin_amdgcn_ballot_w64(mine == a);
         if (part != mypart) continue;
         const LowStore store{low, adapter, lscale[a], a, rank, rank_p};
-        ring::ring_body<2, 16, BN, OUT_F32, 0, 0, true, 0, true, LowStore>(
+        ring::ring_body<2, BM, BN, OUT_F32, 0, 0, true, S, true, LowStore, P>(
             X + (int64_t)k0 * 2, LA + ((int64_t)a * rank * K + k0) * 2, low, M, rank, min(kslice, K - k0), nullptr, nullptr,
             nullptr, m0, n0, 0, 0, ring, red, store, K);
         __syncthreads();
@@ -229,8 +235,9 @@ int64_t low_slice_k(int64_t K, int slices) { return ((K + slices - 1) / slices +
 // Two workgroups per compute unit, of at least kLowSliceK of K each.
 int lora_most_slices(int64_t rows, int64_t rank) {
     if (rows <= kLowDotRows || rank <= 0) return 1;
-    const int64_t blocks = (rows + 15) / 16 * ((rank + 63) / 64), s = 512 / blocks;
-    return s < 1 ? 1 : (s > kLowMostSlices ? kLowMostSlices : (int)s);
+    const int64_t height = rows >= kLowTallRows ? 64 : 16, most = rows >= kLowTallRows ? 2 : kLowMostSlices;
+    const int64_t blocks = (rows + height - 1) / height * ((rank + 63) / 64), s = 512 / blocks;
+    return s < 1 ? 1 : (s > most ? (int)most : (int)s);
 }
 
 int lora_low_slices(const LoraArgs& a) {
@@ -257,13 +264,21 @@ hipError_t launch_lora_low(const LoraArgs& a) {
         const unsigned parts = (unsigned)(a.adapters < kLowParts ? a.adapters : kLowParts);
         const unsigned slices = (unsigned)a.low_slices;
         const int kslice = (int)low_slice_k(a.K, a.low_slices);
-#define LIBGEMM_GO(BN)                                                                                      \
-    lora_low_ring_kernel<BN><<<dim3(blocks, (unsigned)((rank + BN - 1) / BN), parts * slices), 256, 0, a.stream>>>( \
-        (const uint8_t*)a.X, (const uint8_t*)a.LA, a.adapter, a.lscale, (int)a.M, (int)a.K, rank, rank_p,   \
-        (int)a.adapters, (int)parts, kslice, a.low)
-        if (rank <= 16) LIBGEMM_GO(16);
-        else if (rank <= 32) LIBGEMM_GO(32);
-        else LIBGEMM_GO(64);
+#define LIBGEMM_GO(BM, BN)                                                                                           \
+    lora_low_ring_kernel<BM, BN><<<dim3((unsigned)((a.M + BM - 1) / BM), (unsigned)((rank + BN - 1) / BN),          \
+                                        parts * slices),                                                            \
+                                   256, 0, a.stream>>>((const uint8_t*)a.X, (const uint8_t*)a.LA, a.adapter, a.lscale, \
+                                                       (int)a.M, (int)a.K, rank, rank_p, (int)a.adapters,           \
+                                                       (int)parts, kslice, a.low)
+        if (a.M >= kLowTallRows) {
+            if (rank <= 16) LIBGEMM_GO(64, 16);
+            else if (rank <= 32) LIBGEMM_GO(64, 32);
+            else LIBGEMM_GO(64, 64);
+        } else {
+            if (rank <= 16) LIBGEMM_GO(16, 16);
+            else if (rank <= 32) LIBGEMM_GO(16, 32);
+            else LIBGEMM_GO(16, 64);
+        }
 #undef LIBGEMM_GO
         return hipGetLastError();
     }

@@ -82,18 +82,30 @@ hipError_t launch_grouped_ring(const GroupedArgs& a) {
     return hipGetLastError();
 }
 
+// The adapters' ring: K tiles per barrier and stages. 16 rows, N = K = 4096,
+// rank 16, cold weight: 14.8 us with 4 tiles of 16 x 16 per barrier and 12
+// stages (8: 14.3, but 64 rows 22.1 against 21.6), 20.6 with one and 8 (any
+// depth up to 32 stages then 20.6 to 25.7). Wider tiles: 128 rows 32.9 us with
+// 2, 36.2 with 4.
+template <int BM, int BN>
+struct LoraRing {
+    static constexpr int P = BM * BN <= 512 ? 4 : 2;
+    static constexpr int FIT = 128 * 1024 / ((BM + BN) * 128), S = (FIT < 12 ? FIT : 12) / P * P;
+};
+
 template <int ES, int BM, int BN, int OUT, int FA, int FB>
 __global__ __launch_bounds__(256) void lora_ring_kernel(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                                         void* __restrict__ C, int M, int N, int K,
                                                         const float* __restrict__ sA, const float* __restrict__ sB,
                                                         int tiles_m, int tiles_n, int eflags, int vec_out,
                                                         LoraExtra ext) {
-    using T = ring::Ring<ES, BM, BN, true>;
+    constexpr int S = LoraRing<BM, BN>::S, P = LoraRing<BM, BN>::P;
+    using T = ring::Ring<ES, BM, BN, true, S>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
     __shared__ v4f red[T::RED_SLOTS];
     int tm, tn;
     tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
-    ring::ring_body<ES, BM, BN, OUT, FA, FB, true, 0, true, LoraExtra>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
+    ring::ring_body<ES, BM, BN, OUT, FA, FB, true, S, true, LoraExtra, P>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                       tn * BN, eflags, vec_out, ring, red, ext);
 }
 
