@@ -11,17 +11,16 @@
 // is shared between rows and a wave takes one (i, r): a dot product over K, both
 // sides read in 16-byte pieces, rows * rank waves.
 //
-// More rows, 16-byte aligned (lora_low_ring_kernel): 16 rows (from 2048 rows on:
-// 64) against 16, 32 or 64 of an adapter's rows on the deep-ring kernel, whose
-// direct loads take whole lines of both and run far ahead: the call is bound by
-// moving X and, for each block of rows again, LA into the compute units (4096
-// rows, K 4096, rank 64: 640 KB to each unit in blocks of 16, 256 KB of 64). A
-// block's adapters are shared out over kLowParts workgroups, one pass each; an
+// More rows, 16-byte aligned (lora_low_ring_kernel): 16 rows against 16, 32 or
+// 64 of an adapter's rows on the deep-ring kernel, whose direct loads take whole
+// lines of both and run far ahead: the call is bound by moving X and, for each
+// 16 rows again, LA into the compute units (4096 rows, K 4096, rank 64: 640 KB
+// each; blocks of 64 rows, which move 256 KB, measured the same). A block's
+// adapters are shared out over kLowParts workgroups, one pass each; an
 // adapter's pass stores its own rows. Where the blocks leave compute units
-// idle, K is cut into slices, each with its own array of sums; every tile of
-// the product then adds them up, so tall blocks use two at most (4096 x 4096 x
-// 4096, rank 64: the two launches take 167 us with one slice, 159 with two or
-// four; 8192 x 4096 x 2048, rank 32: 163, 162 and 169).
+// idle, K is cut into slices, each with its own array of sums, which every
+// tile of the product adds up (4096 x 4096 x 4096, rank 64, two slices: 157 us
+// for both launches, one 167, four in blocks of 64 rows 159).
 //
 // Any alignment (lora_low_kernel): a workgroup takes 16 rows and its 8 waves
 // share out K in tiles of 64, straight from memory to the matrix cores; every
@@ -104,9 +103,9 @@ struct LowStore {
     }
 };
 
-constexpr int kLowParts = 4, kLowDotRows = 64, kLowTallRows = 2048;
+constexpr int kLowParts = 4, kLowDotRows = 64;
 
-template <int BM, int BN>
+template <int BN>
 __global__ __launch_bounds__(256) void lora_low_ring_kernel(const uint8_t* __restrict__ X,
                                                             const uint8_t* __restrict__ LA,
                                                             const int32_t* __restrict__ adapter,
@@ -114,7 +113,7 @@ __global__ __launch_bounds__(256) void lora_low_ring_kernel(const uint8_t* __res
                                                             int rank_p, int adapters, int parts, int kslice,
                                                             float* __restrict__ low) {
     // K tiles per barrier and stages (LDS for two workgroups per compute unit)
-    constexpr int P = BM + BN <= 48 ? 4 : 2, S = BM + BN <= 48 ? 12 : (BM + BN <= 80 ? 6 : 4);
+    constexpr int BM = 16, P = BN == 64 ? 2 : 4, S = BN == 64 ? 6 : 12;
     using T = ring::Ring<2, BM, BN, true, S>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
     __shared__ v4f red[T::RED_SLOTS];
@@ -235,9 +234,8 @@ int64_t low_slice_k(int64_t K, int slices) { return ((K + slices - 1) / slices +
 // Two workgroups per compute unit, of at least kLowSliceK of K each.
 int lora_most_slices(int64_t rows, int64_t rank) {
     if (rows <= kLowDotRows || rank <= 0) return 1;
-    const int64_t height = rows >= kLowTallRows ? 64 : 16, most = rows >= kLowTallRows ? 2 : kLowMostSlices;
-    const int64_t blocks = (rows + height - 1) / height * ((rank + 63) / 64), s = 512 / blocks;
-    return s < 1 ? 1 : (s > most ? (int)most : (int)s);
+    const int64_t blocks = (rows + 15) / 16 * ((rank + 63) / 64), s = 512 / blocks;
+    return s < 1 ? 1 : (s > kLowMostSlices ? kLowMostSlices : (int)s);
 }
 
 int lora_low_slices(const LoraArgs& a) {
@@ -264,21 +262,13 @@ hipError_t launch_lora_low(const LoraArgs& a) {
         const unsigned parts = (unsigned)(a.adapters < kLowParts ? a.adapters : kLowParts);
         const unsigned slices = (unsigned)a.low_slices;
         const int kslice = (int)low_slice_k(a.K, a.low_slices);
-#define LIBGEMM_GO(BM, BN)                                                                                           \
-    lora_low_ring_kernel<BM, BN><<<dim3((unsigned)((a.M + BM - 1) / BM), (unsigned)((rank + BN - 1) / BN),          \
-                                        parts * slices),                                                            \
-                                   256, 0, a.stream>>>((const uint8_t*)a.X, (const uint8_t*)a.LA, a.adapter, a.lscale, \
-                                                       (int)a.M, (int)a.K, rank, rank_p, (int)a.adapters,           \
-                                                       (int)parts, kslice, a.low)
-        if (a.M >= kLowTallRows) {
-            if (rank <= 16) LIBGEMM_GO(64, 16);
-            else if (rank <= 32) LIBGEMM_GO(64, 32);
-            else LIBGEMM_GO(64, 64);
-        } else {
-            if (rank <= 16) LIBGEMM_GO(16, 16);
-            else if (rank <= 32) LIBGEMM_GO(16, 32);
-            else LIBGEMM_GO(16, 64);
-        }
+#define LIBGEMM_GO(BN)                                                                                                \
+    lora_low_ring_kernel<BN><<<dim3(blocks, (unsigned)((rank + BN - 1) / BN), parts * slices), 256, 0, a.stream>>>( \
+        (const uint8_t*)a.X, (const uint8_t*)a.LA, a.adapter, a.lscale, (int)a.M, (int)a.K, rank, rank_p,           \
+        (int)a.adapters, (int)parts, kslice, a.low)
+        if (rank <= 16) LIBGEMM_GO(16);
+        else if (rank <= 32) LIBGEMM_GO(32);
+        else LIBGEMM_GO(64);
 #undef LIBGEMM_GO
         return hipGetLastError();
     }

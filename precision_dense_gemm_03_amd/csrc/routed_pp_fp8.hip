@@ -9,6 +9,8 @@ hipError_t launch_grouped_pp_e4m3(const GroupedArgs& a, int bm) {
     switch (bm) {
         case 256: return a.b_kmajor ? routed::launch_grouped_pp<1, 0, 0, true, 256>(a)
                                     : routed::launch_grouped_pp<1, 0, 0, false, 256>(a);
+        case 192: return a.b_kmajor ? routed::launch_grouped_pp<1, 0, 0, true, 192>(a)
+                                    : routed::launch_grouped_pp<1, 0, 0, false, 192>(a);
         default: return a.b_kmajor ? routed::launch_grouped_pp<1, 0, 0, true, 128>(a)
                                    : routed::launch_grouped_pp<1, 0, 0, false, 128>(a);
     }
