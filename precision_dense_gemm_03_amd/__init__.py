@@ -61,6 +61,7 @@ Functions keep the C names:
     moe_gather(x, token, y=None, stream=None) -> y
     moe_combine(z, row, weight, y=None, stream=None) -> y
     moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None) -> (dZ, dweight)
+Outputs and workspaces that these calls allocate belong to the call's stream.
 The output dtype of a GEMM is taken from C: float32, float16, or 8-bit codes
 (uint8 or torch.float8_e4m3fn: E4M3; torch.float8_e5m2, or uint8 with
 out_fmt=FMT_E5M2: E5M2). FP8 operands are uint8 codes or torch float8 tensors.
@@ -949,8 +950,8 @@ def gemm_f16_lora_bt(A, Bt, LA, LB, adapter, lscale, C, workspace=None, stream=N
         raise ValueError("gemm_f16_lora_bt takes float16 operands")
     M, N, K = _dims_bt(A, Bt, C)
     rows, K, rank, adapters, low, ws = _lora_dims(A, N, LA, LB, adapter, lscale, workspace, stream)
-    _check(lib().gemm_f16_lora_bt(_ptr(A), _ptr(Bt), *low, _ptr(C), _out_dtype(C), rows, N, K, rank, adapters, *_ws_args(ws), _stream_handle(stream)),
-           "gemm_f16_lora_bt")
+    _check(lib().gemm_f16_lora_bt(_ptr(A), _ptr(Bt), *low, _ptr(C), _out_dtype(C), rows, N, K, rank,
+                                  adapters, *_ws_args(ws), _stream_handle(stream)), "gemm_f16_lora_bt")
     return C
 
 
@@ -964,8 +965,8 @@ def gemm_fp8_lora_bt(A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C,
     _need(sB, torch.float32, (N,), "sB")
     _need(X, torch.float16, (M, K), "X")
     rows, K, rank, adapters, low, ws = _lora_dims(X, N, LA, LB, adapter, lscale, workspace, stream)
-    _check(lib().gemm_fp8_lora_bt(_ptr(A), int(fmt_a), _ptr(Bt), int(fmt_b), _ptr(sA), _ptr(sB), _ptr(X), *low, _ptr(C), _out_dtype(C), rows, N, K, rank,
-                                  adapters, *_ws_args(ws), _stream_handle(stream)), "gemm_fp8_lora_bt")
+    _check(lib().gemm_fp8_lora_bt(_ptr(A), int(fmt_a), _ptr(Bt), int(fmt_b), _ptr(sA), _ptr(sB), _ptr(X), *low, _ptr(C),
+                                  _out_dtype(C), rows, N, K, rank, adapters, *_ws_args(ws), _stream_handle(stream)), "gemm_fp8_lora_bt")
     return C
 
 

@@ -220,7 +220,9 @@ __device__ __forceinline__ void store_one(void* C, int64_t idx, float y, int efl
 }
 
 // Tiles that the kernels of unaligned operands (UA) hold in registers ahead of
-// the LDS, by tile rows.
+// the LDS, by tile rows. 64: two (over 240 shapes 0.85 to 0.96 of the time with
+// one; four leave two or three waves per SIMD of four and take 1.03 to 1.14).
+// 128: one (two take all registers of a second workgroup).
 constexpr int kAhead64 = 2, kAhead128 = 1;
 
 // GES: bytes per element of A and B in global memory. GES == ES except for
@@ -583,10 +585,11 @@ __device__ __forceinline__ void tile_body(const uint8_t* __restrict__ A, const u
                     if (k0 + u >= nk) break;
                     read_b(u & 1, bop);
                     mma_tile(u & 1, bop);
-                    if (k0 + u + 1 >= nk) break;
-                    put(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
-                    fetch(k0 + u + 1 + D, (u + 1) % D);
-                    __syncthreads();
+                    if (k0 + u + 1 < nk) {
+                        put(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
+                        fetch(k0 + u + 1 + D, (u + 1) % D);
+                    }
+                    __syncthreads();   // (after the last tile too: the caller may start another on the same LDS)
                 }
             }
         }

@@ -68,10 +68,6 @@ __device__ __forceinline__ void store_values(T* p, const float (&v)[N]) {
     }
 }
 
-// 16384 tokens of 2048 halves to 131072 rows: 144 us, 7.4 TB/s of reads and
-// writes together (each token is read again for each of its 8 experts, from
-// beyond the L2s). Rows picked by ranges of tokens, one range per XCD and L2,
-// measured 272 us: the writes then scatter.
 // The row of this lane, in a scalar register where whole waves share it.
 template <int LPR>
 __device__ __forceinline__ int64_t lane_row() {
@@ -94,6 +90,10 @@ __device__ __forceinline__ void fetch_rows(const int32_t* __restrict__ row, cons
     }
 }
 
+// 16384 tokens of 2048 halves to 131072 rows: 144 us, 7.4 TB/s of reads and
+// writes together (each token is read again for each of its 8 experts, from
+// beyond the L2s). Rows picked by ranges of tokens, one range per XCD and L2,
+// measured 272 us: the writes then scatter.
 template <int LPR>
 __global__ __launch_bounds__(kRowThreads) void moe_gather_kernel(const uint8_t* __restrict__ x,
                                                                  const int32_t* __restrict__ token,
