@@ -68,7 +68,10 @@ int64_t wgrad_blocks(int64_t groups, int64_t tiles_m, int64_t tiles_n) {
     return (groups * tiles_n + 7) / 8 * 8 * tiles_m;
 }
 
-template <int OUT>
+// LINES: C goes past the caches, in whole 128-byte lines. (A parameter of the
+// kernel: of two stores in the branches of a condition the compiler makes one,
+// without the hint.)
+template <int OUT, bool LINES>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void wgrad_pp_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C,
     const int32_t* __restrict__ offsets, int groups, int rows, int M, int N, int tiles_m, int tiles_n, int vec_out) {
@@ -330,7 +333,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             const int row = m0 + 128 * G + half * ROWS + r, col = n0 + 64 * wj + seg * (16 / ES);
             if (row < M && col < N) {
                 v4i* dst = reinterpret_cast<v4i*>(Cb + ((int64_t)row * N + col) * ES);
-                if (vec_out == 2) __builtin_nontemporal_store(v, dst);
+                if constexpr (LINES) __builtin_nontemporal_store(v, dst);
                 else *dst = v;
             }
         }
@@ -510,23 +513,24 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
     const int64_t blocks = wgrad_blocks(a.groups, tiles_m, tiles_n);
     if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
     const int rows = (int)a.K, M = (int)a.M, N = (int)a.N, groups = (int)a.groups;
-    // 2: rows of whole 128-byte lines, which go past the caches (8192 rows, 8
-    // groups, 2048 x 4096 FP32: 173 -> 165 us; lines written in two parts, 18
-    // groups of 2232 x 824: 17.9 -> 31.2)
+    // Whole lines past the caches: 4096 rows, 8 groups, 2048 x 4096 FP16 102 -> 89
+    // us; lines written in two parts, 18 groups of 2232 x 824: 17.9 -> 31.2.
     const bool lines = ((uintptr_t)a.C & 127) == 0 && a.N * (a.out_dtype == OUT_F32 ? 4 : 2) % 128 == 0;
-    const int vec_out = pp::aligned16(a.C) ? (lines ? 2 : 1) : 0;
-#define LIBGEMM_PP(OUT)                                                                                    \
-    wgrad_pp_kernel<OUT><<<(unsigned)blocks, 512, 0, a.stream>>>((const uint8_t*)a.A, (const uint8_t*)a.B, a.C, \
-                                                                 a.offsets, groups, rows, M, N, (int)tiles_m,   \
-                                                                 (int)tiles_n, vec_out)
+    const int vec_out = pp::aligned16(a.C);
+#define LIBGEMM_PP(OUT, LINES)                                                                             \
+    wgrad_pp_kernel<OUT, LINES><<<(unsigned)blocks, 512, 0, a.stream>>>(                                   \
+        (const uint8_t*)a.A, (const uint8_t*)a.B, a.C, a.offsets, groups, rows, M, N, (int)tiles_m,        \
+        (int)tiles_n, vec_out)
 #define LIBGEMM_TILE(OUT, TS)                                                                                       \
     wgrad_tile_kernel<OUT, TS><<<(unsigned)blocks, 256, 0, a.stream>>>((const _Float16*)a.A, (const _Float16*)a.B, \
                                                                        a.C, a.offsets, groups, rows, M, N,          \
                                                                        (int)tiles_m, (int)tiles_n)
     const bool f32 = a.out_dtype == OUT_F32;
     if (size == 256) {
-        if (f32) LIBGEMM_PP(OUT_F32);
-        else LIBGEMM_PP(OUT_F16);
+        if (f32 && lines) LIBGEMM_PP(OUT_F32, true);
+        else if (f32) LIBGEMM_PP(OUT_F32, false);
+        else if (lines) LIBGEMM_PP(OUT_F16, true);
+        else LIBGEMM_PP(OUT_F16, false);
     } else if (size == 128) {
         if (f32) LIBGEMM_TILE(OUT_F32, 128);
         else LIBGEMM_TILE(OUT_F16, 128);
