@@ -198,7 +198,9 @@ struct PpLds {
                         {(LDS_AS uint8_t*)b0, (LDS_AS uint8_t*)b1, (LDS_AS uint8_t*)b2, (LDS_AS uint8_t*)b3}}
 
 // One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N.
-template <int ES, int OUT, int FA, int FB, bool BT, bool EX, int BM, bool RAG = false, class Ext = NoExtra>
+// LINES (FP16 output in whole 128-byte lines): the stores go past the caches.
+template <int ES, int OUT, int FA, int FB, bool BT, bool EX, int BM, bool RAG = false, class Ext = NoExtra,
+          bool LINES = false>
 __device__ __forceinline__ void pp_body(const uint8_t* __restrict__ A, const uint8_t* __restrict__ B,
                                         void* __restrict__ C, int M, int N, int K, const float* __restrict__ sA,
                                         const float* __restrict__ sB, const float* __restrict__ sOut, int m0, int n0,
@@ -781,7 +783,9 @@ __device__ __forceinline__ void pp_body(const uint8_t* __restrict__ A, const uin
         const int r = RPI * p + lane / LPR, seg = lane % LPR;
         const v4i v = *(const LDS_AS v4i*)(ep + r * RB + 16 * (seg ^ esw(r)));
         if (RAG && (m0 + T::MR * G + r >= M || n0 + 64 * wj + seg * (16 / es_out) >= N)) continue;
-        *reinterpret_cast<v4i*>(Cb + ((int64_t)(m0 + T::MR * G + r) * N + n0 + 64 * wj) * es_out + 16 * seg) = v;
+        v4i* dst = reinterpret_cast<v4i*>(Cb + ((int64_t)(m0 + T::MR * G + r) * N + n0 + 64 * wj) * es_out + 16 * seg);
+        if constexpr (LINES) __builtin_nontemporal_store(v, dst);
+        else *dst = v;
     }
 }
 

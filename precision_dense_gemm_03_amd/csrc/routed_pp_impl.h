@@ -17,7 +17,7 @@
 namespace libgemm {
 namespace routed {
 
-template <int ES, int OUT, int FA, int FB, bool BT, int BM, bool TAILS>
+template <int ES, int OUT, int FA, int FB, bool BT, int BM, bool TAILS, bool LINES = false>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void grouped_pp_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C,
     const int32_t* __restrict__ offsets, int groups, int rows, int N, int K, const float* __restrict__ sA,
@@ -37,28 +37,33 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int left = t.end - t.m0;
     if constexpr (TAILS && BM > 64) {
         if (left <= 64) {
-            pp::pp_body<ES, OUT, FA, FB, BT, false, 64, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
+            pp::pp_body<ES, OUT, FA, FB, BT, false, 64, true, pp::NoExtra, LINES>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
                                                               vec_out, lds);
             return;
         }
     }
     if constexpr (TAILS && BM > 128) {
         if (left <= 128) {
-            pp::pp_body<ES, OUT, FA, FB, BT, false, 128, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
+            pp::pp_body<ES, OUT, FA, FB, BT, false, 128, true, pp::NoExtra, LINES>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
                                                                vec_out, lds);
             return;
         }
     }
     if constexpr (TAILS && BM > 192) {
         if (left <= 192) {
-            pp::pp_body<ES, OUT, FA, FB, BT, false, 192, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
+            pp::pp_body<ES, OUT, FA, FB, BT, false, 192, true, pp::NoExtra, LINES>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags,
                                                                vec_out, lds);
             return;
         }
     }
-    pp::pp_body<ES, OUT, FA, FB, BT, false, BM, true>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags, vec_out,
+    pp::pp_body<ES, OUT, FA, FB, BT, false, BM, true, pp::NoExtra, LINES>(A, b, C, t.end, N, K, sA, sb, sOut, t.m0, n0, eflags, vec_out,
                                                       lds);
 }
+
+// FP16 rows of whole 128-byte lines: then the results go past the caches, whose
+// room the operands keep (8192 x 4096 x 4096 in 8 groups, us: FP8 139 -> 125,
+// FP16 280 -> 267).
+inline bool whole_lines(const GemmArgs& a) { return ((uintptr_t)a.C & 127) == 0 && a.N % 64 == 0; }
 
 // What the ping-pong kernel needs (pp_fits), and a grid that can be launched.
 template <int ES>
@@ -77,16 +82,17 @@ hipError_t launch_grouped_pp(const GroupedArgs& a) {
     const int vec_out = pp::aligned16(a.C) && (a.N * out_es) % 16 == 0;
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
-#define LIBGEMM_GO(OUT)                                                                                       \
-    grouped_pp_kernel<ES, OUT, FA, FB, BT, BM, TAILS><<<grid, T::NT, 0, a.stream>>>(                          \
+#define LIBGEMM_GO(OUT, LINES)                                                                                \
+    grouped_pp_kernel<ES, OUT, FA, FB, BT, BM, TAILS, LINES><<<grid, T::NT, 0, a.stream>>>(                          \
         A, B, a.C, a.offsets, (int)a.groups, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, a.sOut, (int)tiles_n,  \
         eflags, vec_out)
     if (a.out_dtype == OUT_F32) {
-        LIBGEMM_GO(OUT_F32);
+        LIBGEMM_GO(OUT_F32, false);
     } else if (a.out_dtype == OUT_F16) {
-        LIBGEMM_GO(OUT_F16);
+        if (whole_lines(a)) LIBGEMM_GO(OUT_F16, true);
+        else LIBGEMM_GO(OUT_F16, false);
     } else if constexpr (ES == 1) {
-        LIBGEMM_GO(OUT_E4M3);
+        LIBGEMM_GO(OUT_E4M3, false);
     } else {
         return hipErrorInvalidValue;
     }
@@ -94,7 +100,7 @@ hipError_t launch_grouped_pp(const GroupedArgs& a) {
     return hipGetLastError();
 }
 
-template <int ES, int OUT, int FA, int FB, int BM>
+template <int ES, int OUT, int FA, int FB, int BM, bool LINES>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void lora_pp_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, void* __restrict__ C, int M, int N, int K,
     const float* __restrict__ sA, const float* __restrict__ sB, int tiles_m, int tiles_n, int eflags, int vec_out,
@@ -103,8 +109,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     LIBGEMM_PP_LDS(T);
     int tm, tn;
     tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
-    pp::pp_body<ES, OUT, FA, FB, true, false, BM, true, LoraExtra>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM, tn * 256,
-                                                                  eflags, vec_out, lds, ext);
+    pp::pp_body<ES, OUT, FA, FB, true, false, BM, true, LoraExtra, LINES>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
+                                                                         tn * 256, eflags, vec_out, lds, ext);
 }
 
 template <int ES, int FA, int FB, int BM>
@@ -117,14 +123,14 @@ hipError_t launch_lora_pp(const LoraArgs& a) {
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
     const LoraExtra ext{a.low, a.adapter, reinterpret_cast<const _Float16*>(a.LB), (int)a.rank,
                         (int)((a.rank + 7) / 8 * 8), (int)a.adapters, a.low_slices, a.M * ((a.rank + 7) / 8 * 8)};
-    if (a.out_dtype == OUT_F32)
-        lora_pp_kernel<ES, OUT_F32, FA, FB, BM><<<grid, 512, 0, a.stream>>>(
-            A, B, a.C, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, (int)tiles_m, (int)tiles_n, eflags, vec_out, ext);
-    else if (a.out_dtype == OUT_F16)
-        lora_pp_kernel<ES, OUT_F16, FA, FB, BM><<<grid, 512, 0, a.stream>>>(
-            A, B, a.C, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, (int)tiles_m, (int)tiles_n, eflags, vec_out, ext);
-    else
-        return hipErrorInvalidValue;
+#define LIBGEMM_GO(OUT, LINES)                                                                                  \
+    lora_pp_kernel<ES, OUT, FA, FB, BM, LINES><<<grid, 512, 0, a.stream>>>(                                     \
+        A, B, a.C, (int)a.M, (int)a.N, (int)a.K, a.sA, a.sB, (int)tiles_m, (int)tiles_n, eflags, vec_out, ext)
+    if (a.out_dtype == OUT_F32) LIBGEMM_GO(OUT_F32, false);
+    else if (a.out_dtype != OUT_F16) return hipErrorInvalidValue;
+    else if (whole_lines(a)) LIBGEMM_GO(OUT_F16, true);
+    else LIBGEMM_GO(OUT_F16, false);
+#undef LIBGEMM_GO
     return hipGetLastError();
 }
 
