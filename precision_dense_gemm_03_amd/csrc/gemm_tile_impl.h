@@ -221,7 +221,7 @@ __device__ __forceinline__ void store_one(void* C, int64_t idx, float y, int efl
 
 // Tiles that the kernels of unaligned operands (UA) hold in registers ahead of
 // the LDS, by tile rows. 64: two (over 240 shapes 0.85 to 0.96 of the time with
-// one; four leave two or three waves per SIMD of four and take 1.03 to 1.14).
+// one; four, which cost occupancy, 1.01 to 1.05 of that with two).
 // 128: one (two take all registers of a second workgroup).
 constexpr int kAhead64 = 2, kAhead128 = 1;
 
