@@ -36,6 +36,9 @@ typedef unsigned long long u64;
 constexpr int kThreads = 1024;
 constexpr int kChunk = 64;      // tokens per mask word
 
+// Chunks of T tokens (in 64 bits: T may be the largest int).
+__host__ __device__ inline int chunks_of(int64_t T) { return (int)((T + kChunk - 1) / kChunk); }
+
 // Total order of the finite and +inf floats as unsigned integers (0: never
 // chosen; -0 counts as +0).
 __device__ __forceinline__ uint32_t order_of(float v) {
@@ -191,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void route_select_kernel(const float* __r
     __shared__ u64 mask[VPL * 16];
     __shared__ int cnt[VPL * 16], base[VPL * 16 + 1], wave_sum[kThreads / 64];
     const int tid = threadIdx.x, l = tid & 15;
-    const int chunks = (T + kChunk - 1) / kChunk;
+    const int chunks = chunks_of(T);
     const int c0 = blockIdx.x * per_block, c1 = min(chunks, c0 + per_block);
     for (int e = tid; e < E; e += kThreads) cnt[e] = 0;
     for (int c = c0; c < c1; ++c) {
@@ -253,7 +256,7 @@ __global__ __launch_bounds__(kThreads) void route_assign_kernel(const int32_t* _
     __syncthreads();
     for (int64_t i = live + (int64_t)blk * kThreads + tid; i < (int64_t)T * K; i += (int64_t)nblk * kThreads)
         token[i] = -1;
-    const int chunks = (T + kChunk - 1) / kChunk;
+    const int chunks = chunks_of(T);
     const int c0 = blk * per_block, c1 = min(chunks, c0 + per_block);
     for (int c = c0; c < c1; ++c) assign_chunk(expert, T, E, K, c, false, mask, base, row, token);
 }
@@ -316,8 +319,6 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
         }
     }
 }
-
-int chunks_of(int64_t T) { return (int)((T + kChunk - 1) / kChunk); }
 
 template <int VPL>
 hipError_t launch_select(const RouteArgs& a, int blocks, int per_block) {
