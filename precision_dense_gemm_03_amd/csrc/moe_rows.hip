@@ -15,6 +15,7 @@
 
 #include "device_common.h"
 #include "moe.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace {
@@ -71,9 +72,9 @@ __device__ __forceinline__ void store_values(T* p, const float (&v)[N]) {
 // The row of this lane, in a scalar register where whole waves share it.
 template <int LPR>
 __device__ __forceinline__ int64_t lane_row() {
-    if constexpr (LPR >= kRowThreads) return blockIdx.x;
+    if constexpr (LPR >= kRowThreads) return wide_block();
     const int sub = threadIdx.x / LPR;
-    return (int64_t)blockIdx.x * (kRowThreads / LPR) + (LPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
+    return wide_block() * (kRowThreads / LPR) + (LPR >= 64 ? __builtin_amdgcn_readfirstlane(sub) : sub);
 }
 
 // Rows j0 .. j0 + KB - 1 of a token: each one's offset in z, -1 where there is
@@ -267,7 +268,7 @@ int lanes_for(int64_t units) {
     return 64;
 }
 
-unsigned blocks_for(int64_t rows, int lpr) { return (unsigned)((rows + kRowThreads / lpr - 1) / (kRowThreads / lpr)); }
+dim3 blocks_for(int64_t rows, int lpr) { return wide_grid((rows + kRowThreads / lpr - 1) / (kRowThreads / lpr)); }
 
 template <typename F>
 hipError_t with_lanes(int lpr, F f) {

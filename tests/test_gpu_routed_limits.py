@@ -52,3 +52,47 @@ def test_route_of_the_most_tokens():
     assert offsets.tolist() == [0, T]
     assert all_equal(expert.view(-1), 0) and all_equal(weight.view(-1), 1.0)
     assert all_equal(row.view(-1), lambda i: i) and all_equal(token, lambda i: i)
+
+
+# more rows than 2^32 threads hold at a workgroup of 256 each (rows of over 128 16-byte units)
+MANY = (1 << 24) + 5
+
+
+def test_gather_of_many_wide_rows():
+    width = 2053
+    say(f"gather to {MANY} rows of {width} bytes")
+    x = torch.randint(0, 256, (7, width), device=DEV, dtype=torch.uint8)
+    token = (torch.arange(MANY, device=DEV) % 8).to(I32)     # 7: no such token
+    y = g.moe_gather(x, token)
+    zero = torch.cat([x, torch.zeros_like(x[:1])])
+    for lo in range(0, MANY, 1 << 21):
+        hi = min(MANY, lo + (1 << 21))
+        want = zero[torch.arange(lo, hi, device=DEV) % 8]
+        assert torch.equal(y[lo:hi], want), lo
+
+
+def test_combine_of_many_wide_rows():
+    """y[t] = z[row[t]]; then its gradient, with rows of z for the last tokens only."""
+    width, rows = 1032, 4096
+    say(f"combine of {MANY} tokens of {width} halves")
+    gn = torch.Generator(device=DEV).manual_seed(1)
+    z = torch.randn((rows, width), generator=gn, device=DEV).half()
+    row = (torch.arange(MANY, device=DEV) % (rows + 1)).to(I32).view(-1, 1)     # `rows`: none
+    y = g.moe_combine(z, row, None)
+    padded = torch.cat([z, torch.zeros_like(z[:1])])
+    step = 1 << 21
+    for lo in range(0, MANY, step):
+        hi = min(MANY, lo + step)
+        assert torch.equal(y[lo:hi], padded[row[lo:hi, 0].long()]), lo
+    # the gradient with dy = y: <z, z> and z in the named rows
+    row.fill_(-1)
+    row[MANY - rows:, 0] = torch.arange(rows, device=DEV).to(I32)
+    weight = torch.ones((MANY, 1), device=DEV)
+    say("and its gradient")
+    dz, dw = g.moe_combine_backward(y, z, row, weight)
+    last = y[MANY - rows:]
+    assert torch.equal(dz, last)
+    assert bool((dw[:MANY - rows] == 0).all())
+    dot = (z.double() * last.double()).sum(1, keepdim=True)
+    size = (z.double() * last.double()).abs().sum(1, keepdim=True)
+    assert bool(((dw[MANY - rows:].double() - dot).abs() <= 1e-5 * size).all())
