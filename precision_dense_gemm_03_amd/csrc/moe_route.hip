@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include "moe.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace {
@@ -272,7 +273,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
                                                              const float* __restrict__ dweight, int T, int E, int K,
                                                              int renorm, float* __restrict__ dlogits) {
     const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t t = wide_block() * 4 + (threadIdx.x >> 6);
     if (t >= T) return;
     const float* lg = logits + t * E;
     int ex = -1;
@@ -365,7 +366,7 @@ hipError_t launch_route_backward(const float* logits, const int32_t* expert, con
                                  const float* dweight, int64_t T, int64_t E, int64_t K, int renorm, float* dlogits,
                                  hipStream_t stream) {
     if (T == 0 || E == 0) return hipSuccess;
-    route_backward_kernel<<<(unsigned)((T + 3) / 4), 256, 0, stream>>>(logits, expert, weight, dweight, (int)T, (int)E,
+    route_backward_kernel<<<wide_grid((T + 3) / 4), 256, 0, stream>>>(logits, expert, weight, dweight, (int)T, (int)E,
                                                                        (int)K, renorm, dlogits);
     return hipGetLastError();
 }

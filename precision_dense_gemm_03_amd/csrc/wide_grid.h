@@ -1,9 +1,9 @@
 // Launches of any number of workgroups. Of a launch of 2^32 threads and more in
 // one direction only their number modulo 2^32 runs, and the launch reports no
 // error; so workgroups beyond 2^22 (2^32 threads are 2^23 of 512) go on in y:
-// workgroup w is x = w % 2^22, y = w / 2^22. The last y may
-// hold more workgroups than were asked for; a kernel ends those by its bounds.
-// 2^22 is a multiple of the 8 XCDs, so w % 8 still names a workgroup's XCD.
+// workgroup w is x = w % 2^22, y = w / 2^22. The last y may hold more
+// workgroups than were asked for; a kernel ends those by its bounds. 2^22 is a
+// multiple of the 8 XCDs, so w % 8 still names a workgroup's XCD.
 #pragma once
 
 #include <hip/hip_runtime.h>

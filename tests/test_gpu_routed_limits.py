@@ -96,3 +96,18 @@ def test_combine_of_many_wide_rows():
     dot = (z.double() * last.double()).sum(1, keepdim=True)
     size = (z.double() * last.double()).abs().sum(1, keepdim=True)
     assert bool(((dw[MANY - rows:].double() - dot).abs() <= 1e-5 * size).all())
+
+
+def test_route_backward_of_many_tokens():
+    """Four tokens to a workgroup of 256: 2^32 threads from 2^26 tokens on. Two experts of weight 1/2 and dweight
+    (t % 4, 0): dlogits (t % 4) / 4 and its negative, exactly."""
+    T = (1 << 26) + 21
+    say(f"route backward of {T} tokens")
+    t = torch.arange(T, device=DEV) % 4
+    logits = torch.zeros((T, 2), device=DEV)
+    expert = torch.tensor([[0, 1]], dtype=I32, device=DEV).repeat(T, 1)
+    weight = torch.full((T, 2), 0.5, device=DEV)
+    dweight = torch.stack([t.float(), torch.zeros_like(t, dtype=F32)], 1)
+    for renorm in (True, False):
+        d = g.moe_route_backward_f32(logits, expert, weight, dweight, renorm=renorm)
+        assert torch.equal(d[:, 0], t.float() / 4) and torch.equal(d[:, 1], -t.float() / 4), renorm
