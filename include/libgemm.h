@@ -335,7 +335,8 @@ int64_t gemm_f16_guarded_workspace_size(int64_t M, int64_t N, int64_t K);
  * offsets[0] or from offsets[groups] on belong to no group. The host never
  * reads offsets, so the calls can be enqueued behind the kernels that write
  * them. Offsets out of order or outside [0, rows] give unspecified results but
- * no access outside the operands. groups is at most 4096. */
+ * no access outside the operands. groups is at most 4096; rows, M, N, K and rank
+ * of the products in this section are at most 2^31 - 65536 (GEMM_ERR_DIM). */
 
 /*
  * gemm_f16_grouped — C[r] = A[r] · B[g(r)] for FP16 operands, FP32

@@ -28,6 +28,11 @@ bool aliased(const Range (&written)[W], const Range (&read)[R]) {
 
 constexpr int64_t kMaxRowGroups = 4096;
 
+// The product kernels count rows, columns and K in 32 bits up to the end of a
+// tile (which starts at any row of a group) or of the steps loaded ahead: less
+// than 2^16 past the size.
+bool size_ok(int64_t d) { return d >= 0 && d <= ((int64_t)1 << 31) - (1 << 16); }
+
 bool fmt_ok(int f) { return f == GEMM_FMT_E4M3 || f == GEMM_FMT_E5M2; }
 
 // a * b * c * es below the byte limit, with a * b below 2^62 first.
@@ -47,7 +52,7 @@ int grouped_common(int kind, const void* A, int fmt_a, const void* B, int fmt_b,
     if (out_dtype < GEMM_OUT_F32 || out_dtype > (kind == KIND_F16 ? GEMM_OUT_F16 : GEMM_OUT_E5M2)) return GEMM_ERR_DTYPE;
     if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b)) return GEMM_ERR_DTYPE;
     const int64_t os = out_size(out_dtype);
-    if (!dim_ok(rows) || !dim_ok(N) || !dim_ok(K) || groups < 0 || groups > kMaxRowGroups) return GEMM_ERR_DIM;
+    if (!size_ok(rows) || !size_ok(N) || !size_ok(K) || groups < 0 || groups > kMaxRowGroups) return GEMM_ERR_DIM;
     if (!bytes_ok(rows, K, es) || !bytes_ok(rows, N, os) || !bytes3_ok(K, N, groups, es)) return GEMM_ERR_DIM;
     if (rows == 0 || N == 0) return GEMM_OK;
     if (!C || !offsets) return GEMM_ERR_NULL;
@@ -82,8 +87,7 @@ int lora_common(int kind, const void* A, int fmt_a, const void* Bt, int fmt_b, c
     if (out_dtype != GEMM_OUT_F32 && out_dtype != GEMM_OUT_F16) return GEMM_ERR_DTYPE;
     if (!fmt_ok(fmt_a) || !fmt_ok(fmt_b)) return GEMM_ERR_DTYPE;
     const int64_t os = out_size(out_dtype);
-    if (!dim_ok(rows) || !dim_ok(N) || !dim_ok(K) || !dim_ok(rank) || !dim_ok(adapters)) return GEMM_ERR_DIM;
-    if (rank > kMaxDim - 7) return GEMM_ERR_DIM;
+    if (!size_ok(rows) || !size_ok(N) || !size_ok(K) || !size_ok(rank) || !dim_ok(adapters)) return GEMM_ERR_DIM;
     if (!bytes_ok(rows, K, 2) || !bytes_ok(K, N, es) || !bytes_ok(rows, N, os) || !bytes3_ok(rank, K, adapters, 2) ||
         !bytes3_ok(rank, N, adapters, 2) || !bytes_ok(rows, rank + 7, 32))
         return GEMM_ERR_DIM;
@@ -171,7 +175,7 @@ int gemm_f16_grouped_wgrad(const void* A, const void* B, const int32_t* offsets,
                            int64_t M, int64_t N, int64_t groups, hipStream_t stream) {
     if (out_dtype != GEMM_OUT_F32 && out_dtype != GEMM_OUT_F16) return GEMM_ERR_DTYPE;
     const int64_t os = out_size(out_dtype);
-    if (!dim_ok(rows) || !dim_ok(M) || !dim_ok(N) || groups < 0 || groups > kMaxRowGroups) return GEMM_ERR_DIM;
+    if (!size_ok(rows) || !size_ok(M) || !size_ok(N) || groups < 0 || groups > kMaxRowGroups) return GEMM_ERR_DIM;
     if (!bytes_ok(rows, M, 2) || !bytes_ok(rows, N, 2) || !bytes3_ok(M, N, groups, os)) return GEMM_ERR_DIM;
     if (M == 0 || N == 0 || groups == 0) return GEMM_OK;
     if (!C || !offsets || (rows > 0 && (!A || !B))) return GEMM_ERR_NULL;
@@ -188,7 +192,7 @@ int gemm_f16_grouped_wgrad(const void* A, const void* B, const int32_t* offsets,
 }
 
 int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank) {
-    if (!dim_ok(rows) || !dim_ok(rank) || rank > kMaxDim - 7 || !bytes_ok(rows, rank + 7, 32)) return GEMM_ERR_DIM;
+    if (!size_ok(rows) || !size_ok(rank) || !bytes_ok(rows, rank + 7, 32)) return GEMM_ERR_DIM;
     return lora_low_bytes(rows, rank);
 }
 

@@ -164,3 +164,33 @@ def test_binding_refusals():
         g.moe_combine(a, ad.reshape(2, 2), torch.ones((2, 1)))
     with pytest.raises(ValueError):
         g.moe_combine_backward(a, a, ad.reshape(2, 2), torch.ones((2, 2)))
+
+
+LARGEST = (1 << 31) - 65536
+
+
+@pytest.mark.parametrize("size", [LARGEST + 1, (1 << 31) - 200, (1 << 31) - 1])
+def test_sizes_whose_last_tile_passes_2_to_31(size):
+    """Row, column and K indices run past the size, to the end of a tile or a step, in 32 bits: refused before any
+    launch."""
+    small = dict(rows=1, N=1, K=1, groups=1, A=1 << 50, B=2 << 50, off=3 << 50, C=4 << 50)
+    for which in ("rows", "N", "K"):
+        assert f16_grouped(**{**small, which: size}) == [DIM] * 2, which
+        fp8 = {**small, which: size, "sA": 5 << 50, "sB": 6 << 50}
+        assert fp8_grouped(False, **fp8) == [DIM] * 2 and fp8_grouped(True, **fp8) == [DIM] * 2, which
+    L = g.lib()
+    for dims in ((size, 1, 1), (1, size, 1), (1, 1, size)):
+        assert L.gemm_f16_grouped_wgrad(1 << 50, 2 << 50, 3 << 50, 4 << 50, 0, *dims, 1, None) == DIM, dims
+    far = dict(rows=1, N=1, K=1, rank=1, adapters=1, wsb=1 << 45, **{n: (i + 1) << 50 for i, n in enumerate(
+        ("A", "B", "sA", "sB", "X", "LA", "LB", "ad", "ls", "C", "ws"))})
+    for which in ("rows", "N", "K", "rank"):
+        for kind in ("f16", "fp8"):
+            assert lora(kind, **{**far, which: size}) == DIM, which
+    assert L.gemm_lora_workspace_size(size, 1) == DIM and L.gemm_lora_workspace_size(1, size) == DIM
+
+
+def test_largest_sizes_are_taken():
+    assert g.lib().gemm_lora_workspace_size(LARGEST, 1) == LARGEST * 8 * 4
+    for which in ("N", "K"):
+        assert f16_grouped(**{**dict(rows=0, N=1, K=1), which: LARGEST}) == [0, 0]
+    assert f16_grouped(rows=LARGEST, N=0) == [0, 0]
