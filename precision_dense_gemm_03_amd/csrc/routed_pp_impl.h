@@ -24,7 +24,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const float* __restrict__ sB, const float* __restrict__ sOut, int tiles_n, int eflags, int vec_out) {
     using T = pp::Pp<ES, BM>;
     LIBGEMM_PP_LDS(T);
-    const RowTile t = find_row_tile<BM>(offsets, groups, rows, blockIdx.x, tiles_n);
+    const RowTile t = find_row_tile<BM>(offsets, groups, rows, (int)wide_block(), tiles_n);
     if (t.m0 >= t.end) return;
     const int n0 = t.tn * T::BN;
     if (t.group < 0) {
@@ -69,14 +69,14 @@ inline bool whole_lines(const GemmArgs& a) { return ((uintptr_t)a.C & 127) == 0 
 template <int ES>
 bool grouped_pp_fits(const GroupedArgs& a) {
     const bool fits = a.b_kmajor ? pp::pp_fits<ES, true, 256>(a) : pp::pp_fits<ES, false, 256>(a);
-    return fits && most_workgroups(a.M, a.groups, 128, (a.N + 255) / 256) <= 0x7FFFFFFF;
+    return fits && most_workgroups(a.M, a.groups, 128, (a.N + 255) / 256) <= kMostWorkgroups;
 }
 
 template <int ES, int FA, int FB, bool BT, int BM, bool TAILS = true>
 hipError_t launch_grouped_pp(const GroupedArgs& a) {
     using T = pp::Pp<ES, BM>;
     const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
-    const unsigned grid = (unsigned)most_workgroups(a.M, a.groups, BM, tiles_n);
+    const dim3 grid = wide_grid(most_workgroups(a.M, a.groups, BM, tiles_n));
     const int eflags = (a.out_dtype == OUT_E5M2 ? EPI_E5M2 : 0) | (a.channel ? EPI_CHANNEL : 0);
     const int64_t out_es = a.out_dtype == OUT_F32 ? 4 : (a.out_dtype == OUT_F16 ? 2 : 1);
     const int vec_out = pp::aligned16(a.C) && (a.N * out_es) % 16 == 0;

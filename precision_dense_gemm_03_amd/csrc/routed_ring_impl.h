@@ -29,7 +29,7 @@ __global__ __launch_bounds__(256) void grouped_ring_kernel(
     constexpr int S64 = kRingBytes / ((64 + BN) * 128);
     __shared__ __attribute__((aligned(1024))) uint8_t ring[kRingBytes];
     __shared__ v4f red[ring::Ring<ES, 16, BN, BT, S16>::RED_SLOTS];
-    const RowTile t = find_row_tile<64>(offsets, groups, rows, blockIdx.x, tiles_n);
+    const RowTile t = find_row_tile<64>(offsets, groups, rows, (int)wide_block(), tiles_n);
     if (t.m0 >= t.end) return;
     const int n0 = t.tn * BN;
     if (t.group < 0) {
@@ -53,13 +53,13 @@ __global__ __launch_bounds__(256) void grouped_ring_kernel(
 template <int ES>
 bool grouped_ring_fits(const GroupedArgs& a) {
     const bool fits = a.b_kmajor ? ring::ring_fits<ES, 64, true>(a, 64) : ring::ring_fits<ES, 64, false>(a, 64);
-    return fits && most_workgroups(a.M, a.groups, 64, (a.N + 63) / 64) <= 0x7FFFFFFF;
+    return fits && most_workgroups(a.M, a.groups, 64, (a.N + 63) / 64) <= kMostWorkgroups;
 }
 
 template <int ES, int FA, int FB, bool BT>
 hipError_t launch_grouped_ring(const GroupedArgs& a) {
     const int64_t tiles_n = (a.N + 63) / 64;
-    const unsigned grid = (unsigned)most_workgroups(a.M, a.groups, 64, tiles_n);
+    const dim3 grid = wide_grid(most_workgroups(a.M, a.groups, 64, tiles_n));
     const int eflags = (a.out_dtype == OUT_E5M2 ? EPI_E5M2 : 0) | (a.channel ? EPI_CHANNEL : 0);
     const int64_t out_es = a.out_dtype == OUT_F32 ? 4 : (a.out_dtype == OUT_F16 ? 2 : 1);
     const int vec_out = ((uintptr_t)a.C % (4 * out_es)) == 0 && (a.N % 4) == 0;

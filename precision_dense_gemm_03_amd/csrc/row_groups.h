@@ -22,6 +22,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "wide_grid.h"
+
 namespace libgemm {
 
 struct RowTile {
@@ -112,6 +114,10 @@ inline int64_t most_workgroups(int64_t rows, int64_t groups, int bm, int64_t til
     const int64_t segs = groups + 2 < rows ? groups + 2 : rows;
     return (rows + segs * (bm - 1)) / bm * ((tiles_n + 7) / 8 * 8 + 8);
 }
+
+// Workgroups that a kernel can count: find_row_tile takes an int, and the last
+// y of a wide grid fills up with more than were asked for.
+constexpr int64_t kMostWorkgroups = 0x7FFFFFFF - (1 << kWideBits);
 
 // Zeros in columns [n0, n0 + BN) of rows [m0, min(end, m0 + BM)): the rows of no group.
 template <int BM, int BN, int ES>

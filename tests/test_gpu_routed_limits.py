@@ -111,3 +111,30 @@ def test_route_backward_of_many_tokens():
     for renorm in (True, False):
         d = g.moe_route_backward_f32(logits, expert, weight, dweight, renorm=renorm)
         assert torch.equal(d[:, 0], t.float() / 4) and torch.equal(d[:, 1], -t.float() / 4), renorm
+
+
+def grouped_rows(rows, n, k, out, name, monkeypatch):
+    """C[r] = A[r] B[g] in small whole numbers, two groups, rows of no group at both ends."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    lead, cut, tail = 1001, rows // 2 + 3, 70
+    gn = torch.Generator(device=DEV).manual_seed(2)
+    a = torch.randint(-3, 4, (rows, k), generator=gn, device=DEV, dtype=torch.int8).half()
+    b = torch.randint(-3, 4, (2, n, k), generator=gn, device=DEV).half()
+    offsets = torch.tensor([lead, cut, rows - tail], dtype=I32, device=DEV)
+    c = torch.full((rows, n), 9.0, dtype=out, device=DEV)
+    say(f"{name} over {rows} rows")
+    g.gemm_f16_grouped_bt(a, b, offsets, c)
+    step = 1 << 24
+    for e, (lo, hi) in enumerate(((lead, cut), (cut, rows - tail))):
+        w = b[e].float().t().contiguous()
+        for at in range(lo, hi, step):
+            end = min(hi, at + step)
+            assert torch.equal(c[at:end].float(), a[at:end].float() @ w), (e, at)
+    assert bool((c[:lead] == 0).all()) and bool((c[rows - tail:] == 0).all())
+
+
+@pytest.mark.parametrize("name,rows", [("grouped_ring", (1 << 26) + 4001), ("grouped_pp_128", (1 << 26) + 4001),
+                                       ("grouped_pp_256", (1 << 27) + 4001), ("grouped_tile_64", (1 << 26) + 4001)])
+def test_grouped_of_many_rows(name, rows, monkeypatch):
+    """Workgroups of 256 or 512 threads that reach 2^32 threads."""
+    grouped_rows(rows, 8, 8, F16, name, monkeypatch)
