@@ -32,6 +32,7 @@
 
 #include "gemm_pp_impl.h"
 #include "gemm_tile_impl.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace {
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             default: return (LDS_AS uint8_t*)b3;
         }
     };
-    const WgradTile w = wgrad_tile(blockIdx.x, offsets, groups, rows, tiles_m, tiles_n);
+    const WgradTile w = wgrad_tile((int)wide_block(), offsets, groups, rows, tiles_m, tiles_n);
     if (w.group < 0) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -353,7 +354,7 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
     __shared__ __attribute__((aligned(16))) uint8_t smem_raw[4 * OP];
     LDS_AS uint8_t* smem = (LDS_AS uint8_t*)smem_raw;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-    const WgradTile w = wgrad_tile(blockIdx.x, offsets, groups, rows, tiles_m, tiles_n);
+    const WgradTile w = wgrad_tile((int)wide_block(), offsets, groups, rows, tiles_m, tiles_n);
     if (w.group < 0) return;
     const int grp = w.group, m0 = w.tm * TS, n0 = w.tn * TS, lo = w.lo, hi = w.hi;
     const int nk = (hi - lo + BK - 1) / BK;
@@ -511,18 +512,19 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
     }
     const int64_t tiles_m = (a.M + size - 1) / size, tiles_n = (a.N + size - 1) / size;
     const int64_t blocks = wgrad_blocks(a.groups, tiles_m, tiles_n);
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (blocks > kMostWorkgroups) return hipErrorInvalidValue;
+    const dim3 grid = wide_grid(blocks);
     const int rows = (int)a.K, M = (int)a.M, N = (int)a.N, groups = (int)a.groups;
     // Whole lines past the caches: 4096 rows, 8 groups, 2048 x 4096 FP16 102 -> 89
     // us; lines written in two parts, 18 groups of 2232 x 824: 17.9 -> 31.2.
     const bool lines = ((uintptr_t)a.C & 127) == 0 && a.N * (a.out_dtype == OUT_F32 ? 4 : 2) % 128 == 0;
     const int vec_out = pp::aligned16(a.C);
 #define LIBGEMM_PP(OUT, LINES)                                                                             \
-    wgrad_pp_kernel<OUT, LINES><<<(unsigned)blocks, 512, 0, a.stream>>>(                                   \
+    wgrad_pp_kernel<OUT, LINES><<<grid, 512, 0, a.stream>>>(                                                \
         (const uint8_t*)a.A, (const uint8_t*)a.B, a.C, a.offsets, groups, rows, M, N, (int)tiles_m,        \
         (int)tiles_n, vec_out)
 #define LIBGEMM_TILE(OUT, TS)                                                                                       \
-    wgrad_tile_kernel<OUT, TS><<<(unsigned)blocks, 256, 0, a.stream>>>((const _Float16*)a.A, (const _Float16*)a.B, \
+    wgrad_tile_kernel<OUT, TS><<<grid, 256, 0, a.stream>>>((const _Float16*)a.A, (const _Float16*)a.B, \
                                                                        a.C, a.offsets, groups, rows, M, N,          \
                                                                        (int)tiles_m, (int)tiles_n)
     const bool f32 = a.out_dtype == OUT_F32;

@@ -115,10 +115,6 @@ inline int64_t most_workgroups(int64_t rows, int64_t groups, int bm, int64_t til
     return (rows + segs * (bm - 1)) / bm * ((tiles_n + 7) / 8 * 8 + 8);
 }
 
-// Workgroups that a kernel can count: find_row_tile takes an int, and the last
-// y of a wide grid fills up with more than were asked for.
-constexpr int64_t kMostWorkgroups = 0x7FFFFFFF - (1 << kWideBits);
-
 // Zeros in columns [n0, n0 + BN) of rows [m0, min(end, m0 + BM)): the rows of no group.
 template <int BM, int BN, int ES>
 __device__ __forceinline__ void zero_rows(void* C, int m0, int end, int n0, int N) {

@@ -12,6 +12,7 @@
 namespace libgemm {
 
 constexpr int kWideBits = 22;
+constexpr int64_t kMostWorkgroups = 0x7FFFFFFF - (1 << kWideBits);   // for kernels that count them in an int
 
 inline dim3 wide_grid(int64_t workgroups) {
     const int64_t x = (int64_t)1 << kWideBits;

@@ -138,3 +138,28 @@ def grouped_rows(rows, n, k, out, name, monkeypatch):
 def test_grouped_of_many_rows(name, rows, monkeypatch):
     """Workgroups of 256 or 512 threads that reach 2^32 threads."""
     grouped_rows(rows, 8, 8, F16, name, monkeypatch)
+
+
+@pytest.mark.parametrize("name,m,n", [("wgrad_pp", 8, (1 << 19) + 256), ("wgrad_tile_128", 1, (1 << 19) + 128),
+                                      ("wgrad_tile_64", 1, (1 << 18) + 64)])
+def test_weight_gradients_of_many_tiles(name, m, n, monkeypatch):
+    """4096 groups whose tiles reach 2^32 threads; rows in every 1365th, the last group among them."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    groups, every, per = 4096, 1365, 2
+    gn = torch.Generator(device=DEV).manual_seed(3)
+    full = range(0, groups, every)
+    sizes = torch.zeros(groups, dtype=torch.int64)
+    sizes[::every] = per
+    offsets = torch.cat([torch.zeros(1, dtype=torch.int64), sizes.cumsum(0)]).to(I32).to(DEV)
+    rows = int(offsets[-1])
+    a = torch.randint(-3, 4, (rows, m), generator=gn, device=DEV).half()
+    b = torch.randint(-3, 4, (rows, n), generator=gn, device=DEV).half()
+    c = torch.full((groups, m, n), 9.0, dtype=F16, device=DEV)
+    say(f"{name}: {groups} gradients of {m} x {n}")
+    g.gemm_f16_grouped_wgrad(a, b, offsets, c)
+    assert full[-1] == groups - 1
+    for i, e in enumerate(full):
+        x, y = a[per * i:per * i + per].float().t().contiguous(), b[per * i:per * i + per].float()
+        assert torch.equal(c[e].float(), x @ y), e
+    for lo, hi in zip(full, full[1:]):
+        assert bool((c[lo + 1:hi] == 0).all()), lo
