@@ -33,6 +33,7 @@
 #include "device_common.h"
 #include "gemm_ring_impl.h"
 #include "kernels.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace {
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(256) void lora_low_dot_kernel(const _Float16* __res
                                                            int rank, int rank_p, int adapters,
                                                            float* __restrict__ low) {
     const int lane = threadIdx.x & 63;
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int64_t w = wide_block() * 4 + (threadIdx.x >> 6);
     if (w >= waves) return;
     const int64_t row = w / rank_p;
     const int r = (int)(w % rank_p);
@@ -229,31 +230,17 @@ bool low_ring_ok(const LoraArgs& a) {
 // K of a slice: whole K tiles of the ring kernel.
 int64_t low_slice_k(int64_t K, int slices) { return ((K + slices - 1) / slices + 63) / 64 * 64; }
 
-}  // namespace
+// Rows of one launch: their workgroups (16 rows, up to 512 threads) stay below
+// 2^32 threads.
+constexpr int64_t kLowLaunchRows = 1 << 24;
 
-// Two workgroups per compute unit, of at least kLowSliceK of K each.
-int lora_most_slices(int64_t rows, int64_t rank) {
-    if (rows <= kLowDotRows || rank <= 0) return 1;
-    const int64_t blocks = (rows + 15) / 16 * ((rank + 63) / 64), s = 512 / blocks;
-    return s < 1 ? 1 : (s > kLowMostSlices ? kLowMostSlices : (int)s);
-}
-
-int lora_low_slices(const LoraArgs& a) {
-    if (!low_ring_ok(a)) return 1;
-    const int64_t most = lora_most_slices(a.M, a.rank);
-    int64_t s = a.K / kLowSliceK < most ? a.K / kLowSliceK : most;
-    if (s <= 1) return 1;
-    const int64_t per = low_slice_k(a.K, (int)s);
-    return (int)((a.K + per - 1) / per);   // none of them empty
-}
-
-hipError_t launch_lora_low(const LoraArgs& a) {
+hipError_t launch_low_rows(const LoraArgs& a) {
     const _Float16* X = reinterpret_cast<const _Float16*>(a.X);
     const _Float16* LA = reinterpret_cast<const _Float16*>(a.LA);
     const int rank = (int)a.rank, rank_p = (rank + 7) / 8 * 8;
     if (a.M <= kLowDotRows) {
         const int64_t waves = a.M * rank_p;
-        lora_low_dot_kernel<<<(unsigned)((waves + 3) / 4), 256, 0, a.stream>>>(
+        lora_low_dot_kernel<<<wide_grid((waves + 3) / 4), 256, 0, a.stream>>>(
             X, LA, a.adapter, a.lscale, waves, (int)a.K, rank, rank_p, (int)a.adapters, a.low);
         return hipGetLastError();
     }
@@ -281,6 +268,37 @@ hipError_t launch_lora_low(const LoraArgs& a) {
     else LIBGEMM_GO(8);
 #undef LIBGEMM_GO
     return hipGetLastError();
+}
+
+}  // namespace
+
+// Two workgroups per compute unit, of at least kLowSliceK of K each.
+int lora_most_slices(int64_t rows, int64_t rank) {
+    if (rows <= kLowDotRows || rank <= 0) return 1;
+    const int64_t blocks = (rows + 15) / 16 * ((rank + 63) / 64), s = 512 / blocks;
+    return s < 1 ? 1 : (s > kLowMostSlices ? kLowMostSlices : (int)s);
+}
+
+int lora_low_slices(const LoraArgs& a) {
+    if (!low_ring_ok(a)) return 1;
+    const int64_t most = lora_most_slices(a.M, a.rank);
+    int64_t s = a.K / kLowSliceK < most ? a.K / kLowSliceK : most;
+    if (s <= 1) return 1;
+    const int64_t per = low_slice_k(a.K, (int)s);
+    return (int)((a.K + per - 1) / per);   // none of them empty
+}
+
+hipError_t launch_lora_low(const LoraArgs& call) {
+    LoraArgs a = call;
+    for (int64_t r0 = 0; r0 < call.M; r0 += kLowLaunchRows) {   // (slices of K: few rows only, one launch)
+        a.M = call.M - r0 < kLowLaunchRows ? call.M - r0 : kLowLaunchRows;
+        a.X = reinterpret_cast<const _Float16*>(call.X) + r0 * call.K;
+        a.adapter = call.adapter + r0;
+        a.low = call.low + r0 * ((call.rank + 7) / 8 * 8);
+        const hipError_t e = launch_low_rows(a);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace libgemm

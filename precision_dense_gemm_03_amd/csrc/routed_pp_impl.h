@@ -107,8 +107,10 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     LoraExtra ext) {
     using T = pp::Pp<ES, BM>;
     LIBGEMM_PP_LDS(T);
+    const int64_t id = wide_block();
+    if (id >= (int64_t)tiles_m * tiles_n) return;
     int tm, tn;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    tile_coords((int)id, tiles_m, tiles_n, tm, tn);
     pp::pp_body<ES, OUT, FA, FB, true, false, BM, true, LoraExtra, LINES>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                          tn * 256, eflags, vec_out, lds, ext);
 }
@@ -116,7 +118,8 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 template <int ES, int FA, int FB, int BM>
 hipError_t launch_lora_pp(const LoraArgs& a) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + 255) / 256;
-    const unsigned grid = (unsigned)(tiles_m * tiles_n);
+    if (tiles_m * tiles_n > kMostWorkgroups) return hipErrorInvalidValue;
+    const dim3 grid = wide_grid(tiles_m * tiles_n);
     const int eflags = a.channel ? EPI_CHANNEL : 0;
     const int vec_out = pp::aligned16(a.C) && (a.N * (a.out_dtype == OUT_F32 ? 4 : 2)) % 16 == 0;
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);

@@ -103,8 +103,10 @@ __global__ __launch_bounds__(256) void lora_ring_kernel(const uint8_t* __restric
     using T = ring::Ring<ES, BM, BN, true, S>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
     __shared__ v4f red[T::RED_SLOTS];
+    const int64_t id = wide_block();
+    if (id >= (int64_t)tiles_m * tiles_n) return;
     int tm, tn;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    tile_coords((int)id, tiles_m, tiles_n, tm, tn);
     ring::ring_body<ES, BM, BN, OUT, FA, FB, true, S, true, LoraExtra, P>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                       tn * BN, eflags, vec_out, ring, red, ext);
 }
@@ -112,7 +114,8 @@ __global__ __launch_bounds__(256) void lora_ring_kernel(const uint8_t* __restric
 template <int ES, int FA, int FB, int BM, int BN>
 hipError_t launch_lora_ring(const LoraArgs& a) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BN - 1) / BN;
-    const unsigned grid = (unsigned)(tiles_m * tiles_n);
+    if (tiles_m * tiles_n > kMostWorkgroups) return hipErrorInvalidValue;
+    const dim3 grid = wide_grid(tiles_m * tiles_n);
     const int eflags = a.channel ? EPI_CHANNEL : 0;
     const int vec_out = ((uintptr_t)a.C % (a.out_dtype == OUT_F32 ? 16 : 8)) == 0 && (a.N % 4) == 0;
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);

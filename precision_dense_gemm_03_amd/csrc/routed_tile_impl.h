@@ -70,8 +70,10 @@ __global__ __launch_bounds__(256) void lora_tile_kernel(const uint8_t* __restric
                                                         void* __restrict__ C, int M, int N, int K,
                                                         const float* __restrict__ sA, const float* __restrict__ sB,
                                                         int tiles_m, int tiles_n, int eflags, LoraExtra ext) {
+    const int64_t id = wide_block();
+    if (id >= (int64_t)tiles_m * tiles_n) return;
     int tm, tn;
-    tile_coords(blockIdx.x, tiles_m, tiles_n, tm, tn);
+    tile_coords((int)id, tiles_m, tiles_n, tm, tn);
     tile::tile_body<ES, OUT, BM, BM, BK, 2, 2, FA, FB, true, ES, true, LoraExtra>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                            tn * BM, 1, eflags, K, 0, ext);
 }
@@ -85,8 +87,8 @@ template <int ES, int BM, int FA, int FB>
 hipError_t launch_lora_tile(const LoraArgs& a) {
     constexpr int BK = 128 / ES;
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + BM - 1) / BM;
-    if (tiles_m * tiles_n > 0x7FFFFFFF) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)(tiles_m * tiles_n);
+    if (tiles_m * tiles_n > kMostWorkgroups) return hipErrorInvalidValue;
+    const dim3 grid = wide_grid(tiles_m * tiles_n);
     const int eflags = a.channel ? EPI_CHANNEL : 0;
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);

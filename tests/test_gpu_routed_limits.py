@@ -1,6 +1,6 @@
 """Routed calls at the ends of their size ranges: sizes next to 2^31, and
 launches of 2^32 threads and more. Every case has a 288 GB card in mind and
-keeps its operands below 100 GB; outputs are checked on the device, exactly
+takes at most 130 GB of it; outputs are checked on the device, exactly
 where the arithmetic is exact."""
 import pytest
 import torch
@@ -163,3 +163,63 @@ def test_weight_gradients_of_many_tiles(name, m, n, monkeypatch):
         assert torch.equal(c[e].float(), x @ y), e
     for lo, hi in zip(full, full[1:]):
         assert bool((c[lo + 1:hi] == 0).all()), lo
+
+
+def lora_rows(rows, n, k, rank, name, monkeypatch, count=3):
+    """Small whole numbers; adapters in turn, every fourth row without one."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    gn = torch.Generator(device=DEV).manual_seed(4)
+    unit = torch.randint(-3, 4, (4001, k), generator=gn, device=DEV).half()      # 4001 rows over and over
+    a = torch.empty((rows, k), dtype=F16, device=DEV)
+    whole = rows // 4001 * 4001
+    a[:whole].view(-1, 4001, k).copy_(unit)
+    a[whole:] = unit[:rows - whole]
+    b = torch.randint(-3, 4, (n, k), generator=gn, device=DEV).half()
+    la = torch.randint(-2, 3, (count, rank, k), generator=gn, device=DEV).half()
+    lb = torch.randint(-2, 3, (count, n, rank), generator=gn, device=DEV).half()
+    scale = torch.tensor([1.0, 2.0, 0.5][:count], device=DEV)
+    adapter = torch.arange(rows, dtype=I32, device=DEV)
+    adapter.remainder_(count + 1).sub_(1)
+    c = torch.full((rows, n), 9.0, dtype=F16, device=DEV)
+    say(f"{name} over {rows} rows, rank {rank}")
+    g.gemm_f16_lora_bt(a, b, la, lb, adapter, scale, c)
+    step = 1 << 24
+    for at in range(0, rows, step):
+        x, who = a[at:at + step].float(), adapter[at:at + step]
+        ref = x @ b.float().t()
+        for e in range(count):
+            y = (x @ la[e].float().t()) @ lb[e].float().t() * scale[e]
+            ref += torch.where((who == e)[:, None], y, torch.zeros_like(y))
+        assert torch.equal(c[at:at + step].float(), ref), at
+
+
+@pytest.mark.parametrize("name,rows,k", [("lora_tile_64", (1 << 27) + 19, 1), ("lora_ring", (1 << 28) + 4001, 8),
+                                         ("lora_tile_64", (1 << 30) + 77, 1), ("lora_ring", (1 << 30) + 77, 8),
+                                         ("lora_pp_192", 192 * (1 << 23) + 77, 8)])
+def test_adapters_of_many_rows(name, rows, k, monkeypatch):
+    """Low-rank values of 2^27 and 2^28 rows, and products of 2^30 and more, reach 2^32 threads."""
+    lora_rows(rows, 8 if k == 8 else 1, k, 2, name, monkeypatch)
+
+
+@pytest.mark.parametrize("rows,name", [(64, "lora_ring"), (65, "lora_tile_64"), (65, "lora_ring")])
+def test_adapters_of_a_large_rank(rows, name, monkeypatch):
+    """rows * rank waves of 64 threads reach 2^32; more than 2^16 blocks of 64 low-rank values."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    n, k, rank = 8, 8, (1 << 22) + 88
+    gn = torch.Generator(device=DEV).manual_seed(5)
+    a = torch.randint(-3, 4, (rows, k), generator=gn, device=DEV).half()
+    b = torch.randint(-3, 4, (n, k), generator=gn, device=DEV).half()
+    at = torch.tensor([0, 5, 63, 64, 1 << 20, (1 << 20) + 1, (1 << 22) - 1, 1 << 22, rank - 1], device=DEV)
+    la = torch.zeros((2, rank, k), dtype=F16, device=DEV)
+    lb = torch.randint(-2, 3, (2, n, rank), generator=gn, device=DEV, dtype=torch.int8).half()
+    la[:, at] = torch.randint(-2, 3, (2, len(at), k), generator=gn, device=DEV).half()
+    adapter = (torch.arange(rows, device=DEV) % 3 - 1).to(I32)
+    scale = torch.tensor([1.0, 2.0], device=DEV)
+    c = torch.full((rows, n), 9.0, dtype=F32, device=DEV)
+    say(f"{name}: {rows} rows, rank {rank}")
+    g.gemm_f16_lora_bt(a, b, la, lb, adapter, scale, c)
+    ref = a.float() @ b.float().t()
+    for e in range(2):
+        y = (a.float() @ la[e, at].float().t()) @ lb[e][:, at].float().t() * scale[e]
+        ref += torch.where((adapter == e)[:, None], y, torch.zeros_like(y))
+    assert torch.equal(c, ref)
