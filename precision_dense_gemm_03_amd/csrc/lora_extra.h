@@ -5,7 +5,7 @@
 //
 // low is FP32 and LB FP16, so each row's low values are split into two FP16
 // numbers, hi + lo, of 22 bits together, after scaling the row's piece of 64
-// by a power of two that puts its largest value into [2^14, 2^15): the split
+// by a power of two that puts its largest finite value into [2^14, 2^15): the split
 // then drops at most 2^-22 of that largest value (lo rounds to half a step,
 // 2^-11 of hi's half step), below FP32's own rounding of the sums it came from
 // for any K above 16. The scaling is undone on the FP32 sum, exactly. Both
@@ -76,7 +76,18 @@ struct LoraExtra {
             }
         }
         for (int d = first_d; d < end_d; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-        const int e = m > 0.0f && m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) - 15 : 0;
+        if (__builtin_amdgcn_ballot_w64(m == __builtin_inff())) {   // infinities: the largest finite value
+            m = 0.0f;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float a = __builtin_fabsf(v[s][i]);
+                    if (a < __builtin_inff()) m = fmaxf(m, a);
+                }
+            for (int d = first_d; d < end_d; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        }
+        const int e = m > 0.0f ? __builtin_amdgcn_frexp_expf(m) - 15 : 0;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
 #pragma unroll

@@ -1,0 +1,56 @@
+"""Adapters whose low-rank values or weights hold infinities, on every kernel
+of the products (named through LIBGEMM_CONFIG): what the FP32 formula makes of
+them, whichever kernel runs."""
+import pytest
+import torch
+
+import precision_dense_gemm_03_amd as g
+
+pytestmark = pytest.mark.gpu
+
+DEV = torch.device("cuda:0")
+F16, F32, I32 = torch.float16, torch.float32, torch.int32
+INF = float("inf")
+LORA = ["lora_pp_256", "lora_pp_192", "lora_ring", "lora_tile_128", "lora_tile_64"]
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(DEV)
+    g.lib()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rank", [2, 40, 130])
+@pytest.mark.parametrize("name", LORA)
+def test_infinite_low_rank_value(name, rank, monkeypatch):
+    """A low-rank value that overflows FP32 beside finite ones above FP16's range, of opposite sign in the product:
+    the infinity decides, it does not meet another one."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    rows, n, k = 70, 72, 64
+    gn = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.zeros((rows, k), dtype=F16, device=DEV)
+    x[:, 0], x[:, 1] = 128.0, 1.0
+    b = torch.randint(-3, 4, (n, k), generator=gn, device=DEV).half()
+    la = torch.zeros((2, rank, k), dtype=F16, device=DEV)
+    lb = torch.zeros((2, n, rank), dtype=F16, device=DEV)
+    sign = torch.where(torch.arange(n, device=DEV) % 2 == 0, 1.0, -1.0).half()
+    la[:, rank - 2, 0], lb[:, :, rank - 2] = 128.0, sign      # 2^14
+    la[:, rank - 1, 1], lb[:, :, rank - 1] = 1.0, -sign       # 1
+    scale = torch.tensor([1.0, 2.0 ** 120], device=DEV)
+    adapter = (torch.arange(rows, device=DEV) % 3 - 1).to(I32)
+    base = x.float() @ b.float().t()
+    want = torch.where((adapter == 0)[:, None], base + sign.float() * (2.0 ** 14 - 1), base)
+    want = torch.where((adapter == 1)[:, None], (sign.float() * INF).expand(rows, n), want)
+    for out in (F32, F16):
+        c = torch.full((rows, n), 9.0, dtype=out, device=DEV)
+        say(f"{name} rank {rank} {out}")
+        g.gemm_f16_lora_bt(x, b, la, lb, adapter, scale, c)
+        assert torch.equal(c, want.to(out)), (c[1], want[1])
