@@ -9,7 +9,8 @@
 // then drops at most 2^-22 of that largest value (lo rounds to half a step,
 // 2^-11 of hi's half step), below FP32's own rounding of the sums it came from
 // for any K above 16. The scaling is undone on the FP32 sum, exactly. Both
-// halves meet LB's operand, loaded once, on the matrix cores.
+// halves meet LB's operand, loaded once, on the matrix cores; infinities and NaN
+// of LB meet hi alone (lo may be zero, or of the other sign).
 //
 // Rows of one block may have several adapters: each adapter present multiplies
 // the whole block and only its rows take the sum, so no other adapter's values
@@ -19,6 +20,28 @@
 #include "device_common.h"
 
 namespace libgemm {
+
+// Top bit of each half that is an infinity or a NaN, in four words.
+__device__ __forceinline__ v4u non_finite(v8h b) {
+    v4u w = __builtin_bit_cast(v4u, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = ((w[i] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
+    return w;
+}
+
+__device__ __forceinline__ bool any_non_finite(v8h b) {
+    const v4u w = non_finite(b);
+    return (w[0] | w[1] | w[2] | w[3]) != 0u;
+}
+
+// The finite halves, zero in the others' place.
+__device__ __forceinline__ v8h finite_part(v8h b) {
+    v4u w = __builtin_bit_cast(v4u, b);
+    const v4u bad = non_finite(b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] &= ~((bad[i] >> 15) * 0xFFFFu);
+    return __builtin_bit_cast(v8h, w);
+}
 
 struct LoraExtra {
     static constexpr bool kActive = true, kStores = false;
@@ -126,8 +149,9 @@ struct LoraExtra {
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             if (p0 + 32 * s >= rank_p) break;
-                            const v8h b = lb_chunk(a, col, p0 + 8 * (4 * s + g), N);
+                            v8h b = lb_chunk(a, col, p0 + 8 * (4 * s + g), N);
                             sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi[s], b, sum, 0, 0, 0);
+                            if (__builtin_amdgcn_ballot_w64(any_non_finite(b))) b = finite_part(b);
                             sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo[s], b, sum, 0, 0, 0);
                         }
 #pragma unroll
@@ -158,11 +182,13 @@ struct LoraExtra {
         const int tid = threadIdx.x, lane = tid & 63, lr = lane & 31, h = lane >> 5;
         LDS_AS int* ids = (LDS_AS int*)lds.a[2];
         LDS_AS int* exps = ids + BM;
+        LDS_AS int* special = exps + BM;   // whether an infinity or NaN of LB was met
         auto slot = [](int r, int c) __attribute__((always_inline)) -> int {
             return r * 128 + ((c ^ ((r & 7) ^ ((r >> 3) & 1))) << 4);
         };
         const int srow = tid >> 1, half = tid & 1;   // staging: 32 values of a row (of low, of LB) per thread
         if (tid < BM) ids[tid] = adapter_of(m0 + tid, M);
+        if (tid == 0) *special = 0;
         for (int p0 = 0; p0 < rank_p; p0 += 64) {
             if (srow < BM) {
                 v8h hi[4], lo[4];
@@ -191,11 +217,16 @@ struct LoraExtra {
 #pragma unroll
                 for (int k = 0; k < (BM + 63) / 64; ++k) id[k] = id[k] == a ? -1 : id[k];
                 LDS_AS uint8_t* lb = srow < 128 ? lds.b[0] : lds.b[1];
+                bool bad = false;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    *(LDS_AS v8h*)(lb + slot(srow & 127, 4 * half + q)) =
-                        lb_chunk(a, min(n0 + srow, N - 1), p0 + 32 * half + 8 * q, N);
+                for (int q = 0; q < 4; ++q) {
+                    const v8h v = lb_chunk(a, min(n0 + srow, N - 1), p0 + 32 * half + 8 * q, N);
+                    bad |= any_non_finite(v);
+                    *(LDS_AS v8h*)(lb + slot(srow & 127, 4 * half + q)) = v;
+                }
+                if (__builtin_amdgcn_ballot_w64(bad) != 0 && lane == 0) *special = 1;
                 __syncthreads();
+                const bool finite = *special == 0;
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
                     const int r = MR * G + 32 * i + lr;
@@ -210,10 +241,11 @@ struct LoraExtra {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) sum[x] = 0.0f;
                         for (int s = 0; s < 4 && p0 + 16 * s < rank_p; ++s) {
-                            const v8h bo = *(const LDS_AS v8h*)(b + slot(c, 2 * s + h));
+                            v8h bo = *(const LDS_AS v8h*)(b + slot(c, 2 * s + h));
                             const v8h ho = *(const LDS_AS v8h*)(lds.a[0] + slot(r, 2 * s + h));
                             const v8h lw = *(const LDS_AS v8h*)(lds.a[1] + slot(r, 2 * s + h));
                             sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(bo, ho, sum, 0, 0, 0);
+                            if (!finite) bo = finite_part(bo);
                             sum = __builtin_amdgcn_mfma_f32_32x32x16_f16(bo, lw, sum, 0, 0, 0);
                         }
 #pragma unroll

@@ -54,3 +54,35 @@ def test_infinite_low_rank_value(name, rank, monkeypatch):
         say(f"{name} rank {rank} {out}")
         g.gemm_f16_lora_bt(x, b, la, lb, adapter, scale, c)
         assert torch.equal(c, want.to(out)), (c[1], want[1])
+
+
+@pytest.mark.parametrize("rank", [3, 40, 130])
+@pytest.mark.parametrize("name", LORA)
+def test_infinite_weight(name, rank, monkeypatch):
+    """An infinity in LB meets the low-rank value itself, not the parts it is split into: 1 - 2^-13 (whose second
+    part is negative), 1 + 2^-12 (positive) and 1 (zero) all give infinity of LB's sign; NaN stays NaN, and the
+    other columns keep their bits."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    rows, n, k = 70, 272, 64
+    gn = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.zeros((rows, k), dtype=F16, device=DEV)
+    x[:, 0], x[:, 1] = 1.0, torch.tensor([-2.0 ** -13, 2.0 ** -12, 0.0], device=DEV).half()[torch.arange(rows, device=DEV) % 3]
+    b = torch.randint(-3, 4, (n, k), generator=gn, device=DEV).half()
+    b[:, 1] = 0
+    la = torch.zeros((2, rank, k), dtype=F16, device=DEV)
+    la[:, rank - 1, :2] = 1.0
+    lb = torch.zeros((2, n, rank), dtype=F16, device=DEV)
+    lb[:, :, rank - 1] = torch.randint(-3, 4, (2, n), generator=gn, device=DEV).half()
+    low = x[:, :2].float().sum(1, keepdim=True)
+    base = x.float() @ b.float().t()
+    lb[1, 3, rank - 1], lb[1, 130, rank - 1], lb[1, 200, rank - 1] = INF, -INF, float("nan")
+    adapter = (torch.arange(rows, device=DEV) // 3 % 3 - 1).to(I32)
+    want = base.clone()
+    for e in range(2):
+        want = torch.where((adapter == e)[:, None], base + low * lb[e, :, rank - 1].float(), want)
+    assert bool(want[adapter == 1][:, [3, 130]].isinf().all()) and bool(want[adapter != 1].isfinite().all())
+    c = torch.full((rows, n), 9.0, dtype=F32, device=DEV)
+    say(f"{name} rank {rank}")
+    g.gemm_f16_lora_bt(x, b, la, lb, adapter, torch.ones(2, device=DEV), c)
+    assert torch.equal(c.nan_to_num(nan=7.25), want.nan_to_num(nan=7.25))
+    assert torch.equal(c.isnan(), want.isnan())
