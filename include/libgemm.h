@@ -432,6 +432,22 @@ int gemm_fp8_lora_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b, 
 /* Bytes of workspace the adapter calls need (GEMM_ERR_DIM for a bad size). */
 int64_t gemm_lora_workspace_size(int64_t rows, int64_t rank);
 
+/*
+ * gemm_select_config_grouped / _wgrad / _lora — host-only queries, as
+ * gemm_select_config: the kernel that gemm_f16_grouped(_bt) (kind 0),
+ * gemm_fp8_grouped*(_bt) (kind 1), gemm_f16_grouped_wgrad, gemm_f16_lora_bt
+ * (kind 0) or gemm_fp8_lora_bt (kind 1) would launch for these sizes and
+ * 16-byte aligned operands (that of the product; calls that write zeros or run
+ * the plain product launch none of these). LIBGEMM_CONFIG=<name> replaces the
+ * choice where that kernel takes the operands. Kind 0 ignores the formats.
+ */
+int gemm_select_config_grouped(int kind, int out_dtype, int64_t rows, int64_t N, int64_t K, int64_t groups,
+                               int fmt_a, int fmt_b, int b_kmajor, char* buf, int buflen);
+int gemm_select_config_wgrad(int out_dtype, int64_t rows, int64_t M, int64_t N, int64_t groups, char* buf,
+                             int buflen);
+int gemm_select_config_lora(int kind, int out_dtype, int64_t rows, int64_t N, int64_t K, int64_t rank,
+                            int64_t adapters, int fmt_a, int fmt_b, char* buf, int buflen);
+
 /* ------------------------------------------------------- expert routing */
 
 /*

@@ -53,6 +53,9 @@ Functions keep the C names:
     gemm_f16_lora_bt(A, Bt, LA, LB, adapter, lscale, C, workspace=None, stream=None)
     gemm_fp8_lora_bt(A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C, workspace=None, stream=None)
     lora_workspace_size(rows, rank) -> int
+    select_config_grouped(kind, out_dtype, rows, N, K, groups, fmt_a=0, fmt_b=0, b_kmajor=0) -> str
+    select_config_wgrad(out_dtype, rows, M, N, groups) -> str
+    select_config_lora(kind, out_dtype, rows, N, K, rank, adapters, fmt_a=0, fmt_b=0) -> str
   Expert routing:
     moe_route_f32(logits, topk, renorm=True, expert=None, weight=None, offsets=None, row=None, token=None,
                   workspace=None, stream=None) -> (expert, weight, offsets, row, token)
@@ -198,6 +201,12 @@ def lib() -> ctypes.CDLL:
     L.gemm_f16_lora_bt.argtypes = [vp] * 7 + [i32] + [i64] * 5 + [vp, i64, vp]
     L.gemm_fp8_lora_bt.restype = i32
     L.gemm_fp8_lora_bt.argtypes = [vp, i32, vp, i32] + [vp] * 8 + [i32] + [i64] * 5 + [vp, i64, vp]
+    L.gemm_select_config_grouped.restype = i32
+    L.gemm_select_config_grouped.argtypes = [i32, i32, i64, i64, i64, i64, i32, i32, i32, ctypes.c_char_p, i32]
+    L.gemm_select_config_wgrad.restype = i32
+    L.gemm_select_config_wgrad.argtypes = [i32, i64, i64, i64, i64, ctypes.c_char_p, i32]
+    L.gemm_select_config_lora.restype = i32
+    L.gemm_select_config_lora.argtypes = [i32, i32, i64, i64, i64, i64, i64, i32, i32, ctypes.c_char_p, i32]
     L.gemm_lora_workspace_size.restype = i64
     L.gemm_lora_workspace_size.argtypes = [i64, i64]
     L.moe_route_f32.restype = i32
@@ -920,6 +929,33 @@ def gemm_f16_grouped_wgrad(A, B, offsets, C, stream=None):
     _check(lib().gemm_f16_grouped_wgrad(_ptr(A), _ptr(B), _ptr(offsets), _ptr(C), _out_dtype(C), rows, M, N, groups,
                                         _stream_handle(stream)), "gemm_f16_grouped_wgrad")
     return C
+
+
+def select_config_grouped(kind: int, out_dtype: int, rows: int, N: int, K: int, groups: int, fmt_a: int = 0,
+                          fmt_b: int = 0, b_kmajor: int = 0) -> str:
+    """The kernel that the grouped products (kind KIND_F16 or KIND_FP8; K-major weights with b_kmajor) would launch for
+    16-byte aligned operands."""
+    buf = ctypes.create_string_buffer(128)
+    _check(lib().gemm_select_config_grouped(kind, out_dtype, rows, N, K, groups, int(fmt_a), int(fmt_b), int(b_kmajor),
+                                            buf, len(buf)), "gemm_select_config_grouped")
+    return buf.value.decode()
+
+
+def select_config_wgrad(out_dtype: int, rows: int, M: int, N: int, groups: int) -> str:
+    """The kernel that gemm_f16_grouped_wgrad would launch for 16-byte aligned operands."""
+    buf = ctypes.create_string_buffer(128)
+    _check(lib().gemm_select_config_wgrad(out_dtype, rows, M, N, groups, buf, len(buf)), "gemm_select_config_wgrad")
+    return buf.value.decode()
+
+
+def select_config_lora(kind: int, out_dtype: int, rows: int, N: int, K: int, rank: int, adapters: int, fmt_a: int = 0,
+                       fmt_b: int = 0) -> str:
+    """The kernel of the product that gemm_f16_lora_bt (KIND_F16) or gemm_fp8_lora_bt (KIND_FP8) would launch for
+    16-byte aligned operands."""
+    buf = ctypes.create_string_buffer(128)
+    _check(lib().gemm_select_config_lora(kind, out_dtype, rows, N, K, rank, adapters, int(fmt_a), int(fmt_b), buf,
+                                         len(buf)), "gemm_select_config_lora")
+    return buf.value.decode()
 
 
 def lora_workspace_size(rows: int, rank: int) -> int:

@@ -1,6 +1,8 @@
 // C-ABI entry points of the products whose weight depends on the row (grouped
 // by expert, per-row adapters) and of expert routing (include/libgemm.h).
 // Arguments are validated before any HIP call, as in abi.cpp.
+#include <cstdio>
+
 #include "abi_common.h"
 #include "kernels.h"
 #include "moe.h"
@@ -209,6 +211,53 @@ int gemm_fp8_lora_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b, 
                      void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     return lora_common(KIND_FP8, A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C, out_dtype, rows, N, K,
                        rank, adapters, workspace, workspace_bytes, stream);
+}
+
+static int put_name(const char* name, char* buf, int buflen) {
+    if (!buf || buflen <= 0) return GEMM_ERR_NULL;
+    std::snprintf(buf, (size_t)buflen, "%s", name);
+    return GEMM_OK;
+}
+
+static bool kinds_ok(int kind, int out_dtype, int most_out, int fmt_a, int fmt_b) {
+    if (kind != KIND_F16 && kind != KIND_FP8) return false;
+    if (out_dtype < GEMM_OUT_F32 || out_dtype > (kind == KIND_F16 ? GEMM_OUT_F16 : most_out)) return false;
+    return fmt_ok(fmt_a) && fmt_ok(fmt_b);
+}
+
+int gemm_select_config_grouped(int kind, int out_dtype, int64_t rows, int64_t N, int64_t K, int64_t groups, int fmt_a,
+                               int fmt_b, int b_kmajor, char* buf, int buflen) {
+    if (!kinds_ok(kind, out_dtype, GEMM_OUT_E5M2, fmt_a, fmt_b)) return GEMM_ERR_DTYPE;
+    if (!size_ok(rows) || !size_ok(N) || !size_ok(K) || groups < 0 || groups > kMaxRowGroups) return GEMM_ERR_DIM;
+    GroupedArgs a;
+    static_cast<GemmArgs&>(a) = GemmArgs{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype, rows, N, K,
+                                         nullptr, kind == KIND_F16 ? 0 : fmt_a, kind == KIND_F16 ? 0 : fmt_b, 0};
+    a.b_kmajor = b_kmajor ? 1 : 0;
+    a.groups = groups;
+    return put_name(grouped_kernel_name(kind, a), buf, buflen);
+}
+
+int gemm_select_config_wgrad(int out_dtype, int64_t rows, int64_t M, int64_t N, int64_t groups, char* buf, int buflen) {
+    if (out_dtype != GEMM_OUT_F32 && out_dtype != GEMM_OUT_F16) return GEMM_ERR_DTYPE;
+    if (!size_ok(rows) || !size_ok(M) || !size_ok(N) || groups < 0 || groups > kMaxRowGroups) return GEMM_ERR_DIM;
+    GroupedArgs a;
+    static_cast<GemmArgs&>(a) = GemmArgs{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype, M, N, rows,
+                                         nullptr};
+    a.groups = groups;
+    return put_name(wgrad_kernel_name(a), buf, buflen);
+}
+
+int gemm_select_config_lora(int kind, int out_dtype, int64_t rows, int64_t N, int64_t K, int64_t rank, int64_t adapters,
+                            int fmt_a, int fmt_b, char* buf, int buflen) {
+    if (!kinds_ok(kind, out_dtype, GEMM_OUT_F16, fmt_a, fmt_b)) return GEMM_ERR_DTYPE;
+    if (!size_ok(rows) || !size_ok(N) || !size_ok(K) || !size_ok(rank) || !dim_ok(adapters)) return GEMM_ERR_DIM;
+    LoraArgs a;
+    static_cast<GemmArgs&>(a) = GemmArgs{nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, out_dtype, rows, N, K,
+                                         nullptr, kind == KIND_F16 ? 0 : fmt_a, kind == KIND_F16 ? 0 : fmt_b, 0};
+    a.b_kmajor = 1;
+    a.rank = rank;
+    a.adapters = adapters;
+    return put_name(lora_kernel_name(kind, a), buf, buflen);
 }
 
 // ------------------------------------------------------------- expert routing

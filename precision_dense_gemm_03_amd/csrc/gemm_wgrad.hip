@@ -471,10 +471,8 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
             }
 }
 
-}  // namespace
-
-hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
-    if (a.M <= 0 || a.N <= 0 || a.groups <= 0) return hipSuccess;
+// Rows and columns of a tile: 256 (the ping-pong kernel), 128 or 64.
+int choose_wgrad(const GroupedArgs& a) {
     // 16-byte pieces of both operands' rows, and 32-bit offsets over 8 steps
     const bool pp_ok = pp::aligned16(a.A) && pp::aligned16(a.B) && a.M % 8 == 0 && a.N % 8 == 0 &&
                        a.M < (1 << 21) && a.N < (1 << 21);
@@ -510,6 +508,19 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
         if (std::strcmp(env, "wgrad_tile_128") == 0) size = 128;
         if (std::strcmp(env, "wgrad_tile_64") == 0) size = 64;
     }
+    return size;
+}
+
+}  // namespace
+
+const char* wgrad_kernel_name(const GroupedArgs& a) {
+    const int size = choose_wgrad(a);
+    return size == 256 ? "wgrad_pp" : (size == 128 ? "wgrad_tile_128" : "wgrad_tile_64");
+}
+
+hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
+    if (a.M <= 0 || a.N <= 0 || a.groups <= 0) return hipSuccess;
+    const int size = choose_wgrad(a);
     const int64_t tiles_m = (a.M + size - 1) / size, tiles_n = (a.N + size - 1) / size;
     const int64_t blocks = wgrad_blocks(a.groups, tiles_m, tiles_n);
     if (blocks > kMostWorkgroups) return hipErrorInvalidValue;

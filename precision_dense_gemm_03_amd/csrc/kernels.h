@@ -126,6 +126,10 @@ hipError_t launch_lora_low(const LoraArgs& a);
 int lora_most_slices(int64_t rows, int64_t rank);
 int lora_low_slices(const LoraArgs& a);
 hipError_t launch_lora(int kind, const LoraArgs& a);
+// Names of the kernels that these calls launch (host only).
+const char* grouped_kernel_name(int kind, const GroupedArgs& a);
+const char* wgrad_kernel_name(const GroupedArgs& a);
+const char* lora_kernel_name(int kind, const LoraArgs& a);
 hipError_t launch_lora_tile_f16(const LoraArgs& a, int bm);
 hipError_t launch_lora_tile_fp8(const LoraArgs& a, int bm);
 // The deep-ring kernel over row groups of few rows / with adapters, for

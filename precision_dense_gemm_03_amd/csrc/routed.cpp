@@ -129,29 +129,28 @@ double estimate(int which, const LoraCost& c, const LoraArgs& a, int64_t ring_co
     return rounds * k * c.per_k + c.fixed + share * (double)ceil_div(a.rank, 32) * c.term;
 }
 
-}  // namespace
+// The kernels by name, in the order of the enums.
+enum GroupedKernel { G_PP_256, G_PP_192, G_PP_128, G_RING, G_TILE_128, G_TILE_64 };
+constexpr const char* kGroupedNames[] = {"grouped_pp_256", "grouped_pp_192", "grouped_pp_128",
+                                         "grouped_ring", "grouped_tile_128", "grouped_tile_64"};
+constexpr const char* kLoraNames[N_LORA] = {"lora_pp_256", "lora_pp_192", "lora_ring", "lora_tile_128", "lora_tile_64"};
 
-hipError_t launch_grouped(int kind, const GroupedArgs& a) {
+GroupedKernel choose_grouped(int kind, const GroupedArgs& a) {
     const bool f16 = kind == KIND_F16, bt = a.b_kmajor != 0;
-    const bool mixed = a.fmt_a || a.fmt_b;
+    const bool mixed = a.fmt_a || a.fmt_b;   // (one height on the ping-pong kernel: 192 rows)
     const bool pp_ok = f16 ? grouped_pp_takes_f16(a) : grouped_pp_takes_fp8(a);
     const bool ring_ok = f16 ? grouped_ring_takes_f16(a) : grouped_ring_takes_fp8(a);
-    auto pp = [&](int bm) {
-        return f16 ? launch_grouped_pp_f16(a, bm) : (mixed ? launch_grouped_pp_mixed(a) : launch_grouped_pp_e4m3(a, bm));
-    };
-    auto ring = [&] { return f16 ? launch_grouped_ring_f16(a) : launch_grouped_ring_fp8(a); };
-    auto tile = [&](int bm) { return f16 ? launch_grouped_tile_f16(a, bm) : launch_grouped_tile_fp8(a, bm); };
     const Named named;
-    if (pp_ok && named("grouped_pp_256")) return pp(256);
-    if (pp_ok && named("grouped_pp_192")) return pp(192);
-    if (pp_ok && named("grouped_pp_128")) return pp(128);
-    if (ring_ok && named("grouped_ring")) return ring();
-    if (named("grouped_tile_128")) return tile(128);
-    if (named("grouped_tile_64")) return tile(64);
+    if (pp_ok && named("grouped_pp_256")) return mixed ? G_PP_192 : G_PP_256;
+    if (pp_ok && named("grouped_pp_192")) return G_PP_192;
+    if (pp_ok && named("grouped_pp_128")) return mixed ? G_PP_192 : G_PP_128;
+    if (ring_ok && named("grouped_ring")) return G_RING;
+    if (named("grouped_tile_128")) return G_TILE_128;
+    if (named("grouped_tile_64")) return G_TILE_64;
     int best = -1;
     double least = 0.0;
     for (int i = 0; i < N_GROUPED; ++i) {
-        if ((i == PP_256 || i == PP_128) && (!pp_ok || (i == PP_128 && mixed))) continue;   // (mixed formats: one height)
+        if ((i == PP_256 || i == PP_128) && (!pp_ok || (i == PP_128 && mixed))) continue;
         if (i == RING && !ring_ok) continue;
         const double t = estimate(kGrouped[f16 ? 0 : 1][bt ? 1 : 0][i], a, f16 ? 2 : 1);
         if (best < 0 || t < least) {
@@ -160,10 +159,58 @@ hipError_t launch_grouped(int kind, const GroupedArgs& a) {
         }
     }
     switch (best) {
-        case PP_256: return pp(shorter_tiles(a) ? 192 : 256);
-        case PP_128: return pp(128);
-        case RING: return ring();
-        case TILE_128: return tile(128);
+        case PP_256: return mixed || shorter_tiles(a) ? G_PP_192 : G_PP_256;
+        case PP_128: return G_PP_128;
+        case RING: return G_RING;
+        case TILE_128: return G_TILE_128;
+        default: return G_TILE_64;
+    }
+}
+
+int choose_lora(int kind, const LoraArgs& a) {
+    const bool f16 = kind == KIND_F16, mixed = a.fmt_a || a.fmt_b;   // (as above)
+    const bool ring_ok = f16 ? lora_ring_takes_f16(a) : lora_ring_takes_fp8(a);
+    const bool pp_ok = f16 ? lora_pp_takes_f16(a) : lora_pp_takes_fp8(a);
+    const Named named;
+    if (pp_ok && named("lora_pp_256")) return mixed ? L_PP_192 : L_PP_256;
+    if (pp_ok && named("lora_pp_192")) return L_PP_192;
+    if (ring_ok && named("lora_ring")) return L_RING;
+    if (named("lora_tile_128")) return L_TILE_128;
+    if (named("lora_tile_64")) return L_TILE_64;
+    int64_t cost = 0;
+    lora_ring_shape(a.M, a.N, &cost);
+    int best = -1;
+    double least = 0.0;
+    for (int i = 0; i < N_LORA; ++i) {
+        if ((i == L_PP_256 || i == L_PP_192) && !pp_ok) continue;
+        if (i == L_PP_256 && mixed) continue;
+        if (i == L_RING && !ring_ok) continue;
+        const double t = estimate(i, kLora[f16 ? 0 : 1][i], a, cost);
+        if (best < 0 || t < least) {
+            best = i;
+            least = t;
+        }
+    }
+    return best;
+}
+
+}  // namespace
+
+const char* grouped_kernel_name(int kind, const GroupedArgs& a) { return kGroupedNames[choose_grouped(kind, a)]; }
+const char* lora_kernel_name(int kind, const LoraArgs& a) { return kLoraNames[choose_lora(kind, a)]; }
+
+hipError_t launch_grouped(int kind, const GroupedArgs& a) {
+    const bool f16 = kind == KIND_F16, mixed = a.fmt_a || a.fmt_b;
+    auto pp = [&](int bm) {
+        return f16 ? launch_grouped_pp_f16(a, bm) : (mixed ? launch_grouped_pp_mixed(a) : launch_grouped_pp_e4m3(a, bm));
+    };
+    auto tile = [&](int bm) { return f16 ? launch_grouped_tile_f16(a, bm) : launch_grouped_tile_fp8(a, bm); };
+    switch (choose_grouped(kind, a)) {
+        case G_PP_256: return pp(256);
+        case G_PP_192: return pp(192);
+        case G_PP_128: return pp(128);
+        case G_RING: return f16 ? launch_grouped_ring_f16(a) : launch_grouped_ring_fp8(a);
+        case G_TILE_128: return tile(128);
         default: return tile(64);
     }
 }
@@ -174,37 +221,14 @@ hipError_t launch_lora(int kind, const LoraArgs& call) {
     const hipError_t e = launch_lora_low(a);
     if (e != hipSuccess) return e;
     const bool f16 = kind == KIND_F16, mixed = a.fmt_a || a.fmt_b;
-    const bool ring_ok = f16 ? lora_ring_takes_f16(a) : lora_ring_takes_fp8(a);
-    const bool pp_ok = f16 ? lora_pp_takes_f16(a) : lora_pp_takes_fp8(a);
     auto pp = [&](int bm) {
         return f16 ? launch_lora_pp_f16(a, bm) : (mixed ? launch_lora_pp_mixed(a) : launch_lora_pp_e4m3(a, bm));
     };
-    auto ring = [&] { return f16 ? launch_lora_ring_f16(a) : launch_lora_ring_fp8(a); };
     auto tile = [&](int bm) { return f16 ? launch_lora_tile_f16(a, bm) : launch_lora_tile_fp8(a, bm); };
-    const Named named;
-    if (pp_ok && named("lora_pp_256")) return pp(256);
-    if (pp_ok && named("lora_pp_192")) return pp(192);
-    if (ring_ok && named("lora_ring")) return ring();
-    if (named("lora_tile_128")) return tile(128);
-    if (named("lora_tile_64")) return tile(64);
-    int64_t cost = 0;
-    lora_ring_shape(a.M, a.N, &cost);
-    int best = -1;
-    double least = 0.0;
-    for (int i = 0; i < N_LORA; ++i) {
-        if ((i == L_PP_256 || i == L_PP_192) && !pp_ok) continue;
-        if (i == L_PP_256 && mixed) continue;   // (mixed formats: one height)
-        if (i == L_RING && !ring_ok) continue;
-        const double t = estimate(i, kLora[f16 ? 0 : 1][i], a, cost);
-        if (best < 0 || t < least) {
-            best = i;
-            least = t;
-        }
-    }
-    switch (best) {
+    switch (choose_lora(kind, a)) {
         case L_PP_256: return pp(256);
         case L_PP_192: return pp(192);
-        case L_RING: return ring();
+        case L_RING: return f16 ? launch_lora_ring_f16(a) : launch_lora_ring_fp8(a);
         case L_TILE_128: return tile(128);
         default: return tile(64);
     }

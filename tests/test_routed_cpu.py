@@ -194,3 +194,41 @@ def test_largest_sizes_are_taken():
     for which in ("N", "K"):
         assert f16_grouped(**{**dict(rows=0, N=1, K=1), which: LARGEST}) == [0, 0]
     assert f16_grouped(rows=LARGEST, N=0) == [0, 0]
+
+
+def test_select_config_of_the_routed_calls(monkeypatch):
+    monkeypatch.delenv("LIBGEMM_CONFIG", raising=False)
+    h, f8 = g.KIND_F16, g.KIND_FP8
+    sel, lo, wg = g.select_config_grouped, g.select_config_lora, g.select_config_wgrad
+    assert sel(h, g.OUT_F16, 16, 4096, 4096, 16, b_kmajor=1) == "grouped_ring"
+    assert sel(h, g.OUT_F16, 5003, 1416, 2048, 32) == "grouped_pp_128"
+    assert sel(f8, g.OUT_F16, 16384, 12288, 4096, 16, b_kmajor=1) == "grouped_pp_256"
+    assert sel(f8, g.OUT_F16, 16384, 4096, 4096, 16, 1, 0, 1) == "grouped_pp_192"       # E5M2 pairs: one height
+    assert sel(h, g.OUT_F16, 5000, 4096, 1001, 4, b_kmajor=1).startswith("grouped_tile")   # rows of no whole 16 bytes
+    assert wg(g.OUT_F32, 8192, 2048, 4096, 8) == "wgrad_pp" and wg(g.OUT_F32, 8192, 2047, 4096, 8) != "wgrad_pp"
+    assert lo(h, g.OUT_F16, 16, 4096, 4096, 16, 16) == "lora_ring" and lo(h, g.OUT_F16, 4096, 4096, 4096, 64, 8) == "lora_pp_256"
+    monkeypatch.setenv("LIBGEMM_CONFIG", "grouped_pp_256")
+    assert sel(h, g.OUT_F16, 16, 4096, 4096, 16) == "grouped_pp_256"
+    assert sel(f8, g.OUT_F16, 16, 4096, 4096, 16, 0, 1) == "grouped_pp_192"
+    assert sel(h, g.OUT_F16, 16, 4096, 4095, 16, b_kmajor=1) != "grouped_pp_256"            # not its operands
+    monkeypatch.setenv("LIBGEMM_CONFIG", "wgrad_tile_64")
+    assert wg(g.OUT_F32, 8192, 2048, 4096, 8) == "wgrad_tile_64"
+    monkeypatch.setenv("LIBGEMM_CONFIG", "lora_pp_256")
+    assert lo(f8, g.OUT_F16, 4, 64, 64, 8, 2, 1, 1) == "lora_pp_192" and lo(f8, g.OUT_F16, 4, 64, 64, 8, 2) == "lora_pp_256"
+
+
+def test_select_config_of_the_routed_calls_refusals():
+    import ctypes
+    L, buf = g.lib(), ctypes.create_string_buffer(64)
+    assert L.gemm_select_config_grouped(2, 0, 1, 1, 1, 1, 0, 0, 0, buf, 64) == DTYPE
+    assert L.gemm_select_config_grouped(0, 2, 1, 1, 1, 1, 0, 0, 0, buf, 64) == DTYPE
+    assert L.gemm_select_config_grouped(1, 3, 1, 1, 1, 1, 2, 0, 0, buf, 64) == DTYPE
+    assert L.gemm_select_config_grouped(1, 3, 1, 1, 1, 4097, 0, 0, 0, buf, 64) == DIM
+    assert L.gemm_select_config_grouped(1, 3, 1, 1, 1, 1, 0, 0, 0, None, 64) == NULL
+    assert L.gemm_select_config_grouped(1, 3, 0, 0, 0, 0, 0, 0, 0, buf, 64) == 0
+    assert L.gemm_select_config_wgrad(2, 1, 1, 1, 1, buf, 64) == DTYPE
+    assert L.gemm_select_config_wgrad(0, -1, 1, 1, 1, buf, 64) == DIM
+    assert L.gemm_select_config_wgrad(0, 0, 0, 0, 0, buf, 0) == NULL and L.gemm_select_config_wgrad(0, 0, 0, 0, 0, buf, 8) == 0
+    assert L.gemm_select_config_lora(1, 2, 1, 1, 1, 1, 1, 0, 0, buf, 64) == DTYPE
+    assert L.gemm_select_config_lora(1, 1, 1, 1, 1, 1 << 31, 1, 0, 0, buf, 64) == DIM
+    assert L.gemm_select_config_lora(1, 1, 0, 0, 0, 0, 0, 0, 0, buf, 64) == 0
