@@ -409,9 +409,11 @@ int gemm_f16_grouped_wgrad(const void* A, const void* B, const int32_t* offsets,
  *   workspace  device, 16-byte aligned, at least
  *              gemm_lora_workspace_size(rows, rank) bytes, contents on entry
  *              and return unspecified; calls that share it must not overlap
- * The low-rank values are FP32 (two launches). rank = 0 or adapters = 0 is the
- * plain product (no workspace needed). Errors as gemm_f16_bt, plus
- * GEMM_ERR_WORKSPACE.
+ * The low-rank values are FP32 (two launches); the deep-ring kernel multiplies
+ * them with LB as they are, the tile kernels as two FP16 parts, which hold a
+ * value to 2^-22 of itself or 2^-39 of the largest of its 64 neighbours. rank =
+ * 0 or adapters = 0 is the plain product (no workspace needed). Errors as
+ * gemm_f16_bt, plus GEMM_ERR_WORKSPACE.
  */
 int gemm_f16_lora_bt(const void* A, const void* Bt, const void* LA, const void* LB, const int32_t* adapter,
                      const float* lscale, void* C, int out_dtype, int64_t rows, int64_t N, int64_t K,

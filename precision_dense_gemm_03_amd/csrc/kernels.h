@@ -118,8 +118,7 @@ hipError_t launch_grouped_tile_fp8(const GroupedArgs& a, int bm);
 // F16 [groups, M, N]. K holds the number of rows.
 hipError_t launch_grouped_wgrad(const GroupedArgs& a);
 // low[i, r] = lscale[a_i] <X[i], LA[a_i, r]>, zero for rows without an adapter
-// and from rank on.
-// in a.low_slices parts, each the sum over a slice of K.
+// and from rank on, in a.low_slices parts, each the sum over a slice of K.
 hipError_t launch_lora_low(const LoraArgs& a);
 // Slices that launch_lora_low can use: the most for these rows and rank (what
 // the workspace holds), and those for a call.
@@ -161,8 +160,8 @@ bool lora_ring_takes_fp8(const LoraArgs& a);
 hipError_t launch_lora_ring_f16(const LoraArgs& a);
 hipError_t launch_lora_ring_fp8(const LoraArgs& a);
 // The ping-pong tile kernel over row groups / with adapters: whether it takes
-// the operands (16-byte alignment, 32-bit offsets), and its launches (bm 128 or
-// 256 rows, adapters 192 or 256; pairs with E5M2: 192).
+// the operands (16-byte alignment, 32-bit offsets), and its launches (bm 128, 192
+// or 256 rows, adapters 192 or 256; pairs with E5M2: 192).
 bool grouped_pp_takes_f16(const GroupedArgs& a);
 bool grouped_pp_takes_fp8(const GroupedArgs& a);
 bool lora_pp_takes_f16(const LoraArgs& a);

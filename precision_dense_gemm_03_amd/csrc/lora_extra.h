@@ -3,14 +3,18 @@
 //
 //   y[i, j] = base[i, j] + sum_r low[i, r] LB[a_i, j, r],   a_i the row's adapter
 //
-// low is FP32 and LB FP16, so each row's low values are split into two FP16
-// numbers, hi + lo, of 22 bits together, after scaling the row's piece of 64
-// by a power of two that puts its largest finite value into [2^14, 2^15): the split
-// then drops at most 2^-22 of that largest value (lo rounds to half a step,
-// 2^-11 of hi's half step), below FP32's own rounding of the sums it came from
-// for any K above 16. The scaling is undone on the FP32 sum, exactly. Both
-// halves meet LB's operand, loaded once, on the matrix cores; infinities and NaN
-// of LB meet hi alone (lo may be zero, or of the other sign).
+// low is FP32 and LB FP16. The tile kernels (add16, add_tile) split each row's
+// low values into two FP16 numbers, hi + lo, after scaling the row's piece of 64
+// by a power of two that puts its largest finite value into [2^14, 2^15). hi
+// is off by at most 2^-11 of the value and lo by at most 2^-11 of what hi left,
+// or half FP16's smallest step, so a value enters to 2^-22 of itself or 2^-39 of
+// the piece's largest, whichever is more: two bits fewer than FP32 holds. That
+// is the choice made here: K products summed in FP32 are seldom that exact, and
+// a third part would cost half as many matrix instructions again. The deep-ring
+// kernel (add_row4, few rows) multiplies the FP32 values as they are. The
+// scaling is undone on the FP32 sum, exactly. Both halves meet LB's operand,
+// loaded once; infinities and NaN of LB meet hi alone (lo may be zero, or of the
+// other sign).
 //
 // Rows of one block may have several adapters: each adapter present multiplies
 // the whole block and only its rows take the sum, so no other adapter's values

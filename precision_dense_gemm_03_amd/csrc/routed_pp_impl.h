@@ -3,9 +3,9 @@
 //
 // Grouped: tiles of BM x 256, and with TAILS a group's last rows at the
 // smallest of 64, 128, 192 and 256 rows that holds them (the four bodies share
-// the LDS rings). One workgroup per tile the host cannot rule out
-// (row_groups.h: up to one row of tiles per group more than there are; such a
-// workgroup ends after its look at the offsets). A fixed number of workgroups
+// the LDS rings; pairs with E5M2 are built at 192 rows only, without TAILS). One
+// workgroup per tile the host cannot rule out, and more (most_workgroups); one
+// without a tile ends after its look at the offsets. A fixed number of workgroups
 // walking the tiles measured slower: the walk's state cost the main loop its
 // registers (47 spilled per lane with 256 rows).
 #pragma once

@@ -109,7 +109,10 @@ __device__ __forceinline__ RowTile find_row_tile(const int32_t* __restrict__ off
 
 // Workgroups that cover every tile that offsets in order can give: all rows of
 // tiles, of which each nonempty segment pads at most one, and for each of them
-// one column more than its eighth.
+// its columns rounded up to whole rounds of the XCDs, and one round more. (The
+// columns of a share are consecutive numbers, of which one XCD gets at most an
+// eighth, rounded up; so the last round is never needed, and those workgroups,
+// as those of rows that no segment pads, end after their look at the offsets.)
 inline int64_t most_workgroups(int64_t rows, int64_t groups, int bm, int64_t tiles_n) {
     const int64_t segs = groups + 2 < rows ? groups + 2 : rows;
     return (rows + segs * (bm - 1)) / bm * ((tiles_n + 7) / 8 * 8 + 8);
