@@ -23,6 +23,9 @@
  *   - Results never depend on pointer alignment; 16-byte aligned pointers and
  *     row lengths that are multiples of 16 bytes take the fastest kernels.
  *   - Dimensions are int64_t; each must be in [0, 2^31 - 1].
+ *   - A plain product, transposed quantize or re-layout whose tiles would take a
+ *     launch of 2^32 threads or more (results of 2^36 elements; narrow ones of
+ *     2^30, decode ones of 2^25 columns) returns GEMM_ERR_LAUNCH.
  */
 #ifndef LIBGEMM_H
 #define LIBGEMM_H

@@ -14,6 +14,7 @@
 #include "device_common.h"
 #include "kernels.h"
 #include "quantize_tile.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 
@@ -207,7 +208,7 @@ hipError_t launch_quantize_transposed(const float* x, int64_t rows, int64_t cols
     if (rows <= 0 || cols <= 0) return hipSuccess;
     const int64_t tiles_r = (rows + kQtRows - 1) / kQtRows, tiles_c = (cols + kQtCols - 1) / kQtCols;
     const int64_t blocks = tiles_r * tiles_c;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_holds(blocks, kThreads)) return hipErrorInvalidValue;
     // 16-byte input rows need an aligned base and cols % 4 == 0; 16-byte
     // output segments an aligned base and rows % 16 == 0.
     const int vec_in = aligned16(x) && cols % 4 == 0;
@@ -226,7 +227,7 @@ hipError_t launch_transpose(const void* src, int64_t rows, int64_t cols, int ele
     if (rows <= 0 || cols <= 0) return hipSuccess;
     const int64_t tiles_r = (rows + kTrTile - 1) / kTrTile, tiles_c = (cols + kTrTile - 1) / kTrTile;
     const int64_t blocks = tiles_r * tiles_c;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_holds(blocks, kThreads)) return hipErrorInvalidValue;
     if (elem_bytes == 2)
         transpose_kernel<uint16_t><<<(unsigned)blocks, kThreads, 0, stream>>>(
             reinterpret_cast<const uint16_t*>(src), rows, cols, reinterpret_cast<uint16_t*>(dst), tiles_c);

@@ -30,6 +30,7 @@
 #include "device_common.h"
 #include "kernels.h"
 #include "quantize_tile.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 
@@ -259,7 +260,7 @@ hipError_t launch_amax_quantize_pair_bt(const float* xa, int64_t na, const float
     const int64_t tiles_r = (K + kQtRows - 1) / kQtRows, tiles_c = (N + kQtCols - 1) / kQtCols;
     const int64_t tiles = tiles_r * tiles_c;
     const int ga = (int)std::min<int64_t>(4096, std::max<int64_t>(1, (na + 8191) / 8192));
-    if (tiles + ga > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_holds(tiles + ga, kThreads)) return hipErrorInvalidValue;
     // 16-byte input rows: an aligned base and N % 4 == 0; 16-byte output
     // pieces: an aligned base and K % 16 == 0.
     const int vec_in = vec_b && N % 4 == 0;

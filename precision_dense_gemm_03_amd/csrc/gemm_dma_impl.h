@@ -53,6 +53,7 @@
 #include "device_common.h"
 #include "kernels.h"
 #include "tile_order.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace dma {
@@ -472,7 +473,7 @@ hipError_t launch_dma(const GemmArgs& a) {
     const bool aligned = aligned16(a.A) && aligned16(a.B) && (a.K * ES) % 16 == 0 && (BT || (a.N * ES) % 16 == 0);
     const bool fits = (int64_t)T::BM * a.K * ES < (1ll << 31) &&
                       (BT ? (int64_t)T::BN * a.K * ES : (int64_t)T::BK * a.N * ES) < (1ll << 31) &&
-                      blocks <= 0x7FFFFFFF;
+                      launch_holds(blocks, T::NT);
     if (!aligned || !fits) return fallback(ES == 1 ? KIND_FP8 : KIND_F16, a);
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);

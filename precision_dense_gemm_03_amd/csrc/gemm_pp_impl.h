@@ -79,6 +79,7 @@
 #include "device_common.h"
 #include "kernels.h"
 #include "tile_order.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace pp {
@@ -837,7 +838,7 @@ hipError_t launch_pp(const GemmArgs& a) {
     const int64_t tiles_n = (a.N + T::BN - 1) / T::BN;
     const int64_t blocks = tiles_m * tiles_n;
     if (blocks <= 0) return hipSuccess;
-    if (!pp_fits<ES, BT, BM>(a) || blocks > 0x7FFFFFFF) return fallback(ES == 1 ? KIND_FP8 : KIND_F16, a, EX);
+    if (!pp_fits<ES, BT, BM>(a) || !launch_holds(blocks, T::NT)) return fallback(ES == 1 ? KIND_FP8 : KIND_F16, a, EX);
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
     const int M = (int)a.M, N = (int)a.N, K = (int)a.K;

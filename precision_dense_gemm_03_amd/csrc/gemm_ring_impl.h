@@ -54,6 +54,7 @@
 #include "device_common.h"
 #include "kernels.h"
 #include "tile_order.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace ring {
@@ -776,7 +777,7 @@ hipError_t launch_ring(const GemmArgs& a) {
     const int64_t tiles_n = (a.N + BN - 1) / BN;
     const int64_t blocks = tiles_m * tiles_n;
     if (blocks <= 0) return hipSuccess;
-    if (!ring_fits<ES, BN, BT>(a, BM) || blocks > 0x7FFFFFFF) return fallback(ES == 1 ? KIND_FP8 : KIND_F16, a);
+    if (!ring_fits<ES, BN, BT>(a, BM) || !launch_holds(blocks, 256)) return fallback(ES == 1 ? KIND_FP8 : KIND_F16, a);
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
     const int M = (int)a.M, N = (int)a.N, K = (int)a.K;

@@ -16,6 +16,7 @@
 //     epilogue applies sA*sB and converts (FP8 guide §3.2).
 #include "device_common.h"
 #include "kernels.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 
@@ -225,7 +226,7 @@ template <int ES, int MMAX, int COLS, int NT, int U, int FA = 0, int FB = 0>
 hipError_t launch_stream(const GemmArgs& a) {
     const int64_t blocks = (a.N + COLS - 1) / COLS;
     if (blocks <= 0 || a.M <= 0) return hipSuccess;
-    if (blocks > 0x7FFFFFFF || a.M > MMAX) return hipErrorInvalidValue;
+    if (!launch_holds(blocks, NT) || a.M > MMAX) return hipErrorInvalidValue;
     const int splits = a.splits > 1 ? a.splits : 1;
     constexpr int kgran = stream_kgran<ES, COLS, NT, U>();
     if (splits > 1 && (a.k_chunk % kgran != 0 || a.k_chunk <= 0 || (int64_t)(splits - 1) * a.k_chunk >= a.K ||

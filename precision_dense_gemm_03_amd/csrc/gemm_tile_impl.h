@@ -39,6 +39,7 @@
 #include "device_common.h"
 #include "kernels.h"
 #include "tile_order.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 namespace tile {
@@ -273,7 +274,7 @@ hipError_t launch_tile(const GemmArgs& a) {
     const int64_t tiles_n = (a.N + BN - 1) / BN;
     const int64_t blocks = tiles_m * tiles_n;
     if (blocks <= 0) return hipSuccess;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_holds(blocks, 64 * WM * WN)) return hipErrorInvalidValue;
     const int splits = a.splits > 1 ? a.splits : 1;
     if (splits > 1 && (a.k_chunk % BK != 0 || a.k_chunk <= 0 || (int64_t)(splits - 1) * a.k_chunk >= a.K ||
                        splits > 65535 || !a.ws))

@@ -28,6 +28,7 @@
 // cross-workgroup reduction.
 #include "device_common.h"
 #include "kernels.h"
+#include "wide_grid.h"
 
 namespace libgemm {
 
@@ -257,7 +258,7 @@ hipError_t launch_gemv_kmajor_coop(const GemmArgs& a) {
     if (a.M > MMAX || !a.b_kmajor || a.splits > 1) return hipErrorInvalidValue;
     if (ES == 1 && (a.fmt_a != FA || a.fmt_b != FB)) return hipErrorInvalidValue;
     const int64_t blocks = (a.N + R - 1) / R;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_holds(blocks, 64 * W)) return hipErrorInvalidValue;
     const int vec = aligned16(a.A) && aligned16(a.B) && ((a.K * ES) % 16 == 0);
     const int eflags = a.channel ? EPI_CHANNEL : 0;
     gemv_kmajor_coop_kernel<ES, MMAX, R, W, FA, FB><<<(unsigned)blocks, 64 * W, 0, a.stream>>>(
@@ -274,7 +275,7 @@ hipError_t launch_gemv_kmajor(const GemmArgs& a) {
     if (ES == 1 && (a.fmt_a != FA || a.fmt_b != FB)) return hipErrorInvalidValue;
     constexpr int rows_per_block = (NT / 64) * R;
     const int64_t blocks = (a.N + rows_per_block - 1) / rows_per_block;
-    if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (!launch_holds(blocks, NT)) return hipErrorInvalidValue;
     const int vec = aligned16(a.A) && aligned16(a.B) && ((a.K * ES) % 16 == 0);
     const int eflags = a.channel ? EPI_CHANNEL : 0;
     gemv_kmajor_kernel<ES, MMAX, R, U, NT, FA, FB><<<(unsigned)blocks, NT, 0, a.stream>>>(

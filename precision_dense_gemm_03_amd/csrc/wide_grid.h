@@ -14,6 +14,9 @@ namespace libgemm {
 constexpr int kWideBits = 22;
 constexpr int64_t kMostWorkgroups = 0x7FFFFFFF - (1 << kWideBits);   // for kernels that count them in an int
 
+// Whether x alone holds them (kernels that take no wide grid).
+inline bool launch_holds(int64_t workgroups, int threads) { return workgroups <= 0xFFFFFFFFll / threads; }
+
 inline dim3 wide_grid(int64_t workgroups) {
     const int64_t x = (int64_t)1 << kWideBits;
     return workgroups <= x ? dim3((unsigned)workgroups) : dim3((unsigned)x, (unsigned)((workgroups + x - 1) / x));
