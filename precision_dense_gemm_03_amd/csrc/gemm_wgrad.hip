@@ -20,7 +20,7 @@
 // A product of few tiles is bound by the steps one tile takes one after
 // another, so the smaller tile wins there: 1819 rows in 23 groups, 304 x 208:
 // 9.5 us with 64, 15.3 with 128, 19.5 ping-pong; 8192 rows in 8 groups, 2048 x
-// 4096 into FP32: ping-pong, 168 us, 0.82 PFLOP/s.
+// 4096 into FP32: ping-pong, 164 us, 0.84 PFLOP/s.
 //
 // Order of the tiles: the column tiles of all groups, counted through, go
 // round the XCDs, each with all its row tiles, so every XCD gets an equal part

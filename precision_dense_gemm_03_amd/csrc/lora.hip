@@ -19,8 +19,8 @@
 // adapters are shared out over kLowParts workgroups, one pass each; an
 // adapter's pass stores its own rows. Where the blocks leave compute units
 // idle, K is cut into slices, each with its own array of sums, which every
-// tile of the product adds up (4096 x 4096 x 4096, rank 64, two slices: 157 us
-// for both launches, one 167, four in blocks of 64 rows 159).
+// tile of the product adds up (4096 x 4096 x 4096, rank 64, two slices: 155.4 us
+// for both launches, one 156.3).
 //
 // Any alignment (lora_low_kernel): a workgroup takes 16 rows and its 8 waves
 // share out K in tiles of 64, straight from memory to the matrix cores; every

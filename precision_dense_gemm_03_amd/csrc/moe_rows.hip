@@ -91,7 +91,7 @@ __device__ __forceinline__ void fetch_rows(const int32_t* __restrict__ row, cons
     }
 }
 
-// 16384 tokens of 2048 halves to 131072 rows: 144 us, 7.4 TB/s of reads and
+// 16384 tokens of 2048 halves to 131072 rows: 141 us, 7.4 TB/s of reads and
 // writes together (each token is read again for each of its 8 experts, from
 // beyond the L2s). Rows picked by ranges of tokens, one range per XCD and L2,
 // measured 272 us: the writes then scatter.

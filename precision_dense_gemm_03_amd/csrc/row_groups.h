@@ -17,6 +17,10 @@
 // XCDs, so workgroup b takes the (b / 8)th tile of XCD b % 8. (All the groups'
 // last, partly filled rows of tiles after all others, to level the load with
 // short tiles, measured 5 to 10 % slower: they read the weights again alone.)
+// The height of a share hardly matters: shares of up to 3, 6, 12 and 64 rows
+// of tiles are within 1 % of each other on 16 to 16384 rows in 8 to 64 groups
+// (8192 rows, 8 groups, 4096 x 4096 FP16 280, 281, 281, 281 us; 16384 rows, 16
+// groups, 12288 x 4096 FP8 737, 736, 736, 733).
 #pragma once
 
 #include <hip/hip_runtime.h>
