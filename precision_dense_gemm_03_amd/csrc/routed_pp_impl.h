@@ -107,10 +107,9 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     LoraExtra ext) {
     using T = pp::Pp<ES, BM>;
     LIBGEMM_PP_LDS(T);
-    const int64_t id = wide_block();
-    if (id >= (int64_t)tiles_m * tiles_n) return;
+    if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
-    tile_coords((int)id, tiles_m, tiles_n, tm, tn);
+    tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
     pp::pp_body<ES, OUT, FA, FB, true, false, BM, true, LoraExtra, LINES>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                          tn * 256, eflags, vec_out, lds, ext);
 }

@@ -103,10 +103,9 @@ __global__ __launch_bounds__(256) void lora_ring_kernel(const uint8_t* __restric
     using T = ring::Ring<ES, BM, BN, true, S>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
     __shared__ v4f red[T::RED_SLOTS];
-    const int64_t id = wide_block();
-    if (id >= (int64_t)tiles_m * tiles_n) return;
+    if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
-    tile_coords((int)id, tiles_m, tiles_n, tm, tn);
+    tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
     ring::ring_body<ES, BM, BN, OUT, FA, FB, true, S, true, LoraExtra, P>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                       tn * BN, eflags, vec_out, ring, red, ext);
 }

@@ -70,10 +70,9 @@ __global__ __launch_bounds__(256) void lora_tile_kernel(const uint8_t* __restric
                                                         void* __restrict__ C, int M, int N, int K,
                                                         const float* __restrict__ sA, const float* __restrict__ sB,
                                                         int tiles_m, int tiles_n, int eflags, LoraExtra ext) {
-    const int64_t id = wide_block();
-    if (id >= (int64_t)tiles_m * tiles_n) return;
+    if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
-    tile_coords((int)id, tiles_m, tiles_n, tm, tn);
+    tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
     tile::tile_body<ES, OUT, BM, BM, BK, 2, 2, FA, FB, true, ES, true, LoraExtra>(A, B, C, M, N, K, sA, sB, nullptr, tm * BM,
                                                                            tn * BM, 1, eflags, K, 0, ext);
 }

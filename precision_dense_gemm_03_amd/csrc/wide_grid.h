@@ -24,4 +24,9 @@ inline dim3 wide_grid(int64_t workgroups) {
 
 __device__ __forceinline__ int64_t wide_block() { return ((int64_t)blockIdx.y << kWideBits) + blockIdx.x; }
 
+// Whether this workgroup is past the `count` asked for. Those of y = 0 never
+// are, and need not wait for the count (4 x 11664 x 1040 with adapters: 13.88 us
+// with the wait, 13.84 without).
+__device__ __forceinline__ bool past_last_block(int64_t count) { return blockIdx.y != 0 && wide_block() >= count; }
+
 }  // namespace libgemm
