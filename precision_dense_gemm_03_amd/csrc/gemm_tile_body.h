@@ -420,6 +420,19 @@
                     const int row = row0 + tm * 16 + r, col = col0 + tn * 16;
                     if (row < M && col < N) store_one<OUT>(C, (int64_t)row * N + col, acc[tm][tn][r], eflags);
                 }
+        static_assert(BT && GES == ES, "adapters stand beside K-major weights");
+        auto product = [&](int row, int col) __attribute__((always_inline)) -> float {
+            const uint8_t* pa = A + (int64_t)row * K * ES;
+            const uint8_t* pb = B + (int64_t)col * K * ES;
+            float sum = 0.0f;
+#pragma unroll 1
+            for (int k = 0; k < K; ++k) sum = __builtin_fmaf(element<ES, FA>(pa, k), element<ES, FB>(pb, k), sum);
+            sum *= scale;
+            return chan ? sum * (sA[row] * sB[col]) : sum;
+        };
+        ext.template repair16<T::TM, T::TN>(
+            acc, m0 + wm * T::WTM, n0 + wn * T::WTN, M, N, product,
+            [&](int row, int col, float y) { store_one<OUT>(C, (int64_t)row * N + col, y, eflags); });
         return;
     }
     if (interior_mn) {

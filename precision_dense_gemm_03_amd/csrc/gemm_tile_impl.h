@@ -220,6 +220,14 @@ __device__ __forceinline__ void store_one(void* C, int64_t idx, float y, int efl
     }
 }
 
+// Element k of a row: FP16, or FP8 of format F.
+template <int ES, int F>
+__device__ __forceinline__ float element(const uint8_t* row, int64_t k) {
+    if constexpr (ES == 2) return (float)reinterpret_cast<const _Float16*>(row)[k];
+    else if constexpr (F == FMT_E5M2) return __builtin_amdgcn_cvt_f32_bf8((int)row[k], 0);
+    else return __builtin_amdgcn_cvt_f32_fp8((int)row[k], 0);
+}
+
 // Tiles that the kernels of unaligned operands (UA) hold in registers ahead of
 // the LDS, by tile rows. 64: two (over 240 shapes 0.85 to 0.96 of the time with
 // one; four, which cost occupancy, 1.01 to 1.05 of that with two).

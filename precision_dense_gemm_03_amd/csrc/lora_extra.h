@@ -5,7 +5,8 @@
 //
 // low is FP32 and LB FP16. The tile kernels (add16, add_tile) split each row's
 // low values into two FP16 numbers, hi + lo, after scaling the row's piece of 64
-// by a power of two that puts its largest finite value into [2^14, 2^15). hi
+// by a power of two that puts its largest value into [2^14, 2^15) (an infinity:
+// as if it were 2^127). hi
 // is off by at most 2^-11 of the value and lo by at most 2^-11 of what hi left,
 // or half FP16's smallest step, so a value enters to 2^-22 of itself or 2^-39 of
 // the piece's largest, whichever is more: two bits fewer than FP32 holds. That
@@ -13,8 +14,10 @@
 // a third part would cost half as many matrix instructions again. The deep-ring
 // kernel (add_row4, few rows) multiplies the FP32 values as they are. The
 // scaling is undone on the FP32 sum, exactly. Both halves meet LB's operand,
-// loaded once; infinities and NaN of LB meet hi alone (lo may be zero, or of the
-// other sign).
+// loaded once. An infinity of LB must meet hi alone (lo may be zero, or of the
+// other sign): add_tile looks for them as it stages LB; add16 computes elements
+// that come out as NaN again, element by element (looking at LB's values there,
+// or at each sum, cost 6 to 17 % where rows of many adapters share a block).
 //
 // Rows of one block may have several adapters: each adapter present multiplies
 // the whole block and only its rows take the sum, so no other adapter's values
@@ -103,18 +106,8 @@ struct LoraExtra {
             }
         }
         for (int d = first_d; d < end_d; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-        if (__builtin_amdgcn_ballot_w64(m == __builtin_inff())) {   // infinities: the largest finite value
-            m = 0.0f;
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = __builtin_fabsf(v[s][i]);
-                    if (a < __builtin_inff()) m = fmaxf(m, a);
-                }
-            for (int d = first_d; d < end_d; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-        }
-        const int e = m > 0.0f ? __builtin_amdgcn_frexp_expf(m) - 15 : 0;
+        // (beside an infinity the other values only have to stay finite)
+        const int e = m > 0.0f ? (m < __builtin_inff() ? __builtin_amdgcn_frexp_expf(m) : 128) - 15 : 0;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s)
 #pragma unroll
@@ -153,9 +146,8 @@ struct LoraExtra {
 #pragma unroll
                         for (int s = 0; s < 2; ++s) {
                             if (p0 + 32 * s >= rank_p) break;
-                            v8h b = lb_chunk(a, col, p0 + 8 * (4 * s + g), N);
+                            const v8h b = lb_chunk(a, col, p0 + 8 * (4 * s + g), N);
                             sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(hi[s], b, sum, 0, 0, 0);
-                            if (__builtin_amdgcn_ballot_w64(any_non_finite(b))) b = finite_part(b);
                             sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(lo[s], b, sum, 0, 0, 0);
                         }
 #pragma unroll
@@ -167,6 +159,49 @@ struct LoraExtra {
                 }
             }
         }
+    }
+
+    // After add16 and the stores: elements that came out as NaN, from LB's
+    // infinity against lo or as the formula gives them, again in FP32, one by
+    // one. product(row, col) gives the product alone, store(row, col, y) stores.
+    template <int TM, int TN, class Product, class Store>
+    __device__ __forceinline__ void repair16(const v4f (&acc)[TM][TN], int row0, int col0, int M, int N,
+                                             Product product, Store store) const {
+        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < TM * TN; ++i)
+            nan |= __builtin_isunordered(acc[i / TN][i % TN][0], acc[i / TN][i % TN][1]) |
+                   __builtin_isunordered(acc[i / TN][i % TN][2], acc[i / TN][i % TN][3]);
+        if (__builtin_expect(__builtin_amdgcn_ballot_w64(nan) == 0, 1)) return;
+        const int lane = threadIdx.x & 63, j16 = lane & 15, g = lane >> 4;
+        uint64_t todo = 0;
+#pragma unroll
+        for (int i = 0; i < 4 * TM * TN; ++i) {
+            const float y = acc[i / 4 / TN][i / 4 % TN][i % 4];
+            if (y != y) todo |= (uint64_t)1 << i;
+        }
+#pragma unroll 1
+        for (; todo; todo &= todo - 1) {
+            const int i = __builtin_ctzll(todo);
+            const int row = row0 + 16 * (i / (4 * TN)) + 4 * g + i % 4, col = col0 + 16 * (i / 4 % TN) + j16;
+            const int a = adapter_of(row, M);
+            if (a >= 0 && col < N) store(row, col, product(row, col) + one_term(row, col, a, N));
+        }
+    }
+
+    // One element of the term, in FP32.
+    __device__ __forceinline__ float one_term(int row, int col, int a, int N) const {
+        const float* l = low + (int64_t)row * rank_p;
+        const _Float16* b = LB + ((int64_t)a * N + col) * rank;
+        float sum = 0.0f;
+#pragma unroll 1
+        for (int r = 0; r < rank; ++r) {
+            float v = l[r];
+#pragma unroll 1
+            for (int s = 1; s < slices; ++s) v += l[r + s * low_step];
+            sum = __builtin_fmaf(v, (float)b[r], sum);
+        }
+        return sum;
     }
 
     // A 256-column tile of the ping-pong kernel (its acc, LDS regions and wave
