@@ -661,16 +661,31 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
     }
     }
 
-    if constexpr (Ext::kActive) {   // scaled here (each group its part), added to, stored as it is
+    // With Ext the products are scaled here (each group its part), added to and
+    // stored as they are. Not where a scale of the block is infinite or NaN
+    // (odd): a part that is zero, or of another sign, is not the sum; there the
+    // groups join their parts first.
+    v4f factor[T::TN];
+    bool odd = false;
+    if constexpr (Ext::kActive) {
+        if (chan) {
+            const float sr = sA[min(row, M - 1)];
 #pragma unroll
-        for (int tn = 0; tn < T::TN; ++tn) {
-            acc[tn] *= scale;
-            if (chan) {
-                const float sr = sA[min(row, M - 1)];
+            for (int tn = 0; tn < T::TN; ++tn)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[tn][e] *= sr * sB[min(col_of(tn) + e, N - 1)];
+                for (int e = 0; e < 4; ++e) {
+                    factor[tn][e] = sr * sB[min(col_of(tn) + e, N - 1)];
+                    odd |= !(__builtin_fabsf(factor[tn][e]) < __builtin_inff());
+                }
+            odd = __builtin_amdgcn_ballot_w64(odd) != 0;
+        }
+        if (!odd) {
+#pragma unroll
+            for (int tn = 0; tn < T::TN; ++tn) {
+                acc[tn] *= scale;
+                if (chan) acc[tn] *= factor[tn];
+                ext.add_row4(acc[tn], piece[tn], row, col_of(tn), kg, T::KW, N);
             }
-            ext.add_row4(acc[tn], piece[tn], row, col_of(tn), kg, T::KW, N);
         }
     }
 
@@ -686,6 +701,18 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
         for (int q = 1; q < T::KW; ++q)
 #pragma unroll
             for (int tn = 0; tn < T::TN; ++tn) acc[tn] += red[(((q - 1) * T::WPK + wg) * T::TN + tn) * 64 + lane];
+    }
+    if constexpr (Ext::kActive) {
+        if (odd) {
+            const int a = ext.adapter_of(row, M);
+#pragma unroll
+            for (int tn = 0; tn < T::TN; ++tn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[tn][e] *= scale * factor[tn][e];
+                    if (a >= 0 && col_of(tn) + e < N) acc[tn][e] += ext.one_term(row, col_of(tn) + e, a, N);
+                }
+        }
     }
 
     // ---- epilogue: lane holds row 16 wr + j16 and columns 16 (TN wc + tn) + 4 g + 0..3 ----

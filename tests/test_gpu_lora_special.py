@@ -86,3 +86,43 @@ def test_infinite_weight(name, rank, monkeypatch):
     g.gemm_f16_lora_bt(x, b, la, lb, adapter, torch.ones(2, device=DEV), c)
     assert torch.equal(c.nan_to_num(nan=7.25), want.nan_to_num(nan=7.25))
     assert torch.equal(c.isnan(), want.isnan())
+
+
+@pytest.mark.parametrize("kind", ["f16", (0, 0), (1, 0)], ids=str)
+@pytest.mark.parametrize("name", LORA)
+def test_infinite_weight_beside_other_infinities(name, kind, monkeypatch):
+    """Rows and columns whose product is infinite or NaN already, or FP8: the same as the FP32 formula."""
+    monkeypatch.setenv("LIBGEMM_CONFIG", name)
+    rows, n, k, rank = 70, 272, 64, 5
+    x = torch.zeros((rows, k), dtype=F16, device=DEV)
+    x[:, 0] = 1.0
+    x[3::9, 1] = 1.0
+    x[5::9, 1] = -1.0
+    la = torch.zeros((2, rank, k), dtype=F16, device=DEV)
+    la[:, 1, 0] = 1.0
+    lb = torch.zeros((2, n, rank), dtype=F16, device=DEV)
+    lb[:, :, 1] = 2.0
+    lb[1, 3, 1], lb[1, 130, 1], lb[0, 200, 1] = INF, -INF, INF
+    adapter = (torch.arange(rows, device=DEV) % 3 - 1).to(I32)
+    w = torch.zeros((n, k), dtype=F16, device=DEV)
+    w[:, 0] = 0.5
+    c = torch.full((rows, n), 9.0, dtype=F32, device=DEV)
+    say(f"{name} {kind}")
+    one = torch.ones(2, device=DEV)
+    if kind == "f16":
+        w[3::4, 1], w[2::4, 1] = INF, -INF
+        g.gemm_f16_lora_bt(x, w, la, lb, adapter, one, c)
+        base = x.float() @ w.float().t()
+    else:
+        codes = [t.float().to(torch.float8_e5m2 if f else torch.float8_e4m3fn) for t, f in ((x, kind[0]), (w, kind[1]))]
+        sa = torch.ones(rows, device=DEV)
+        sa[7], sa[8] = INF, 2.0
+        sb = torch.full((n,), 4.0, device=DEV)
+        g.gemm_fp8_lora_bt(codes[0], kind[0], codes[1], kind[1], sa, sb, x, la, lb, adapter, one, c)
+        base = (codes[0].float() @ codes[1].float().t()) * sa[:, None] * sb
+    low = x[:, :1].float()
+    want = base.clone()
+    for e in range(2):
+        want = torch.where((adapter == e)[:, None], base + low * lb[e, :, 1].float(), want)
+    assert torch.equal(c.isnan(), want.isnan())
+    assert torch.equal(c.nan_to_num(nan=7.25), want.nan_to_num(nan=7.25))
