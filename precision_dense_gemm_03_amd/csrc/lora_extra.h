@@ -5,18 +5,19 @@
 //
 // low is FP32 and LB FP16. The tile kernels (add16, add_tile) split each row's
 // low values into two FP16 numbers, hi + lo, after scaling the row's piece of 64
-// by a power of two that puts its largest value into [2^14, 2^15) (an infinity:
-// as if it were 2^127). hi
-// is off by at most 2^-11 of the value and lo by at most 2^-11 of what hi left,
-// or half FP16's smallest step, so a value enters to 2^-22 of itself or 2^-39 of
-// the piece's largest, whichever is more: two bits fewer than FP32 holds. That
-// is the choice made here: K products summed in FP32 are seldom that exact, and
-// a third part would cost half as many matrix instructions again. The deep-ring
-// kernel (add_row4, few rows) multiplies the FP32 values as they are. The
-// scaling is undone on the FP32 sum, exactly. Both halves meet LB's operand,
-// loaded once. An infinity of LB must meet hi alone (lo may be zero, or of the
-// other sign): add_tile looks for them as it stages LB; add16 computes elements
-// that come out as NaN again, element by element (looking at LB's values there,
+// by a power of two that puts its largest value into [2^14, 2^15) (an infinity
+// counts as 2^127). hi is off by at most 2^-11 of the value and lo by at most
+// 2^-11 of what hi left, or half FP16's smallest step, so a value enters to 2^-22
+// of itself or 2^-39 of the piece's largest, whichever is more: two bits fewer
+// than FP32 holds. That is the choice made here: K products summed in FP32 are
+// seldom that exact, and a third part would cost half as many matrix
+// instructions again. The deep-ring kernel (add_row4, few rows) multiplies the
+// FP32 values as they are. The scaling is undone on the FP32 sum, exactly. Both
+// halves meet LB's operand, loaded once.
+//
+// An infinity of LB must meet hi alone (lo may be zero, or of the other sign).
+// add_tile looks for them as it stages LB; the tiles of add16 compute elements
+// that came out as NaN again, one by one (repair16; looking at LB's values there,
 // or at each sum, cost 6 to 17 % where rows of many adapters share a block).
 //
 // Rows of one block may have several adapters: each adapter present multiplies
