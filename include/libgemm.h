@@ -515,6 +515,153 @@ int moe_combine_backward(const void* dy, const void* z, int dtype, const int32_t
                          void* dz, float* dweight, int64_t tokens, int64_t topk, int64_t rows,
                          int64_t width, hipStream_t stream);
 
+/* --------------------------------- a dense layer around its products */
+/* What a network's dense layers do beside their products, with the products: the
+ * norm before them (into FP16, or into FP8 codes with a scale per row as
+ * gemm_fp8_channel takes them), bias, activation and residual in their epilogue,
+ * activations kept in 8 bits for the backward pass, and the gradients. Types of
+ * matrices are GEMM_OUT_F32, GEMM_OUT_F16 and, where codes are taken, GEMM_OUT_E4M3
+ * and GEMM_OUT_E5M2. Biases, norm weights and their gradients are FP32.
+ *
+ * 8-bit values (format fmt): FP8 codes q[rows*cols] and one scale byte e for each 32
+ * values of a row, scale[rows*ceil(cols/32)]: a code stands for FP8(code) 2^(e - 127),
+ * e = 255 for NaN. The scale is the least power of two with max|x| / 2^(e - 127) <=
+ * 448 (57344 for E5M2), over the block's finite values, and 1 where that maximum is
+ * 0; codes are x / 2^(e - 127) rounded to nearest even. NaN gives a NaN code;
+ * infinities do in E4M3 and stay infinities in E5M2. */
+
+/*
+ * rms_norm — h = x + residual, rstd = 1 / sqrt(mean(h^2) + eps), y = h weight rstd,
+ * row by row.
+ *   x, residual  device, [rows*width] of dtype (F32 or F16); residual may be NULL
+ *   weight       device, float[width]
+ *   h            device, [rows*width] of dtype, written (x + residual rounded to
+ *                dtype, which the norm is taken of), or NULL
+ *   y            device, [rows*width], written: F32, F16, or FP8 codes (E4M3, E5M2)
+ *   scale        device, float[rows], written for FP8 y (GEMM_ERR_SCALE if NULL):
+ *                max|y| of the row by the rule of amax_scale_f32 (pow2); the code is
+ *                FP8(y / scale), formed as (h weight)(rstd / scale) in FP32
+ *   rstd         device, float[rows], written, or NULL
+ * Squares are summed in FP32. Outputs overlap neither inputs nor each other.
+ */
+int rms_norm(const void* x, const void* residual, int dtype, const float* weight, float eps, void* h, void* y,
+             int y_dtype, float* scale, int pow2, float* rstd, int64_t rows, int64_t width, hipStream_t stream);
+
+/*
+ * rms_norm_backward — with n = h rstd and g = weight dy:
+ *   dx = rstd (g - n mean(g n)) + dh,   dweight[j] = sum over rows of dy n
+ *   dy, dh, dx  device, [rows*width] of dtype (F32 or F16); dh, the gradient that
+ *               reaches h itself, may be NULL; dx is the gradient of x and residual
+ *   h           device, [rows*width] of h_dtype: F32, F16, or 8-bit values with
+ *               hscale (else ignored)
+ *   rstd        device, float[rows], as rms_norm wrote it
+ *   dweight     device, float[width], written, or NULL
+ *   workspace   device, 16-byte aligned, rms_norm_backward_workspace_size(rows,
+ *               width) bytes; calls that share it must not overlap
+ * Sums over rows are in a fixed order. rows = 0 writes zeros to dweight.
+ */
+int rms_norm_backward(const void* dy, const void* dh, int dtype, const void* h, const uint8_t* hscale, int h_dtype,
+                      const float* weight, const float* rstd, void* dx, float* dweight, int64_t rows, int64_t width,
+                      void* workspace, int64_t workspace_bytes, hipStream_t stream);
+int64_t rms_norm_backward_workspace_size(int64_t rows, int64_t width);
+
+/* Activations: z; max(z, 0); z P(z), P the normal distribution function; 0.5 z (1 +
+ * tanh(sqrt(2/pi)(z + 0.044715 z^3))); z / (1 + exp(-z)). */
+#define GEMM_ACT_NONE 0
+#define GEMM_ACT_RELU 1
+#define GEMM_ACT_GELU 2
+#define GEMM_ACT_GELU_TANH 3
+#define GEMM_ACT_SILU 4
+
+/*
+ * gemm_f16_bias_act — z = A·B + bias, C = act(z) + residual, in one launch.
+ *   A, B       device, as gemm_f16
+ *   bias       device, float[N], or NULL
+ *   residual   device, [M*N] of res_dtype (F32 or F16), or NULL
+ *   C          device, [M*N], F32 or F16 (out_dtype)
+ *   Z          device, [M*N], written with z: F32, F16, or 8-bit values with Zscale
+ *              (z_dtype; GEMM_ERR_SCALE if Zscale is NULL); or NULL
+ * All of it in FP32, each output rounded once. M = 0 or N = 0 is a no-op; K = 0 is
+ * the empty sum. M, N and K are at most 2^31 - 65536. Otherwise as gemm_f16; the _bt
+ * call takes the weight K-major, Bt[N,K].
+ */
+int gemm_f16_bias_act(const void* A, const void* B, const float* bias, const void* residual, int res_dtype, void* C,
+                      int out_dtype, int act, void* Z, uint8_t* Zscale, int z_dtype, int64_t M, int64_t N, int64_t K,
+                      hipStream_t stream);
+int gemm_f16_bias_act_bt(const void* A, const void* Bt, const float* bias, const void* residual, int res_dtype, void* C,
+                         int out_dtype, int act, void* Z, uint8_t* Zscale, int z_dtype, int64_t M, int64_t N,
+                         int64_t K, hipStream_t stream);
+
+/*
+ * gemm_fp8_bias_act — the same for FP8 codes: z = (sA·A)(sB·B) + bias.
+ *   A, fmt_a, B, fmt_b  as gemm_fp8_fmt
+ *   sA, sB   device, one float each (channel = 0), or float[M] and float[N]
+ *   sOut     device, one float: required iff out_dtype is an FP8 output, which is
+ *            FP8((act(z) + residual) / sOut)
+ *   C        F32, F16, E4M3 or E5M2
+ */
+int gemm_fp8_bias_act(const uint8_t* A, int fmt_a, const uint8_t* B, int fmt_b, const float* sA, const float* sB,
+                      int channel, const float* sOut, const float* bias, const void* residual, int res_dtype, void* C,
+                      int out_dtype, int act, void* Z, uint8_t* Zscale, int z_dtype, int64_t M, int64_t N, int64_t K,
+                      hipStream_t stream);
+int gemm_fp8_bias_act_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b, const float* sA, const float* sB,
+                         int channel, const float* sOut, const float* bias, const void* residual, int res_dtype,
+                         void* C, int out_dtype, int act, void* Z, uint8_t* Zscale, int z_dtype, int64_t M, int64_t N,
+                         int64_t K, hipStream_t stream);
+
+/*
+ * bias_act_backward — the gradient of that epilogue: dZ = dy act'(z), dbias[j] = sum
+ * over rows of dZ (FP32, before dZ is rounded, in a fixed order). The residual's
+ * gradient is dy itself; those of A and B are products with dZ.
+ *   dy, dZ   device, [rows*cols] of dtype (F32 or F16)
+ *   Z        device, [rows*cols] of z_dtype: F32, F16, or 8-bit values with Zscale;
+ *            not read for GEMM_ACT_NONE. The derivative of RELU is 0 at 0 and NaN
+ *   dbias    device, float[cols], written; dZ or dbias may be NULL
+ *   workspace  device, 16-byte aligned, bias_act_backward_workspace_size(rows, cols)
+ *            bytes where dbias is asked for; calls that share it must not overlap
+ * rows = 0 writes zeros to dbias.
+ */
+int bias_act_backward(const void* dy, int dtype, const void* Z, const uint8_t* Zscale, int z_dtype, int act, void* dZ,
+                      float* dbias, int64_t rows, int64_t cols, void* workspace, int64_t workspace_bytes,
+                      hipStream_t stream);
+int64_t bias_act_backward_workspace_size(int64_t rows, int64_t cols);
+
+/*
+ * quantize_mx_fp8 — 8-bit values of x[rows*cols] (F32 or F16). Values of F16 x above
+ * 61440 (E5M2: 57344) in magnitude, the largest F16 number with the format's
+ * mantissa, count as that, so that what the codes stand for are F16 numbers.
+ * dequantize_mx_fp8 — what they stand for, as F32 or F16 (nearest even, overflow to
+ * inf).
+ */
+int quantize_mx_fp8(const void* x, int dtype, int64_t rows, int64_t cols, int fmt, uint8_t* q, uint8_t* scale,
+                    hipStream_t stream);
+int dequantize_mx_fp8(const uint8_t* q, const uint8_t* scale, int fmt, int64_t rows, int64_t cols, void* y, int dtype,
+                      hipStream_t stream);
+
+/*
+ * gemm_mx_wgrad — the gradient to the weights with 8-bit activations: C[g] =
+ * X[rows of g]ᵀ · B[rows of g], X the values that Q and Qscale stand for as FP16
+ * numbers (nearest even, overflow to inf); zeros for an empty group.
+ *   Q, Qscale  device, 8-bit values [rows*M] of format fmt
+ *   B          device, _Float16[rows*N]
+ *   offsets    device, int32[groups + 1], as gemm_f16_grouped_wgrad; or NULL: one
+ *              group of all rows (groups = 1)
+ *   C          device, float or _Float16 [groups*M*N]; with q_second the transposed
+ *              product, C[g] = Bᵀ · X, [groups*N*M] (the gradient of a K-major weight)
+ */
+int gemm_mx_wgrad(const uint8_t* Q, const uint8_t* Qscale, int fmt, const void* B, const int32_t* offsets, void* C,
+                  int out_dtype, int64_t rows, int64_t M, int64_t N, int64_t groups, int q_second, hipStream_t stream);
+
+/*
+ * gemm_select_config_bias_act / _mx_wgrad — host-only queries, as
+ * gemm_select_config_grouped: the kernel of gemm_f16_bias_act(_bt) (kind 0),
+ * gemm_fp8_bias_act(_bt) (kind 1; z_dtype of Z, or -1 without) and gemm_mx_wgrad.
+ */
+int gemm_select_config_bias_act(int kind, int out_dtype, int64_t M, int64_t N, int64_t K, int fmt_a, int fmt_b,
+                                int b_kmajor, int z_dtype, char* buf, int buflen);
+int gemm_select_config_mx_wgrad(int out_dtype, int64_t rows, int64_t M, int64_t N, int64_t groups, int q_second,
+                                char* buf, int buflen);
+
 /* Human-readable name of a status code (a static string). */
 const char* gemm_status_str(int status);
 

@@ -64,6 +64,26 @@ Functions keep the C names:
     moe_gather(x, token, y=None, stream=None) -> y
     moe_combine(z, row, weight, y=None, stream=None) -> y
     moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None) -> (dZ, dweight)
+  A dense layer around its products (types from the tensors; 8-bit values are FP8 codes and scale bytes, uint8 or torch's
+  float8_e4m3fn / float8_e5m2 and float8_e8m0fnu, one scale per 32 values of a row):
+    rms_norm(x, weight, y, eps=1e-5, residual=None, h=None, scale=None, rstd=None, pow2=False, out_fmt=None,
+             stream=None) -> y
+    rms_norm_backward(dy, h, weight, rstd, dx=None, dweight=None, dh=None, hscale=None, h_fmt=None, workspace=None,
+                      stream=None) -> (dx, dweight)
+    rms_norm_backward_workspace_size(rows, width) -> int
+    gemm_f16_bias_act(A, B, C, bias=None, act=ACT_NONE, residual=None, Z=None, Zscale=None, z_fmt=None, stream=None)
+    gemm_f16_bias_act_bt(A, Bt, C, ...): the same arguments
+    gemm_fp8_bias_act(A, fmt_a, B, fmt_b, sA, sB, C, bias=None, act=ACT_NONE, residual=None, Z=None, Zscale=None,
+                      channel=False, sOut=None, out_fmt=None, z_fmt=None, stream=None)
+    gemm_fp8_bias_act_bt(A, fmt_a, Bt, fmt_b, sA, sB, C, ...): the same arguments
+    bias_act_backward(dy, Z, act, dZ=None, dbias=None, Zscale=None, z_fmt=None, workspace=None, stream=None)
+        -> (dZ, dbias)
+    bias_act_backward_workspace_size(rows, cols) -> int
+    quantize_mx_fp8(x, fmt=FMT_E4M3, q=None, scale=None, stream=None) -> (q, scale)
+    dequantize_mx_fp8(q, scale, fmt, y, stream=None) -> y
+    gemm_mx_wgrad(q, scale, fmt, B, C, offsets=None, q_second=False, stream=None) -> C
+    select_config_bias_act(kind, out_dtype, M, N, K, fmt_a=0, fmt_b=0, b_kmajor=0, z_dtype=-1) -> str
+    select_config_mx_wgrad(out_dtype, rows, M, N, groups=1, q_second=False) -> str
 Outputs and workspaces that these calls allocate belong to the call's stream.
 The output dtype of a GEMM is taken from C: float32, float16, or 8-bit codes
 (uint8 or torch.float8_e4m3fn: E4M3; torch.float8_e5m2, or uint8 with
@@ -85,6 +105,11 @@ KIND_F16 = 0
 KIND_FP8 = 1
 AXIS_ROW = 0
 AXIS_COL = 1
+ACT_NONE = 0
+ACT_RELU = 1
+ACT_GELU = 2
+ACT_GELU_TANH = 3
+ACT_SILU = 4
 
 GEMM_OK = 0
 STATUS_NAMES = {
@@ -221,6 +246,35 @@ def lib() -> ctypes.CDLL:
     L.moe_combine.argtypes = [vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, vp]
     L.moe_combine_backward.restype = i32
     L.moe_combine_backward.argtypes = [vp, vp, i32, vp, vp, vp, vp, i64, i64, i64, i64, vp]
+    f32 = ctypes.c_float
+    L.rms_norm.restype = i32
+    L.rms_norm.argtypes = [vp, vp, i32, vp, f32, vp, vp, i32, vp, i32, vp, i64, i64, vp]
+    L.rms_norm_backward.restype = i32
+    L.rms_norm_backward.argtypes = [vp, vp, i32, vp, vp, i32, vp, vp, vp, vp, i64, i64, vp, i64, vp]
+    L.rms_norm_backward_workspace_size.restype = i64
+    L.rms_norm_backward_workspace_size.argtypes = [i64, i64]
+    for name in ("gemm_f16_bias_act", "gemm_f16_bias_act_bt"):
+        f = getattr(L, name)
+        f.restype = i32
+        f.argtypes = [vp, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, i64, i64, i64, vp]
+    for name in ("gemm_fp8_bias_act", "gemm_fp8_bias_act_bt"):
+        f = getattr(L, name)
+        f.restype = i32
+        f.argtypes = [vp, i32, vp, i32, vp, vp, i32, vp, vp, vp, i32, vp, i32, i32, vp, vp, i32, i64, i64, i64, vp]
+    L.bias_act_backward.restype = i32
+    L.bias_act_backward.argtypes = [vp, i32, vp, vp, i32, i32, vp, vp, i64, i64, vp, i64, vp]
+    L.bias_act_backward_workspace_size.restype = i64
+    L.bias_act_backward_workspace_size.argtypes = [i64, i64]
+    L.quantize_mx_fp8.restype = i32
+    L.quantize_mx_fp8.argtypes = [vp, i32, i64, i64, i32, vp, vp, vp]
+    L.dequantize_mx_fp8.restype = i32
+    L.dequantize_mx_fp8.argtypes = [vp, vp, i32, i64, i64, vp, i32, vp]
+    L.gemm_mx_wgrad.restype = i32
+    L.gemm_mx_wgrad.argtypes = [vp, vp, i32, vp, vp, vp, i32, i64, i64, i64, i64, i32, vp]
+    L.gemm_select_config_bias_act.restype = i32
+    L.gemm_select_config_bias_act.argtypes = [i32, i32, i64, i64, i64, i32, i32, i32, i32, ctypes.c_char_p, i32]
+    L.gemm_select_config_mx_wgrad.restype = i32
+    L.gemm_select_config_mx_wgrad.argtypes = [i32, i64, i64, i64, i64, i32, ctypes.c_char_p, i32]
     _lib = L
     return L
 
@@ -1136,3 +1190,252 @@ def moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None)
     _check(lib().moe_combine_backward(pdy, _ptr(z), dt, _ptr(row), pw, pdz, pdw, T, K, rows, width,
                                       _stream_handle(stream)), "moe_combine_backward")
     return dZ, dweight
+
+
+# ------------------------------------------- a dense layer around its products
+
+def _mx_codes(q, scale, fmt, what):
+    """Pointers of 8-bit values q[rows, cols] and their scales [rows, ceil(cols / 32)]."""
+    torch = _torch()
+    if q.dim() != 2:
+        raise ValueError(f"{what} must be [rows, cols]")
+    if scale is None:
+        raise ValueError(f"{what} holds 8-bit values: their scales are needed")
+    if scale.dtype != torch.uint8:
+        if scale.dtype != getattr(torch, "float8_e8m0fnu", None):
+            raise ValueError(f"{what}'s scales must be uint8 or float8_e8m0fnu, not {scale.dtype}")
+        scale = scale.view(torch.uint8)
+    shape = (q.shape[0], (q.shape[1] + 31) // 32)
+    return _ptr(_u8(q, fmt)), _arg(scale, torch.uint8, shape, f"{what}'s scales")
+
+
+def _held(t, scale, fmt, shape, what):
+    """(pointer, scales' pointer, type) of a matrix of float32, float16 or 8-bit values."""
+    torch = _torch()
+    dt = _out_dtype(t, fmt)
+    if dt in (OUT_E4M3, OUT_E5M2):
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+        return (*_mx_codes(t, scale, None, what), dt)
+    return _arg(t, t.dtype, torch.Size(shape), what), None, dt
+
+
+def _opt(t, dtype, shape, what):
+    return None if t is None else _arg(t, dtype, shape, what)
+
+
+def rms_norm(x, weight, y, eps=1e-5, residual=None, h=None, scale=None, rstd=None, pow2=False, out_fmt=None, stream=None):
+    """y = h * weight / sqrt(mean(h^2) + eps) row by row, h = x + residual rounded to x's type (written to h when given).
+    x[rows, width], residual and h float32 or float16, weight[width] float32; y float32, float16 or FP8 codes with
+    scale[rows] float32 (max|y| / fmax, or its power of two). rstd[rows] float32, written when given, is what the
+    backward pass takes."""
+    torch = _torch()
+    dt = _float_dtype(x, "x")
+    _need(x, x.dtype, 2, "x")
+    rows, width = shape = x.shape
+    yt = _out_dtype(y, out_fmt)
+    if y.shape != shape:
+        raise ValueError(f"y must have shape {tuple(shape)}, not {tuple(y.shape)}")
+    codes = yt in (OUT_E4M3, OUT_E5M2)
+    if codes and scale is None:
+        raise ValueError("FP8 output needs scale[rows]")
+    f32 = torch.float32
+    _check(lib().rms_norm(_ptr(x), _opt(residual, x.dtype, shape, "residual"), dt, _arg(weight, f32, (width,), "weight"),
+                          eps, _opt(h, x.dtype, shape, "h"), _ptr(_u8(y) if codes else y), yt,
+                          _opt(scale if codes else None, f32, (rows,), "scale"), 1 if pow2 else 0,
+                          _opt(rstd, f32, (rows,), "rstd"), rows, width, _stream_handle(stream)), "rms_norm")
+    return y
+
+
+def rms_norm_backward_workspace_size(rows: int, width: int) -> int:
+    n = int(lib().rms_norm_backward_workspace_size(rows, width))
+    _check(n if n < 0 else 0, "rms_norm_backward_workspace_size")
+    return n
+
+
+def rms_norm_backward(dy, h, weight, rstd, dx=None, dweight=None, dh=None, hscale=None, h_fmt=None, workspace=None,
+                      stream=None):
+    """(dx, dweight) of rms_norm. dy, dh (the gradient of h itself, added to dx) and dx are of one type, float32 or
+    float16; h as rms_norm wrote it, or 8-bit values of it with hscale; rstd[rows] as rms_norm wrote it. dweight is
+    computed when given (None otherwise)."""
+    torch = _torch()
+    dt = _float_dtype(dy, "dy")
+    _need(dy, dy.dtype, 2, "dy")
+    rows, width = shape = dy.shape
+    f32 = torch.float32
+    if dx is None:
+        dx = _new(shape, dy.dtype, dy.device, stream)
+    ph, ps, ht = _held(h, hscale, h_fmt, shape, "h")
+    if workspace is None:
+        n = rms_norm_backward_workspace_size(rows, width)
+        workspace = _new(n, torch.uint8, dy.device, stream) if n else None
+    _check(lib().rms_norm_backward(_ptr(dy), _opt(dh, dy.dtype, shape, "dh"), dt, ph, ps, ht,
+                                   _arg(weight, f32, (width,), "weight"), _arg(rstd, f32, (rows,), "rstd"),
+                                   _arg(dx, dy.dtype, shape, "dx"), _opt(dweight, f32, (width,), "dweight"), rows,
+                                   width, *_ws_args(workspace), _stream_handle(stream)), "rms_norm_backward")
+    return dx, dweight
+
+
+def _epilogue(C, bias, residual, Z, Zscale, z_fmt):
+    """Pointers and types of the epilogue's operands for C[M, N]."""
+    torch = _torch()
+    shape = C.shape
+    pb = _opt(bias, torch.float32, (shape[1],), "bias")
+    pr, rt = None, 0
+    if residual is not None:
+        rt = _float_dtype(residual, "residual")
+        pr = _arg(residual, residual.dtype, shape, "residual")
+    pz, ps, zt = (None, None, 0) if Z is None else _held(Z, Zscale, z_fmt, shape, "Z")
+    return pb, pr, rt, pz, ps, zt
+
+
+def _bias_act_f16(name, A, B, C, bias, act, residual, Z, Zscale, z_fmt, stream, bt):
+    torch = _torch()
+    if A.dtype != torch.float16 or B.dtype != torch.float16:
+        raise ValueError(f"{name} takes float16 operands")
+    M, N, K = _dims_bt(A, B, C) if bt else _dims(A, B, C)
+    pb, pr, rt, pz, ps, zt = _epilogue(C, bias, residual, Z, Zscale, z_fmt)
+    _check(getattr(lib(), name)(_ptr(A), _ptr(B), pb, pr, rt, _ptr(C), _out_dtype(C), int(act), pz, ps, zt, M, N, K,
+                                _stream_handle(stream)), name)
+    return C
+
+
+def gemm_f16_bias_act(A, B, C, bias=None, act=ACT_NONE, residual=None, Z=None, Zscale=None, z_fmt=None, stream=None):
+    """C = act(A @ B + bias) + residual for float16 A[M, K] and B[K, N]; C and residual[M, N] float32 or float16,
+    bias[N] float32. Z, when given, takes A @ B + bias: float32, float16, or 8-bit values with Zscale."""
+    return _bias_act_f16("gemm_f16_bias_act", A, B, C, bias, act, residual, Z, Zscale, z_fmt, stream, False)
+
+
+def gemm_f16_bias_act_bt(A, Bt, C, bias=None, act=ACT_NONE, residual=None, Z=None, Zscale=None, z_fmt=None,
+                         stream=None):
+    """gemm_f16_bias_act with a K-major weight Bt[N, K]."""
+    return _bias_act_f16("gemm_f16_bias_act_bt", A, Bt, C, bias, act, residual, Z, Zscale, z_fmt, stream, True)
+
+
+def _bias_act_fp8(name, A, fmt_a, B, fmt_b, sA, sB, C, bias, act, residual, Z, Zscale, channel, sOut, out_fmt, z_fmt,
+                  stream, bt):
+    torch = _torch()
+    A, B = _u8(A, fmt_a), _u8(B, fmt_b)
+    out = _out_dtype(C, out_fmt)
+    codes = out in (OUT_E4M3, OUT_E5M2)
+    Cv = _u8(C) if codes else C
+    M, N, K = _dims_bt(A, B, Cv) if bt else _dims(A, B, Cv)
+    for what, s, n in (("sA", sA, M if channel else 1), ("sB", sB, N if channel else 1),
+                       ("sOut", sOut if codes else None, 1)):
+        if s is not None and (s.dtype != torch.float32 or s.numel() != n):
+            raise ValueError(f"{what} must hold {n} float32 scales")
+    pb, pr, rt, pz, ps, zt = _epilogue(Cv, bias, residual, Z, Zscale, z_fmt)
+    _check(getattr(lib(), name)(_ptr(A), int(fmt_a), _ptr(B), int(fmt_b), _ptr(sA), _ptr(sB), 1 if channel else 0,
+                                _ptr(sOut) if codes else None, pb, pr, rt, _ptr(Cv), out, int(act), pz, ps, zt, M, N,
+                                K, _stream_handle(stream)), name)
+    return C
+
+
+def gemm_fp8_bias_act(A, fmt_a, B, fmt_b, sA, sB, C, bias=None, act=ACT_NONE, residual=None, Z=None, Zscale=None,
+                      channel=False, sOut=None, out_fmt=None, z_fmt=None, stream=None):
+    """C = act((sA*A) @ (sB*B) + bias) + residual for FP8 codes; sA and sB one float32 scale each, or with channel
+    sA[M] and sB[N]. C float32, float16 or FP8 codes (divided by sOut); the rest as gemm_f16_bias_act."""
+    return _bias_act_fp8("gemm_fp8_bias_act", A, fmt_a, B, fmt_b, sA, sB, C, bias, act, residual, Z, Zscale, channel,
+                         sOut, out_fmt, z_fmt, stream, False)
+
+
+def gemm_fp8_bias_act_bt(A, fmt_a, Bt, fmt_b, sA, sB, C, bias=None, act=ACT_NONE, residual=None, Z=None, Zscale=None,
+                         channel=False, sOut=None, out_fmt=None, z_fmt=None, stream=None):
+    """gemm_fp8_bias_act with a K-major weight Bt[N, K]."""
+    return _bias_act_fp8("gemm_fp8_bias_act_bt", A, fmt_a, Bt, fmt_b, sA, sB, C, bias, act, residual, Z, Zscale,
+                         channel, sOut, out_fmt, z_fmt, stream, True)
+
+
+def select_config_bias_act(kind: int, out_dtype: int, M: int, N: int, K: int, fmt_a: int = 0, fmt_b: int = 0,
+                           b_kmajor: int = 0, z_dtype: int = -1) -> str:
+    """The kernel that the products with bias, activation and residual would launch for 16-byte aligned operands."""
+    buf = ctypes.create_string_buffer(128)
+    _check(lib().gemm_select_config_bias_act(kind, out_dtype, M, N, K, int(fmt_a), int(fmt_b), int(b_kmajor),
+                                             int(z_dtype), buf, len(buf)), "gemm_select_config_bias_act")
+    return buf.value.decode()
+
+
+def bias_act_backward_workspace_size(rows: int, cols: int) -> int:
+    n = int(lib().bias_act_backward_workspace_size(rows, cols))
+    _check(n if n < 0 else 0, "bias_act_backward_workspace_size")
+    return n
+
+
+def bias_act_backward(dy, Z, act, dZ=None, dbias=None, Zscale=None, z_fmt=None, workspace=None, stream=None):
+    """(dZ, dbias) of the epilogue act(z) + residual, z = product + bias: dZ = dy * act'(z), dbias its column sums.
+    dy and dZ are of one type, float32 or float16; Z float32, float16 or 8-bit values with Zscale (None for ACT_NONE).
+    dbias is computed when given (None otherwise)."""
+    torch = _torch()
+    dt = _float_dtype(dy, "dy")
+    _need(dy, dy.dtype, 2, "dy")
+    rows, cols = shape = dy.shape
+    if dZ is None:
+        dZ = _new(shape, dy.dtype, dy.device, stream)
+    pz, ps, zt = (None, None, 0) if Z is None else _held(Z, Zscale, z_fmt, shape, "Z")
+    if workspace is None and dbias is not None:
+        n = bias_act_backward_workspace_size(rows, cols)
+        workspace = _new(n, torch.uint8, dy.device, stream) if n else None
+    _check(lib().bias_act_backward(_ptr(dy), dt, pz, ps, zt, int(act), _arg(dZ, dy.dtype, shape, "dZ"),
+                                   _opt(dbias, torch.float32, (cols,), "dbias"), rows, cols, *_ws_args(workspace),
+                                   _stream_handle(stream)), "bias_act_backward")
+    return dZ, dbias
+
+
+def quantize_mx_fp8(x, fmt=FMT_E4M3, q=None, scale=None, stream=None):
+    """8-bit values of float32 or float16 x[rows, cols]: (codes[rows, cols], scale[rows, ceil(cols / 32)]), a power of
+    two 2^(scale - 127) per 32 values of a row."""
+    torch = _torch()
+    dt = _float_dtype(x, "x")
+    _need(x, x.dtype, 2, "x")
+    rows, cols = x.shape
+    if q is None:
+        q = _new((rows, cols), torch.uint8, x.device, stream)
+    if scale is None:
+        scale = _new((rows, (cols + 31) // 32), torch.uint8, x.device, stream)
+    if q.shape != x.shape:
+        raise ValueError(f"q must have shape {tuple(x.shape)}, not {tuple(q.shape)}")
+    pq, ps = _mx_codes(q, scale, fmt, "q")
+    _check(lib().quantize_mx_fp8(_ptr(x), dt, rows, cols, int(fmt), pq, ps, _stream_handle(stream)), "quantize_mx_fp8")
+    return q, scale
+
+
+def dequantize_mx_fp8(q, scale, fmt, y, stream=None):
+    """What 8-bit values stand for, into float32 or float16 y[rows, cols]."""
+    dt = _float_dtype(y, "y")
+    pq, ps = _mx_codes(q, scale, fmt, "q")
+    rows, cols = q.shape
+    _check(lib().dequantize_mx_fp8(pq, ps, int(fmt), rows, cols, _arg(y, y.dtype, q.shape, "y"), dt,
+                                   _stream_handle(stream)), "dequantize_mx_fp8")
+    return y
+
+
+def gemm_mx_wgrad(q, scale, fmt, B, C, offsets=None, q_second=False, stream=None):
+    """X.T @ B for 8-bit values X (q[rows, M], scale) and float16 B[rows, N], into float32 or float16 C[M, N]; with
+    q_second B.T @ X into C[N, M]. With offsets[groups + 1] one product per group of rows, C[groups, ...]."""
+    torch = _torch()
+    pq, ps = _mx_codes(q, scale, fmt, "q")
+    rows, M = q.shape
+    _need(B, torch.float16, 2, "B")
+    N = B.shape[1]
+    if B.shape[0] != rows:
+        raise ValueError(f"q and B must have the same rows, not {rows} and {B.shape[0]}")
+    one = (N, M) if q_second else (M, N)
+    groups = 1
+    if offsets is not None:
+        _need(offsets, torch.int32, 1, "offsets")
+        groups = offsets.shape[0] - 1
+        one = (groups, *one)
+    if groups < 0:
+        raise ValueError("offsets must hold groups + 1 values")
+    ct = _float_dtype(C, "C")
+    _check(lib().gemm_mx_wgrad(pq, ps, int(fmt), _ptr(B), _ptr(offsets), _arg(C, C.dtype, one, "C"), ct, rows, M, N,
+                               groups, 1 if q_second else 0, _stream_handle(stream)), "gemm_mx_wgrad")
+    return C
+
+
+def select_config_mx_wgrad(out_dtype: int, rows: int, M: int, N: int, groups: int = 1, q_second: bool = False) -> str:
+    """The kernel that gemm_mx_wgrad would launch for 16-byte aligned operands."""
+    buf = ctypes.create_string_buffer(128)
+    _check(lib().gemm_select_config_mx_wgrad(out_dtype, rows, M, N, groups, 1 if q_second else 0, buf, len(buf)),
+           "gemm_select_config_mx_wgrad")
+    return buf.value.decode()

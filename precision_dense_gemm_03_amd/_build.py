@@ -22,7 +22,9 @@ SOURCES = ["abi.cpp", "selector.cpp", "amax_quant.hip", "amax_quant_channel.hip"
            "amax_quant_pair.hip", "gemm_ring.hip", "gemm_ring_mixed.hip", "noalloc.hip", "gemm_pp_exact.hip",
            "abi_routed.cpp", "routed.cpp", "routed_tile_f16.hip", "routed_tile_fp8.hip", "lora.hip", "gemm_wgrad.hip",
            "moe_route.hip", "moe_rows.hip", "routed_pp_f16.hip", "routed_pp_fp8.hip", "routed_pp_mixed.hip",
-           "routed_ring_f16.hip", "routed_ring_fp8.hip"]
+           "routed_ring_f16.hip", "routed_ring_fp8.hip", "abi_dense.cpp", "bias_act.cpp", "bias_act_pp.hip",
+           "bias_act_pp_mixed.hip", "bias_act_ring_f16.hip", "bias_act_ring_fp8.hip", "bias_act_tile.hip",
+           "gemm_wgrad_mx.hip", "rms_norm.hip", "act_backward.hip", "mx.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

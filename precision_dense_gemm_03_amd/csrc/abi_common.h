@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
+#include <cstdio>
 
 #include "libgemm.h"
 
@@ -42,6 +43,42 @@ inline int status_of(hipError_t e) {
     if (e == hipSuccess) return GEMM_OK;
     (void)hipGetLastError();
     return GEMM_ERR_LAUNCH;
+}
+
+struct Range {
+    const void* p;
+    int64_t n;
+};
+
+// Every written range against every other range.
+template <int W, int R>
+bool aliased(const Range (&written)[W], const Range (&read)[R]) {
+    for (int i = 0; i < W; ++i) {
+        for (int j = 0; j < R; ++j)
+            if (overlaps(written[i].p, written[i].n, read[j].p, read[j].n)) return true;
+        for (int j = i + 1; j < W; ++j)
+            if (overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return true;
+    }
+    return false;
+}
+
+constexpr int64_t kMaxRowGroups = 4096;
+
+// The product kernels count rows, columns and K in 32 bits up to the end of a
+// tile (which starts at any row of a group) or of the steps loaded ahead: less
+// than 2^16 past the size.
+inline bool size_ok(int64_t d) { return d >= 0 && d <= ((int64_t)1 << 31) - (1 << 16); }
+
+inline bool fmt_ok(int f) { return f == GEMM_FMT_E4M3 || f == GEMM_FMT_E5M2; }
+
+// a * b * c * es below the byte limit, with a * b below 2^62 first.
+inline bool bytes3_ok(int64_t a, int64_t b, int64_t c, int64_t es) { return bytes_ok(a, b, es) && bytes_ok(a * b, c, es); }
+
+// The answer of the host-only queries.
+inline int put_name(const char* name, char* buf, int buflen) {
+    if (!buf || buflen <= 0) return GEMM_ERR_NULL;
+    std::snprintf(buf, (size_t)buflen, "%s", name);
+    return GEMM_OK;
 }
 
 }  // namespace libgemm

@@ -1,8 +1,6 @@
 // C-ABI entry points of the products whose weight depends on the row (grouped
 // by expert, per-row adapters) and of expert routing (include/libgemm.h).
 // Arguments are validated before any HIP call, as in abi.cpp.
-#include <cstdio>
-
 #include "abi_common.h"
 #include "kernels.h"
 #include "moe.h"
@@ -10,35 +8,6 @@
 using namespace libgemm;
 
 namespace {
-
-struct Range {
-    const void* p;
-    int64_t n;
-};
-
-// Every written range against every other range.
-template <int W, int R>
-bool aliased(const Range (&written)[W], const Range (&read)[R]) {
-    for (int i = 0; i < W; ++i) {
-        for (int j = 0; j < R; ++j)
-            if (overlaps(written[i].p, written[i].n, read[j].p, read[j].n)) return true;
-        for (int j = i + 1; j < W; ++j)
-            if (overlaps(written[i].p, written[i].n, written[j].p, written[j].n)) return true;
-    }
-    return false;
-}
-
-constexpr int64_t kMaxRowGroups = 4096;
-
-// The product kernels count rows, columns and K in 32 bits up to the end of a
-// tile (which starts at any row of a group) or of the steps loaded ahead: less
-// than 2^16 past the size.
-bool size_ok(int64_t d) { return d >= 0 && d <= ((int64_t)1 << 31) - (1 << 16); }
-
-bool fmt_ok(int f) { return f == GEMM_FMT_E4M3 || f == GEMM_FMT_E5M2; }
-
-// a * b * c * es below the byte limit, with a * b below 2^62 first.
-bool bytes3_ok(int64_t a, int64_t b, int64_t c, int64_t es) { return bytes_ok(a, b, es) && bytes_ok(a * b, c, es); }
 
 int run_grouped(int kind, const GroupedArgs& a) {
     const int st = check_device();
@@ -211,12 +180,6 @@ int gemm_fp8_lora_bt(const uint8_t* A, int fmt_a, const uint8_t* Bt, int fmt_b, 
                      void* workspace, int64_t workspace_bytes, hipStream_t stream) {
     return lora_common(KIND_FP8, A, fmt_a, Bt, fmt_b, sA, sB, X, LA, LB, adapter, lscale, C, out_dtype, rows, N, K,
                        rank, adapters, workspace, workspace_bytes, stream);
-}
-
-static int put_name(const char* name, char* buf, int buflen) {
-    if (!buf || buflen <= 0) return GEMM_ERR_NULL;
-    std::snprintf(buf, (size_t)buflen, "%s", name);
-    return GEMM_OK;
 }
 
 static bool kinds_ok(int kind, int out_dtype, int most_out, int fmt_a, int fmt_b) {

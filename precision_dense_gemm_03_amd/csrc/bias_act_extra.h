@@ -1,0 +1,507 @@
+// What the products with bias, activation and residual do with a tile's sums, in
+// place of the plain kernels' scaling and store:
+//
+//   z = s acc + bias,  y = act(z) + residual,  C = y (FP8: y / sOut)
+//
+// s the scales' product, FP32 throughout; z itself is stored too where the backward
+// pass wants it, as FP32 or FP16 or as 8-bit values (row_io.h), whose blocks of 32
+// columns a wave holds whole. Types and activation are chosen at run time, once
+// per tile and not per element: the kernels differ in their operands only.
+#pragma once
+
+#include "act.h"
+#include "kernels.h"
+#include "norm.h"
+#include "row_io.h"
+
+namespace libgemm {
+
+// f(IntC<ACT>) for the activation of a call.
+template <class F>
+__device__ __forceinline__ void with_activation(int act, F f) {
+    switch (act) {
+        case ACT_RELU: f(IntC<ACT_RELU>{}); break;
+        case ACT_GELU: f(IntC<ACT_GELU>{}); break;
+        case ACT_GELU_TANH: f(IntC<ACT_GELU_TANH>{}); break;
+        case ACT_SILU: f(IntC<ACT_SILU>{}); break;
+        default: break;
+    }
+}
+
+typedef unsigned int u32_b1 __attribute__((aligned(1)));
+
+struct BiasActExtra {
+    static constexpr bool kActive = false, kStores = false, kFinish = true;
+    const float* sA;
+    const float* sB;
+    const float* sOut;       // FP8 outputs
+    const float* bias;       // [N] or NULL
+    const void* residual;    // [M, N] or NULL
+    void* C;
+    void* Z;                 // or NULL
+    uint8_t* zscale;
+    int act, res_dtype, out_dtype, z_dtype;
+    int channel;             // sA[M] and sB[N], else one each (or NULL)
+
+    // The factor of every element (per channel: beside sA[i] sB[j]).
+    __device__ __forceinline__ float common() const { return channel ? 1.0f : (sA ? *sA : 1.0f) * (sB ? *sB : 1.0f); }
+    __device__ __forceinline__ float out_factor() const { return out_dtype >= OUT_E4M3 ? 1.0f / *sOut : 1.0f; }
+
+    // Four neighbouring values of a row of FP32s, zero from N on.
+    static __device__ __forceinline__ v4f row4(const float* p, int col, int N) {
+        if (col + 4 <= N) return __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + col)));
+        v4f v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = col + e < N ? p[col + e] : 0.0f;
+        return v;
+    }
+
+    __device__ __forceinline__ v4f residual4(int row, int col, int N) const {
+        const int64_t at = (int64_t)row * N;
+        if (res_dtype == OUT_F32) return row4(reinterpret_cast<const float*>(residual) + at, col, N);
+        const _Float16* p = reinterpret_cast<const _Float16*>(residual) + at + col;
+        typedef _Float16 v4hh __attribute__((ext_vector_type(4)));
+        v4f v;
+        if (col + 4 <= N) {
+            const v4hh h = __builtin_bit_cast(v4hh, v2u(*reinterpret_cast<const v2u_b1*>(p)));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = (float)h[e];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = col + e < N ? (float)p[e] : 0.0f;
+        }
+        return v;
+    }
+
+    // Four neighbouring values to an [M, N] matrix of a type.
+    static __device__ __forceinline__ void put4(void* base, int dtype, int row, int col, int N, v4f y) {
+        const int64_t at = (int64_t)row * N + col;
+        if (col + 4 <= N) {
+            if (dtype == OUT_F32) {
+                *reinterpret_cast<v4u_b1*>(reinterpret_cast<float*>(base) + at) = __builtin_bit_cast(v4u, y);
+            } else if (dtype == OUT_F16) {
+                typedef _Float16 v4hh __attribute__((ext_vector_type(4)));
+                const v4hh h = {(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+                *reinterpret_cast<v2u_b1*>(reinterpret_cast<_Float16*>(base) + at) = __builtin_bit_cast(v2u, h);
+            } else {
+                *reinterpret_cast<u32_b1*>(reinterpret_cast<uint8_t*>(base) + at) =
+                    dtype == OUT_E5M2 ? e5m2_pack4(y[0], y[1], y[2], y[3]) : e4m3_pack4(y[0], y[1], y[2], y[3]);
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < N) store_out(base, at + e, y[e], dtype);
+    }
+
+    // 8-bit values of z: the block's exponent from its largest finite magnitude.
+    __device__ __forceinline__ int exponent(float m) const {
+        return z_dtype == OUT_E5M2 ? mx_exponent<FMT_E5M2>(m) : mx_exponent<FMT_E4M3>(m);
+    }
+    __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) const {
+        return z_dtype == OUT_E5M2 ? mx_pack4<FMT_E5M2>(a, b, c, d) : mx_pack4<FMT_E4M3>(a, b, c, d);
+    }
+    __device__ __forceinline__ void put_exponent(int row, int col, int N, int e) const {
+        zscale[(int64_t)row * ((N + kMxBlock - 1) / kMxBlock) + col / kMxBlock] = (uint8_t)(e + 127);
+    }
+
+    // One element (decode kernels): acc is scaled already, per-channel factors too.
+    __device__ __forceinline__ void finish1(float z, int row, int col, int N) const {
+        if (bias) z += bias[col];
+        const int64_t at = (int64_t)row * N + col;
+        if (Z) store_out(Z, at, z, z_dtype);
+        float y = z;
+        with_activation(act, [&](auto a) __attribute__((always_inline)) { y = activate<decltype(a)::value>(z); });
+        if (residual)
+            y += res_dtype == OUT_F32 ? reinterpret_cast<const float*>(residual)[at]
+                                      : (float)reinterpret_cast<const _Float16*>(residual)[at];
+        store_out(C, at, y * out_factor(), out_dtype);
+    }
+
+    // The deep-ring kernel: four neighbouring columns per lane and block, block tn at
+    // columns col0 + 16 tn. Bias and residual are fetched before the K loop.
+    struct Piece {
+        v4f bias, residual;
+    };
+
+    __device__ __forceinline__ void prefetch(Piece& p, int row, int col, int kg, int M, int N) const {
+        p.bias = p.residual = v4f{0.f, 0.f, 0.f, 0.f};
+        if (kg != 0) return;
+        if (bias) p.bias = row4(bias, col, N);
+        if (residual && row < M) p.residual = residual4(row, col, N);
+    }
+
+    template <int TN>
+    __device__ __forceinline__ void finish_ring(v4f (&acc)[TN], const Piece (&piece)[TN], int row, int col0, int M,
+                                                int N) const {
+        if (row >= M) return;
+        const float s = common();
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) {
+            acc[tn] *= s;
+            if (channel) acc[tn] *= sA[row] * row4(sB, col0 + 16 * tn, N);
+            acc[tn] += piece[tn].bias;
+        }
+        if (Z && z_dtype < OUT_E4M3) {
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn) put4(Z, z_dtype, row, col0 + 16 * tn, N, acc[tn]);
+        } else if (Z) {
+            // (the host asks only kernels for this whose waves hold 32 columns and more)
+            if constexpr (TN >= 2) {
+#pragma unroll
+                for (int t = 0; t < TN; t += 2) {
+                    float m = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float x = finite_abs(acc[t + e / 4][e % 4]);
+                        if (col0 + 16 * (t + e / 4) + e % 4 < N) m = fmaxf(m, x);
+                    }
+                    m = fmaxf(m, __shfl_xor(m, 16, 64));
+                    m = fmaxf(m, __shfl_xor(m, 32, 64));
+                    const int e = exponent(m);
+                    const float inv = mx_inverse(e);
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const v4f v = acc[t + u] * inv;
+                        const uint32_t w = codes4(v[0], v[1], v[2], v[3]);
+                        const int col = col0 + 16 * (t + u);
+                        uint8_t* p = reinterpret_cast<uint8_t*>(Z) + (int64_t)row * N + col;
+                        if (col + 4 <= N) {
+                            *reinterpret_cast<u32_b1*>(p) = w;
+                        } else {
+#pragma unroll
+                            for (int b = 0; b < 4; ++b)
+                                if (col + b < N) p[b] = (uint8_t)(w >> (8 * b));
+                        }
+                    }
+                    // lanes 0 to 15 hold the block's first columns
+                    if ((threadIdx.x & 63) < 16 && col0 + 16 * t < N) put_exponent(row, col0 + 16 * t, N, e);
+                }
+            }
+        }
+        with_activation(act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[tn][e] = activate<decltype(a)::value>(acc[tn][e]);
+        });
+        const float f = out_factor();
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) put4(C, out_dtype, row, col0 + 16 * tn, N, (acc[tn] + piece[tn].residual) * f);
+    }
+
+    // The register-staged kernel: acc[tm][tn][r] is row row0 + 16 tm + r, column
+    // col0 + 16 tn; the 16 lanes of a group hold neighbouring columns.
+    template <int TM, int TN>
+    __device__ __forceinline__ void finish_tile16(v4f (&acc)[TM][TN], int row0, int col0, int M, int N) const {
+        static_assert(TN % 2 == 0, "blocks of 32 columns");
+        const float s = common(), f = out_factor();
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) {
+            const int col = min(col0 + 16 * tn, N - 1);
+            const float b = bias ? bias[col] : 0.0f, sb = channel ? sB[col] : 1.0f;
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float v = acc[tm][tn][r] * s;
+                    if (channel) v *= sA[min(row0 + 16 * tm + r, M - 1)] * sb;
+                    acc[tm][tn][r] = v + b;
+                }
+        }
+        if (Z && z_dtype < OUT_E4M3) {
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = row0 + 16 * tm + r, col = col0 + 16 * tn;
+                        if (row < M && col < N) store_out(Z, (int64_t)row * N + col, acc[tm][tn][r], z_dtype);
+                    }
+        } else if (Z) {
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int t = 0; t < TN; t += 2)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int row = row0 + 16 * tm + r;
+                        float m = 0.0f;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            if (col0 + 16 * (t + u) < N) m = fmaxf(m, finite_abs(acc[tm][t + u][r]));
+#pragma unroll
+                        for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
+                        const int e = exponent(m);
+                        const float inv = mx_inverse(e);
+                        if (row >= M) continue;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int col = col0 + 16 * (t + u);
+                            if (col < N)
+                                reinterpret_cast<uint8_t*>(Z)[(int64_t)row * N + col] =
+                                    (uint8_t)codes4(acc[tm][t + u][r] * inv, 0.0f, 0.0f, 0.0f);
+                        }
+                        if ((threadIdx.x & 15) == 0 && col0 + 16 * t < N) put_exponent(row, col0 + 16 * t, N, e);
+                    }
+        }
+        with_activation(act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+            for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+                for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) acc[tm][tn][r] = activate<decltype(a)::value>(acc[tm][tn][r]);
+        });
+#pragma unroll
+        for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = row0 + 16 * tm + r, col = col0 + 16 * tn;
+                    if (row >= M || col >= N) continue;
+                    const int64_t at = (int64_t)row * N + col;
+                    float y = acc[tm][tn][r];
+                    if (residual)
+                        y += res_dtype == OUT_F32 ? reinterpret_cast<const float*>(residual)[at]
+                                                  : (float)reinterpret_cast<const _Float16*>(residual)[at];
+                    store_out(C, at, y * f, out_dtype);
+                }
+    }
+
+    // The ping-pong kernel (its acc, LDS regions and wave layout, gemm_pp_impl.h):
+    // acc[i][j] holds row MR G + 32 i + lane % 32, columns 64 wj + 32 j + 8 q + 4
+    // (lane / 32) + e in value 4 q + e. After the K loop the LDS is free: FP16 and
+    // 8-bit values go through a wave's own part of it, so that memory is read and
+    // written in 16-byte pieces of rows. A wave takes 32 of its rows through all steps
+    // and then the next 32: with each step over all rows at once the sums, changed in
+    // the branches of the run-time types, took twice their registers (593 spilled).
+    template <int MI, class Lds>
+    __device__ __forceinline__ void finish_pp(const v16f (&acc)[MI][2], const Lds& lds, int m0, int n0, int G, int wj,
+                                              int M, int N) const {
+        constexpr int MR = 32 * MI, STAGE = 64 * MI * 64;
+        static_assert(STAGE >= 3 * kPart, "three parts of the wave's LDS");
+        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+        const int col0 = n0 + 64 * wj, lcol = col0 + 4 * h;   // of the wave's block; of this lane: + 32 j + 8 q
+        LDS_AS uint8_t* ep = G == 0 ? (wj == 0 ? lds.b[0] : wj == 1 ? lds.b[1] : wj == 2 ? lds.b[2] : lds.b[3])
+                                    : (wj < 2 ? lds.a[0] : lds.a[1]) + (wj & 1) * STAGE;
+        const float s = common(), f = out_factor();
+        const bool res16 = residual && res_dtype == OUT_F16;
+        auto rows32 = [&](int i, const v16f& left, const v16f& right) __attribute__((always_inline)) {
+            const int row0 = m0 + MR * G + 32 * i, row = row0 + lr;
+            if (row0 >= M) return;
+            v4u held[4];
+            if (res16) fetch16(held, row0, col0, M, N);
+            const float sr = channel ? sA[min(row, M - 1)] : 1.0f;
+            float v[2][16];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int col = lcol + 32 * j + 8 * q;
+                    const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+                    const v4f b = bias ? row4(bias, col, N) : zero;
+                    const v4f sb = channel ? row4(sB, col, N) : zero;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float y = (j == 0 ? left : right)[4 * q + e] * s;
+                        if (channel) y *= sr * sb[e];
+                        v[j][4 * q + e] = y + b[e];
+                    }
+                }
+            if (Z) {
+                if (z_dtype == OUT_F32) put_f32(Z, v, row, lcol, M, N);
+                else if (z_dtype == OUT_F16) put_f16(Z, v, ep, row0, col0, M, N);
+                else put_mx(v, ep, row0, col0, M, N);
+            }
+            with_activation(act, [&](auto a) __attribute__((always_inline)) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) v[j][x] = activate<decltype(a)::value>(v[j][x]);
+            });
+            if (res16) {
+                add16(v, held, ep + kPart);
+            } else if (residual && row < M) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const v4f r = residual4(row, lcol + 32 * j + 8 * q, N);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[j][4 * q + e] += r[e];
+                    }
+            }
+            if (out_dtype == OUT_F32) {
+                put_f32(C, v, row, lcol, M, N);
+            } else if (out_dtype == OUT_F16) {
+                put_f16(C, v, ep + 2 * kPart, row0, col0, M, N);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float y[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[e] = v[j][4 * q + e] * f;
+                        stage8(ep + 2 * kPart, lr, 32 * j + 8 * q + 4 * h,
+                               out_dtype == OUT_E5M2 ? e5m2_pack4(y[0], y[1], y[2], y[3])
+                                                     : e4m3_pack4(y[0], y[1], y[2], y[3]));
+                    }
+                drain8(reinterpret_cast<uint8_t*>(C), ep + 2 * kPart, row0, col0, M, N);
+            }
+        };
+        rows32(0, acc[0][0], acc[0][1]);
+        rows32(1, acc[1][0], acc[1][1]);
+        rows32(2, acc[2][0], acc[2][1]);
+        if constexpr (MI > 3) rows32(3, acc[3][0], acc[3][1]);
+    }
+
+private:
+    typedef _Float16 v4hh __attribute__((ext_vector_type(4)));
+    static constexpr int kPart = 4096;   // 32 rows of 64 halves
+
+    static __device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+    static __device__ __forceinline__ void put_f32(void* base, const float (&v)[2][16], int row, int lcol, int M, int N) {
+        if (row >= M) return;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (lcol + 32 * j + 8 * q < N)
+                    put4(base, OUT_F32, row, lcol + 32 * j + 8 * q, N,
+                         v4f{v[j][4 * q], v[j][4 * q + 1], v[j][4 * q + 2], v[j][4 * q + 3]});
+    }
+
+    // 32 FP16 rows in LDS: 128 bytes a row, 16-byte chunk c of row r at slot c ^ (r / 2
+    // % 8): 32 rows at one column, or 8 rows whole, meet distinct banks.
+    static __device__ __forceinline__ LDS_AS uint8_t* at16(LDS_AS uint8_t* ep, int r, int byte) {
+        return ep + r * 128 + ((((byte >> 4) ^ ((r >> 1) & 7)) << 4) | (byte & 15));
+    }
+
+    static __device__ __forceinline__ void put_f16(void* base, const float (&v)[2][16], LDS_AS uint8_t* ep, int row0,
+                                                   int col0, int M, int N) {
+        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v4hh x = {(_Float16)v[j][4 * q], (_Float16)v[j][4 * q + 1], (_Float16)v[j][4 * q + 2],
+                                (_Float16)v[j][4 * q + 3]};
+                *(LDS_AS v2i*)at16(ep, lr, 2 * (32 * j + 8 * q + 4 * h)) = __builtin_bit_cast(v2i, x);
+            }
+        lds_done();
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int r = 8 * p + (lane >> 3), seg = lane & 7, row = row0 + r, col = col0 + 8 * seg;
+            const v4u w = *(const LDS_AS v4u*)at16(ep, r, 16 * seg);
+            if (row >= M || col >= N) continue;
+            _Float16* d = reinterpret_cast<_Float16*>(base) + (int64_t)row * N + col;
+            if (col + 8 <= N) {
+                *reinterpret_cast<v4u_b1*>(d) = w;
+            } else {
+                const v8h x = __builtin_bit_cast(v8h, w);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < N) d[e] = x[e];
+            }
+        }
+        lds_done();   // the part may be written again
+    }
+
+    // 32 rows of the FP16 residual, in 16-byte pieces of rows.
+    __device__ __forceinline__ void fetch16(v4u (&held)[4], int row0, int col0, int M, int N) const {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int row = row0 + 8 * p + (lane >> 3), col = col0 + 8 * (lane & 7);
+            const _Float16* s = reinterpret_cast<const _Float16*>(residual) + (int64_t)row * N + col;
+            held[p] = v4u{0u, 0u, 0u, 0u};
+            if (row < M && col + 8 <= N) {
+                held[p] = *reinterpret_cast<const v4u_b1*>(s);
+            } else if (row < M && col < N) {
+                v8h x = __builtin_bit_cast(v8h, held[p]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (col + e < N) x[e] = s[e];
+                held[p] = __builtin_bit_cast(v4u, x);
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void add16(float (&v)[2][16], const v4u (&held)[4], LDS_AS uint8_t* ep) {
+        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) *(LDS_AS v4u*)at16(ep, 8 * p + (lane >> 3), 16 * (lane & 7)) = held[p];
+        lds_done();
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const v4hh r = __builtin_bit_cast(v4hh, *(const LDS_AS v2i*)at16(ep, lr, 2 * (32 * j + 8 * q + 4 * h)));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[j][4 * q + e] += (float)r[e];
+            }
+        lds_done();
+    }
+
+    // 32 rows of codes in LDS: 64 bytes a row, chunk c of row r at slot c ^ (r / 4 % 4).
+    static __device__ __forceinline__ void stage8(LDS_AS uint8_t* ep, int r, int byte, uint32_t w) {
+        *(LDS_AS uint32_t*)(ep + r * 64 + ((((byte >> 4) ^ ((r >> 2) & 3)) << 4) | (byte & 15))) = w;
+    }
+
+    static __device__ __forceinline__ void drain8(uint8_t* base, LDS_AS uint8_t* ep, int row0, int col0, int M, int N) {
+        const int lane = threadIdx.x & 63;
+        lds_done();
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int r = 16 * p + (lane >> 2), seg = lane & 3, row = row0 + r, col = col0 + 16 * seg;
+            const v4u w = *(const LDS_AS v4u*)(ep + r * 64 + 16 * (seg ^ ((r >> 2) & 3)));
+            if (row >= M || col >= N) continue;
+            uint8_t* d = base + (int64_t)row * N + col;
+            if (col + 16 <= N) {
+                *reinterpret_cast<v4u_b1*>(d) = w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (col + e < N) d[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
+            }
+        }
+        lds_done();
+    }
+
+    // 8-bit values of z: a row's block of 32 columns is in two lanes.
+    __device__ __forceinline__ void put_mx(const float (&v)[2][16], LDS_AS uint8_t* ep, int row0, int col0, int M,
+                                           int N) const {
+        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5, row = row0 + lr;
+        const bool whole = col0 + 64 <= N;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            float m = 0.0f;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+                const float a = finite_abs(v[j][x]);
+                if (whole || col0 + 32 * j + 8 * (x >> 2) + 4 * h + (x & 3) < N) m = fmaxf(m, a);
+            }
+            m = fmaxf(m, __shfl_xor(m, 32, 64));
+            const int e = exponent(m);
+            const float inv = mx_inverse(e);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                stage8(ep, lr, 32 * j + 8 * q + 4 * h,
+                       codes4(v[j][4 * q] * inv, v[j][4 * q + 1] * inv, v[j][4 * q + 2] * inv, v[j][4 * q + 3] * inv));
+            if (h == 0 && row < M && col0 + 32 * j < N) put_exponent(row, col0 + 32 * j, N, e);
+        }
+        drain8(reinterpret_cast<uint8_t*>(Z), ep, row0, col0, M, N);
+    }
+};
+
+inline BiasActExtra bias_act_extra(const BiasActArgs& a) {
+    return BiasActExtra{a.sA, a.sB, a.sOut, a.bias, a.residual, a.C, a.Z, a.zscale, a.act, a.res_dtype, a.out_dtype,
+                        a.z_dtype, a.channel};
+}
+
+}  // namespace libgemm

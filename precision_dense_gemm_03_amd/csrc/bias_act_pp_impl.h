@@ -1,0 +1,40 @@
+// Products with bias, activation and residual on the ping-pong tile kernel
+// (gemm_pp_impl.h), whose epilogue they replace (bias_act_extra.h).
+#pragma once
+
+#include "bias_act_extra.h"
+#include "gemm_pp_impl.h"
+
+namespace libgemm {
+namespace bias_act {
+
+template <int ES, int FA, int FB, bool BT, int BM>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void bias_act_pp_kernel(
+    const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tiles_m, int tiles_n,
+    BiasActExtra ext) {
+    using T = pp::Pp<ES, BM>;
+    LIBGEMM_PP_LDS(T);
+    if (past_last_block((int64_t)tiles_m * tiles_n)) return;
+    int tm, tn;
+    tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
+    pp::pp_body<ES, OUT_F32, FA, FB, BT, false, BM, true, BiasActExtra>(A, B, nullptr, M, N, K, nullptr, nullptr, nullptr,
+                                                                        tm * BM, tn * 256, 0, 0, lds, ext);
+}
+
+template <int ES, int FA, int FB, bool BT, int BM>
+hipError_t launch_pp(const BiasActArgs& a) {
+    const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + 255) / 256;
+    if (tiles_m * tiles_n > kMostWorkgroups) return hipErrorInvalidValue;
+    bias_act_pp_kernel<ES, FA, FB, BT, BM><<<wide_grid(tiles_m * tiles_n), 512, 0, a.stream>>>(
+        reinterpret_cast<const uint8_t*>(a.A), reinterpret_cast<const uint8_t*>(a.B), (int)a.M, (int)a.N, (int)a.K,
+        (int)tiles_m, (int)tiles_n, bias_act_extra(a));
+    return hipGetLastError();
+}
+
+template <int ES>
+bool pp_takes(const BiasActArgs& a) {
+    return a.b_kmajor ? pp::pp_fits<ES, true, 256>(a) : pp::pp_fits<ES, false, 256>(a);
+}
+
+}  // namespace bias_act
+}  // namespace libgemm

@@ -180,9 +180,10 @@ __device__ __forceinline__ void store_elem(void* C, int64_t idx, float y, int ef
 //
 // RAG (row groups, adapters): tiles that M or N cuts keep the vector stores,
 // masked by row and by 16-byte column piece. Ext: what is added to the
-// products before the store (NoExtra, or LoraExtra of lora_extra.h).
+// products before the store (NoExtra, or LoraExtra of lora_extra.h), or with kFinish
+// what takes the sums (BiasActExtra of bias_act_extra.h).
 struct NoExtra {
-    static constexpr bool kActive = false;
+    static constexpr bool kActive = false, kFinish = false;
 };
 
 // The LDS rings of a workgroup (LIBGEMM_PP_LDS declares them: separate objects,
@@ -606,6 +607,10 @@ __device__ __forceinline__ void pp_body(const uint8_t* __restrict__ A, const uin
     for (; t < nk; ++t) step(t, 0, false);
     if (G == 0) asm volatile("s_barrier" ::: "memory");
 
+    if constexpr (Ext::kFinish) {
+        ext.template finish_pp<T::MI>(acc, lds, m0, n0, G, wj, M, N);
+        return;
+    }
     // ---- epilogue ----
     // Block (i, j), element 4q + e: row MR G + 32 i + lr, column
     // 64 wj + 32 j + 8 q + 4 h + e of the tile.

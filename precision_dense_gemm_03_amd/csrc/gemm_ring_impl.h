@@ -295,12 +295,13 @@ __device__ __forceinline__ void store_elem(void* C, int64_t idx, float y, int ef
 
 // RAG (row groups, adapters): tiles that M or N cuts keep the vector stores,
 // masked. Ext: what is added to the products before the store (NoExtra, or
-// LoraExtra of lora_extra.h), or with kStores what stores them.
+// LoraExtra of lora_extra.h), or with kStores what stores them, or with kFinish what
+// takes the sums (BiasActExtra of bias_act_extra.h).
 struct NoExtra {
-    static constexpr bool kActive = false, kStores = false;
+    static constexpr bool kActive = false, kStores = false, kFinish = false;
 };
 
-template <class Ext, bool ACTIVE = Ext::kActive>
+template <class Ext, bool ACTIVE = Ext::kActive || Ext::kFinish>
 struct ExtPiece {
     typedef int type;
 };
@@ -587,7 +588,7 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
     const int row = m0 + 16 * wr + j16;
     auto col_of = [&](int tn) __attribute__((always_inline)) { return n0 + 16 * (T::TN * wc + tn) + 4 * g; };
     typename ExtPiece<Ext>::type piece[T::TN];
-    if constexpr (Ext::kActive) {
+    if constexpr (Ext::kActive || Ext::kFinish) {
 #pragma unroll
         for (int tn = 0; tn < T::TN; ++tn) ext.prefetch(piece[tn], row, col_of(tn), kg, M, N);
     }
@@ -715,6 +716,10 @@ __device__ __forceinline__ void ring_body(const uint8_t* __restrict__ A, const u
         }
     }
 
+    if constexpr (Ext::kFinish) {
+        ext.template finish_ring<T::TN>(acc, piece, row, col_of(0), M, N);
+        return;
+    }
     // ---- epilogue: lane holds row 16 wr + j16 and columns 16 (TN wc + tn) + 4 g + 0..3 ----
     const bool interior = vec_out && (RAG || ((m0 + BM <= M) && (n0 + BN <= N)));
     if constexpr (RAG) {

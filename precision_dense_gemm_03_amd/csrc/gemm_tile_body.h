@@ -387,6 +387,10 @@
         }
     }
 
+    if constexpr (Ext::kFinish) {
+        ext.template finish_tile16<T::TM, T::TN>(acc, m0 + wm * T::WTM + 4 * g, n0 + wn * T::WTN + j16, M, N);
+        return;
+    }
     // Epilogue: y = acc * (sA*sB), converted, stored with M/N predication on edge tiles.
     // Per-tensor: y = acc * sA*sB (/ sOut). Per-channel (EPI_CHANNEL, sA[M] and
     // sB[N]): y = acc * (1/sOut) * sA[row] * sB[col], loaded only for stored

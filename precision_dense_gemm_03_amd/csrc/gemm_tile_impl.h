@@ -243,9 +243,10 @@ constexpr int kAhead64 = 2, kAhead128 = 1;
 // alignment keep the vector loads (gfx950's global loads take any address),
 // and a row's last partial chunk is read as the 16 bytes that end the row,
 // shifted. Ext: what is added to the products before the store (NoExtra, or
-// LoraExtra of lora_extra.h).
+// LoraExtra of lora_extra.h), or with kFinish what takes the sums (BiasActExtra of
+// bias_act_extra.h).
 struct NoExtra {
-    static constexpr bool kActive = false;
+    static constexpr bool kActive = false, kFinish = false;
 };
 
 // One output tile: rows [m0, m0 + BM) below M, columns [n0, n0 + BN) below N,

@@ -51,6 +51,16 @@ struct LoraArgs : GemmArgs {
     int low_slices = 1;                 // parts of the low-rank values, which the products add up
 };
 
+// A product with bias, activation and residual in its epilogue.
+struct BiasActArgs : GemmArgs {
+    const float* bias = nullptr;        // device, N; or NULL
+    const void* residual = nullptr;     // device, [M, N] of res_dtype; or NULL
+    void* Z = nullptr;                  // device, [M, N] of z_dtype: the values before the activation; or NULL
+    uint8_t* zscale = nullptr;          // their scales, 8-bit values (row_io.h)
+    int act = 0;                        // Activation (act.h)
+    int res_dtype = 0, z_dtype = 0;     // OutDtype
+};
+
 typedef hipError_t (*GemmLauncher)(const GemmArgs&);
 
 // One entry of the compiled-in configuration table.
@@ -128,6 +138,10 @@ hipError_t launch_lora(int kind, const LoraArgs& a);
 // Names of the kernels that these calls launch (host only).
 const char* grouped_kernel_name(int kind, const GroupedArgs& a);
 const char* wgrad_kernel_name(const GroupedArgs& a);
+// launch_grouped_wgrad with A (qs 1) or B (qs 2) held as 8-bit values of format fmt
+// and their scales (row_io.h); a.offsets may be NULL: one group of all rows.
+hipError_t launch_wgrad_mx(const GroupedArgs& a, const uint8_t* scale, int fmt, int qs);
+const char* wgrad_mx_kernel_name(const GroupedArgs& a, int qs);
 const char* lora_kernel_name(int kind, const LoraArgs& a);
 hipError_t launch_lora_tile_f16(const LoraArgs& a, int bm);
 hipError_t launch_lora_tile_fp8(const LoraArgs& a, int bm);
@@ -172,6 +186,23 @@ hipError_t launch_grouped_pp_mixed(const GroupedArgs& a);
 hipError_t launch_lora_pp_f16(const LoraArgs& a, int bm);
 hipError_t launch_lora_pp_e4m3(const LoraArgs& a, int bm);
 hipError_t launch_lora_pp_mixed(const LoraArgs& a);
+
+// Products with bias, activation and residual (bias_act.cpp chooses the kernel).
+hipError_t launch_bias_act(int kind, const BiasActArgs& a);
+const char* bias_act_kernel_name(int kind, const BiasActArgs& a);
+constexpr int64_t kBiasActGemvF16 = 1, kBiasActGemvFp8 = 4;   // rows up to which the decode kernels run
+hipError_t launch_bias_act_gemv_f16(const BiasActArgs& a);
+hipError_t launch_bias_act_gemv_fp8(const BiasActArgs& a);
+bool bias_act_ring_takes(int kind, const BiasActArgs& a);
+hipError_t launch_bias_act_ring_f16(const BiasActArgs& a, int shape);
+hipError_t launch_bias_act_ring_fp8(const BiasActArgs& a, int shape);   // shape: of kLoraRingShapes
+bool bias_act_pp_takes_f16(const BiasActArgs& a);
+bool bias_act_pp_takes_fp8(const BiasActArgs& a);
+hipError_t launch_bias_act_pp_f16(const BiasActArgs& a, int bm);
+hipError_t launch_bias_act_pp_e4m3(const BiasActArgs& a, int bm);
+hipError_t launch_bias_act_pp_mixed(const BiasActArgs& a);
+hipError_t launch_bias_act_tile_f16(const BiasActArgs& a, int bm);
+hipError_t launch_bias_act_tile_fp8(const BiasActArgs& a, int bm);
 
 // C = epilogue(sum over a.splits slices of a.ws), in slice order.
 hipError_t launch_splitk_reduce(const GemmArgs& a);

@@ -91,7 +91,7 @@ __global__ __launch_bounds__(256) void lora_low_dot_kernel(const _Float16* __res
 
 // Stores the low-rank values of the rows whose adapter is `a`.
 struct LowStore {
-    static constexpr bool kActive = false, kStores = true;
+    static constexpr bool kActive = false, kStores = true, kFinish = false;
     float* low;
     const int32_t* adapter;
     float scale;

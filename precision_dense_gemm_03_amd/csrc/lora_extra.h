@@ -52,7 +52,7 @@ __device__ __forceinline__ v8h finite_part(v8h b) {
 }
 
 struct LoraExtra {
-    static constexpr bool kActive = true, kStores = false;
+    static constexpr bool kActive = true, kStores = false, kFinish = false;
     const float* low;         // slices of [rows, rank_p], zero from rank on
     const int32_t* adapter;   // [rows]
     const _Float16* LB;       // [adapters, N, rank]

@@ -1,0 +1,142 @@
+// 8-bit values with a power-of-two scale per 32 (row_io.h): from FP32 or FP16, and
+// back. One pass, bound by bytes: a lane takes 8 values, four lanes a block.
+#include "kernels.h"
+#include "norm.h"
+#include "row_io.h"
+#include "wide_grid.h"
+
+namespace libgemm {
+
+namespace {
+
+constexpr int kThreads = 256;
+
+// The lanes of a wave that hold one block agree on its exponent, and each gives its
+// 8 codes. T: the source's type.
+template <int T, int FMT>
+__device__ __forceinline__ int block_codes(float (&v)[8], uint32_t& lo, uint32_t& hi) {
+    if constexpr (T == OUT_F16) {
+        constexpr float top = FMT == FMT_E5M2 ? 57344.0f : 61440.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)   // (infinities and NaN stay)
+            if (__builtin_fabsf(v[i]) > top && __builtin_fabsf(v[i]) < __builtin_inff()) v[i] = __builtin_copysignf(top, v[i]);
+    }
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
+    m = fmaxf(m, __shfl_xor(m, 1, 64));
+    m = fmaxf(m, __shfl_xor(m, 2, 64));
+    const int e = mx_exponent<FMT>(m);
+    const float inv = mx_inverse(e);
+    lo = mx_pack4<FMT>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+    hi = mx_pack4<FMT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+    return e;
+}
+
+// Whole blocks in a row (cols % 32 == 0): x and q are one run of blocks, U units of
+// 8 values in flight per lane.
+template <int T, int FMT, int U>
+__global__ __launch_bounds__(kThreads) void mx_flat_kernel(const void* __restrict__ x, int64_t units,
+                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+    const int64_t first = wide_block() * (kThreads * U) + threadIdx.x;
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t at = first + u * kThreads;
+        load8<T>(x, at * 8, at < units ? 8 : 0, 1.0f, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t at = first + u * kThreads;
+        uint32_t lo, hi;
+        const int e = block_codes<T, FMT>(v[u], lo, hi);
+        if (at >= units) continue;
+        *reinterpret_cast<v2u_b1*>(q + at * 8) = v2u{lo, hi};
+        if ((threadIdx.x & 3) == 0) scale[at >> 2] = (uint8_t)(e + 127);
+    }
+}
+
+// Any width: a wave goes along a row, 512 values at a time.
+template <int T, int FMT>
+__global__ __launch_bounds__(kThreads) void mx_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols,
+                                                           uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+    const int lane = threadIdx.x & 63;
+    const int64_t blocks = (cols + kMxBlock - 1) / kMxBlock, step = (int64_t)gridDim.x * (kThreads / 64);
+    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); r < rows; r += step)
+        for (int64_t c0 = 0; c0 < cols; c0 += 512) {
+            const int64_t c = c0 + 8 * lane, left = cols - c;
+            const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+            float v[8];
+            load8<T>(x, r * cols + c, n, 1.0f, v);
+            uint32_t lo, hi;
+            const int e = block_codes<T, FMT>(v, lo, hi);
+            if (n > 0) {
+                store_codes8(q + r * cols + c, n, lo, hi);
+                if ((lane & 3) == 0) scale[r * blocks + c / kMxBlock] = (uint8_t)(e + 127);
+            }
+        }
+}
+
+template <int FMT, int T>
+__global__ __launch_bounds__(kThreads) void mx_unpack_kernel(const uint8_t* __restrict__ q,
+                                                             const uint8_t* __restrict__ scale, int64_t rows,
+                                                             int64_t cols, void* __restrict__ y) {
+    const int lane = threadIdx.x & 63;
+    const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
+    for (int64_t r = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); r < rows; r += step)
+        for (int64_t c = 8 * lane; c < cols; c += 512) {
+            float v[8];
+            load_row8<FMT == FMT_E5M2 ? OUT_E5M2 : OUT_E4M3>(q, scale, r, c, cols, v);
+            store8<T>(y, r * cols + c, cols - c >= 8 ? 8 : (int)(cols - c), v);
+        }
+}
+
+// Workgroups of four rows each, as many as keep the chip busy.
+unsigned row_blocks(int64_t rows) {
+    const int64_t n = (rows + 3) / 4;
+    return (unsigned)(n < 256 * 16 ? n : 256 * 16);
+}
+
+template <int T, int FMT>
+hipError_t pack(const void* x, int64_t rows, int64_t cols, uint8_t* q, uint8_t* scale, hipStream_t s) {
+    constexpr int U = T == OUT_F16 ? 4 : 2;
+    if (cols % kMxBlock == 0) {
+        const int64_t units = rows * (cols / 8);
+        // A lane alone with its loads where there are few.
+        const bool few = units < (int64_t)256 * kThreads * 4 * U;
+        const int64_t per = kThreads * (few ? 1 : U), blocks = (units + per - 1) / per;
+        if (few) mx_flat_kernel<T, FMT, 1><<<wide_grid(blocks), kThreads, 0, s>>>(x, units, q, scale);
+        else mx_flat_kernel<T, FMT, U><<<wide_grid(blocks), kThreads, 0, s>>>(x, units, q, scale);
+    } else {
+        mx_rows_kernel<T, FMT><<<row_blocks(rows), kThreads, 0, s>>>(x, rows, cols, q, scale);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_mx(const void* x, int dtype, int64_t rows, int64_t cols, int fmt, uint8_t* q,
+                              uint8_t* scale, hipStream_t s) {
+    if (dtype == OUT_F16)
+        return fmt == FMT_E5M2 ? pack<OUT_F16, FMT_E5M2>(x, rows, cols, q, scale, s)
+                               : pack<OUT_F16, FMT_E4M3>(x, rows, cols, q, scale, s);
+    return fmt == FMT_E5M2 ? pack<OUT_F32, FMT_E5M2>(x, rows, cols, q, scale, s)
+                           : pack<OUT_F32, FMT_E4M3>(x, rows, cols, q, scale, s);
+}
+
+hipError_t launch_dequantize_mx(const uint8_t* q, const uint8_t* scale, int fmt, int64_t rows, int64_t cols, void* y,
+                                int dtype, hipStream_t s) {
+    const unsigned grid = row_blocks(rows);
+#define LIBGEMM_GO(FMT, T) mx_unpack_kernel<FMT, T><<<grid, kThreads, 0, s>>>(q, scale, rows, cols, y)
+    if (fmt == FMT_E5M2) {
+        if (dtype == OUT_F16) LIBGEMM_GO(FMT_E5M2, OUT_F16);
+        else LIBGEMM_GO(FMT_E5M2, OUT_F32);
+    } else {
+        if (dtype == OUT_F16) LIBGEMM_GO(FMT_E4M3, OUT_F16);
+        else LIBGEMM_GO(FMT_E4M3, OUT_F32);
+    }
+#undef LIBGEMM_GO
+    return hipGetLastError();
+}
+
+}  // namespace libgemm
