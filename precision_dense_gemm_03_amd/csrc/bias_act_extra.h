@@ -30,6 +30,11 @@ __device__ __forceinline__ void with_activation(int act, F f) {
 
 typedef unsigned int u32_b1 __attribute__((aligned(1)));
 
+// LINES (ping-pong kernel): the FP16 residual and FP16 and FP32 results come and go
+// past the caches, in whole 128-byte lines (16384 x 12288 x 4096 FP8 with bias and
+// GELU_TANH 751 -> 707 us, with a residual too 808 -> 770: the caches' room is the
+// operands').
+template <bool LINES = false>
 struct BiasActExtra {
     static constexpr bool kActive = false, kStores = false, kFinish = true;
     const float* sA;
@@ -47,9 +52,10 @@ struct BiasActExtra {
     __device__ __forceinline__ float common() const { return channel ? 1.0f : (sA ? *sA : 1.0f) * (sB ? *sB : 1.0f); }
     __device__ __forceinline__ float out_factor() const { return out_dtype >= OUT_E4M3 ? 1.0f / *sOut : 1.0f; }
 
-    // Four neighbouring values of a row of FP32s, zero from N on.
+    // Four neighbouring values of a row of FP32s, zero from N on (FULL: all below N).
+    template <bool FULL = false>
     static __device__ __forceinline__ v4f row4(const float* p, int col, int N) {
-        if (col + 4 <= N) return __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + col)));
+        if (FULL || col + 4 <= N) return __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + col)));
         v4f v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = col + e < N ? p[col + e] : 0.0f;
@@ -275,46 +281,59 @@ struct BiasActExtra {
     // acc[i][j] holds row MR G + 32 i + lane % 32, columns 64 wj + 32 j + 8 q + 4
     // (lane / 32) + e in value 4 q + e. After the K loop the LDS is free: FP16 and
     // 8-bit values go through a wave's own part of it, so that memory is read and
-    // written in 16-byte pieces of rows. A wave takes 32 of its rows through all steps
-    // and then the next 32: with each step over all rows at once the sums, changed in
-    // the branches of the run-time types, took twice their registers (593 spilled).
+    // written in 16-byte pieces of rows.
+    //
+    // A wave takes 32 of its rows through all steps and then the next 32, the sums
+    // moving up, so that there is one copy of the code (one for each 32 rows, over 100
+    // KB with every type's branches, waited for instructions; each step over all rows
+    // at once spilled 593 registers). What M and N cut is read from clamped places and
+    // not stored: a mask per store and none per read.
     template <int MI, class Lds>
-    __device__ __forceinline__ void finish_pp(const v16f (&acc)[MI][2], const Lds& lds, int m0, int n0, int G, int wj,
-                                              int M, int N) const {
+    __device__ __forceinline__ void finish_pp(v16f (&acc)[MI][2], const Lds& lds, int m0, int n0, int G, int wj, int M,
+                                              int cols) const {
         constexpr int MR = 32 * MI, STAGE = 64 * MI * 64;
         static_assert(STAGE >= 3 * kPart, "three parts of the wave's LDS");
-        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
-        const int col0 = n0 + 64 * wj, lcol = col0 + 4 * h;   // of the wave's block; of this lane: + 32 j + 8 q
+        const int col0 = n0 + 64 * wj;   // of the wave's block
+        if (col0 >= cols) return;
         LDS_AS uint8_t* ep = G == 0 ? (wj == 0 ? lds.b[0] : wj == 1 ? lds.b[1] : wj == 2 ? lds.b[2] : lds.b[3])
                                     : (wj < 2 ? lds.a[0] : lds.a[1]) + (wj & 1) * STAGE;
         const float s = common(), f = out_factor();
         const bool res16 = residual && res_dtype == OUT_F16;
-        auto rows32 = [&](int i, const v16f& left, const v16f& right) __attribute__((always_inline)) {
-            const int row0 = m0 + MR * G + 32 * i, row = row0 + lr;
-            if (row0 >= M) return;
+#pragma unroll 1
+        for (int i = 0; i < MI; ++i) {
+            const int row0 = m0 + MR * G + 32 * i;
+            if (row0 >= M) break;
+            // Nothing is carried from one 32 rows to the next but the sums: bias, scales,
+            // addresses and masks of paths that a call does not take, kept over the loop,
+            // spilled 250 registers. So they come from values made anew here.
+            int lane = threadIdx.x & 63, N = cols;
+            asm volatile("" : "+v"(lane), "+s"(N) : : "memory");
+            const int lr = lane & 31, h = lane >> 5, lcol = col0 + 4 * h;   // this lane's columns: + 32 j + 8 q
+            const int row = min(row0 + lr, M - 1);
             v4u held[4];
-            if (res16) fetch16(held, row0, col0, M, N);
-            const float sr = channel ? sA[min(row, M - 1)] : 1.0f;
+            if (res16) fetch16(held, lane, row0, col0, M, N);
             float v[2][16];
+            if (channel) {
+                const float sa = sA[row];
+                each_run(sB, lcol, N, [&](int j, int q, v4f t) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+                    for (int e = 0; e < 4; ++e) v[j][4 * q + e] = acc[0][j][4 * q + e] * (sa * t[e]);
+                });
+            } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int col = lcol + 32 * j + 8 * q;
-                    const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
-                    const v4f b = bias ? row4(bias, col, N) : zero;
-                    const v4f sb = channel ? row4(sB, col, N) : zero;
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float y = (j == 0 ? left : right)[4 * q + e] * s;
-                        if (channel) y *= sr * sb[e];
-                        v[j][4 * q + e] = y + b[e];
-                    }
-                }
+                    for (int x = 0; x < 16; ++x) v[j][x] = acc[0][j][x] * s;
+            }
+            if (bias) {
+                each_run(bias, lcol, N, [&](int j, int q, v4f t) __attribute__((always_inline)) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[j][4 * q + e] += t[e];
+                });
+            }
             if (Z) {
-                if (z_dtype == OUT_F32) put_f32(Z, v, row, lcol, M, N);
-                else if (z_dtype == OUT_F16) put_f16(Z, v, ep, row0, col0, M, N);
-                else put_mx(v, ep, row0, col0, M, N);
+                if (z_dtype >= OUT_E4M3) put_mx(v, ep, lane, row0, col0, M, N);
+                else put_any(Z, z_dtype, v, ep, lane, row0, col0, M, N);
             }
             with_activation(act, [&](auto a) __attribute__((always_inline)) {
 #pragma unroll
@@ -323,22 +342,15 @@ struct BiasActExtra {
                     for (int x = 0; x < 16; ++x) v[j][x] = activate<decltype(a)::value>(v[j][x]);
             });
             if (res16) {
-                add16(v, held, ep + kPart);
-            } else if (residual && row < M) {
+                add16(v, held, ep + kPart, lane);
+            } else if (residual) {
+                each_run(reinterpret_cast<const float*>(residual) + (int64_t)row * N, lcol, N,
+                         [&](int j, int q, v4f t) __attribute__((always_inline)) {
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const v4f r = residual4(row, lcol + 32 * j + 8 * q, N);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) v[j][4 * q + e] += r[e];
-                    }
+                             for (int e = 0; e < 4; ++e) v[j][4 * q + e] += t[e];
+                         });
             }
-            if (out_dtype == OUT_F32) {
-                put_f32(C, v, row, lcol, M, N);
-            } else if (out_dtype == OUT_F16) {
-                put_f16(C, v, ep + 2 * kPart, row0, col0, M, N);
-            } else {
+            if (out_dtype >= OUT_E4M3) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -350,13 +362,16 @@ struct BiasActExtra {
                                out_dtype == OUT_E5M2 ? e5m2_pack4(y[0], y[1], y[2], y[3])
                                                      : e4m3_pack4(y[0], y[1], y[2], y[3]));
                     }
-                drain8(reinterpret_cast<uint8_t*>(C), ep + 2 * kPart, row0, col0, M, N);
+                drain8(reinterpret_cast<uint8_t*>(C), ep + 2 * kPart, lane, row0, col0, M, N);
+            } else {
+                put_any(C, out_dtype, v, ep + 2 * kPart, lane, row0, col0, M, N);
             }
-        };
-        rows32(0, acc[0][0], acc[0][1]);
-        rows32(1, acc[1][0], acc[1][1]);
-        rows32(2, acc[2][0], acc[2][1]);
-        if constexpr (MI > 3) rows32(3, acc[3][0], acc[3][1]);
+#pragma unroll
+            for (int k = 0; k + 1 < MI; ++k) {
+                acc[k][0] = acc[k + 1][0];
+                acc[k][1] = acc[k + 1][1];
+            }
+        }
     }
 
 private:
@@ -365,75 +380,109 @@ private:
 
     static __device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
-    static __device__ __forceinline__ void put_f32(void* base, const float (&v)[2][16], int row, int lcol, int M, int N) {
-        if (row >= M) return;
+    // f(j, q, values) for the lane's eight runs of four columns of a row of FP32s;
+    // what lies past N is some value of the row.
+    template <class F>
+    static __device__ __forceinline__ void each_run(const float* p, int lcol, int N, F f) {
+        v4f t[8];
+        if ((N & 3) == 0) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int k = 0; k < 8; ++k)
+                t[k] = __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + min(lcol + 32 * (k / 4) + 8 * (k % 4), N - 4))));
+        } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (lcol + 32 * j + 8 * q < N)
-                    put4(base, OUT_F32, row, lcol + 32 * j + 8 * q, N,
-                         v4f{v[j][4 * q], v[j][4 * q + 1], v[j][4 * q + 2], v[j][4 * q + 3]});
+            for (int k = 0; k < 8; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[k][e] = p[min(lcol + 32 * (k / 4) + 8 * (k % 4) + e, N - 1)];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f(k / 4, k % 4, t[k]);
     }
 
-    // 32 FP16 rows in LDS: 128 bytes a row, 16-byte chunk c of row r at slot c ^ (r / 2
-    // % 8): 32 rows at one column, or 8 rows whole, meet distinct banks.
+    // 32 rows in LDS: 128 bytes a row, 16-byte chunk c of row r at slot c ^ (r / 2 % 8):
+    // 32 rows at one column, or 8 rows whole, meet distinct banks.
     static __device__ __forceinline__ LDS_AS uint8_t* at16(LDS_AS uint8_t* ep, int r, int byte) {
         return ep + r * 128 + ((((byte >> 4) ^ ((r >> 1) & 7)) << 4) | (byte & 15));
     }
 
-    static __device__ __forceinline__ void put_f16(void* base, const float (&v)[2][16], LDS_AS uint8_t* ep, int row0,
-                                                   int col0, int M, int N) {
-        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+    // FP16 or FP32 values to an [M, N] matrix (FP32 32 columns at a time).
+    static __device__ __forceinline__ void put_any(void* base, int dtype, const float (&v)[2][16], LDS_AS uint8_t* ep,
+                                                   int lane, int row0, int col0, int M, int N) {
+        const int lr = lane & 31, h = lane >> 5;
+        if (dtype == OUT_F16) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const v4hh x = {(_Float16)v[j][4 * q], (_Float16)v[j][4 * q + 1], (_Float16)v[j][4 * q + 2],
-                                (_Float16)v[j][4 * q + 3]};
-                *(LDS_AS v2i*)at16(ep, lr, 2 * (32 * j + 8 * q + 4 * h)) = __builtin_bit_cast(v2i, x);
-            }
-        lds_done();
+                for (int q = 0; q < 4; ++q) {
+                    const v4hh x = {(_Float16)v[j][4 * q], (_Float16)v[j][4 * q + 1], (_Float16)v[j][4 * q + 2],
+                                    (_Float16)v[j][4 * q + 3]};
+                    *(LDS_AS v2i*)at16(ep, lr, 2 * (32 * j + 8 * q + 4 * h)) = __builtin_bit_cast(v2i, x);
+                }
+            drain16<2>(base, ep, lane, row0, col0, M, N);
+        } else {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int r = 8 * p + (lane >> 3), seg = lane & 7, row = row0 + r, col = col0 + 8 * seg;
-            const v4u w = *(const LDS_AS v4u*)at16(ep, r, 16 * seg);
-            if (row >= M || col >= N) continue;
-            _Float16* d = reinterpret_cast<_Float16*>(base) + (int64_t)row * N + col;
-            if (col + 8 <= N) {
-                *reinterpret_cast<v4u_b1*>(d) = w;
-            } else {
-                const v8h x = __builtin_bit_cast(v8h, w);
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (col + e < N) d[e] = x[e];
+                for (int q = 0; q < 4; ++q)
+                    *(LDS_AS v4f*)at16(ep, lr, 4 * (8 * q + 4 * h)) =
+                        v4f{v[j][4 * q], v[j][4 * q + 1], v[j][4 * q + 2], v[j][4 * q + 3]};
+                drain16<4>(base, ep, lane, row0, col0 + 32 * j, M, N);
             }
         }
-        lds_done();   // the part may be written again
+    }
+
+    // The LDS block's 32 rows of 128 bytes to memory, elements of ES bytes.
+    template <int ES>
+    static __device__ __forceinline__ void drain16(void* base, LDS_AS uint8_t* ep, int lane, int row0, int col0, int M, int N) {
+        constexpr int VE = 16 / ES;
+        const int seg = lane & 7, col = col0 + VE * seg;
+        lds_done();
+        uint8_t* d = reinterpret_cast<uint8_t*>(base) + ((int64_t)(row0 + (lane >> 3)) * N + col) * ES;
+        v4u w[4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) w[p] = *(const LDS_AS v4u*)at16(ep, 8 * p + (lane >> 3), 16 * seg);
+        if (N % VE == 0) {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+                if (row0 + 8 * p + (lane >> 3) < M && col < N) {
+                    if constexpr (LINES) __builtin_nontemporal_store(w[p], reinterpret_cast<v4u*>(d + (int64_t)(8 * p) * N * ES));
+                    else *reinterpret_cast<v4u_b1*>(d + (int64_t)(8 * p) * N * ES) = w[p];
+                }
+        } else {
+#pragma unroll
+            for (int p = 0; p < 4; ++p)
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (row0 + 8 * p + (lane >> 3) < M && col + e < N) {
+                        uint8_t* at = d + ((int64_t)(8 * p) * N + e) * ES;
+                        if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(at) = w[p][e];
+                        else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(w[p][e / 2] >> (16 * (e & 1)));
+                    }
+        }
+        lds_done();   // the block may be written again
     }
 
     // 32 rows of the FP16 residual, in 16-byte pieces of rows.
-    __device__ __forceinline__ void fetch16(v4u (&held)[4], int row0, int col0, int M, int N) const {
-        const int lane = threadIdx.x & 63;
+    __device__ __forceinline__ void fetch16(v4u (&held)[4], int lane, int row0, int col0, int M, int N) const {
+        const int col = col0 + 8 * (lane & 7);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const int row = row0 + 8 * p + (lane >> 3), col = col0 + 8 * (lane & 7);
-            const _Float16* s = reinterpret_cast<const _Float16*>(residual) + (int64_t)row * N + col;
-            held[p] = v4u{0u, 0u, 0u, 0u};
-            if (row < M && col + 8 <= N) {
-                held[p] = *reinterpret_cast<const v4u_b1*>(s);
-            } else if (row < M && col < N) {
-                v8h x = __builtin_bit_cast(v8h, held[p]);
+            const _Float16* s =
+                reinterpret_cast<const _Float16*>(residual) + (int64_t)min(row0 + 8 * p + (lane >> 3), M - 1) * N;
+            if ((N & 7) == 0) {
+                if constexpr (LINES) held[p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(s + min(col, N - 8)));
+                else held[p] = *reinterpret_cast<const v4u_b1*>(s + min(col, N - 8));
+            } else {
+                v8h x;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (col + e < N) x[e] = s[e];
+                for (int e = 0; e < 8; ++e) x[e] = s[min(col + e, N - 1)];
                 held[p] = __builtin_bit_cast(v4u, x);
             }
         }
     }
 
-    static __device__ __forceinline__ void add16(float (&v)[2][16], const v4u (&held)[4], LDS_AS uint8_t* ep) {
-        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5;
+    static __device__ __forceinline__ void add16(float (&v)[2][16], const v4u (&held)[4], LDS_AS uint8_t* ep, int lane) {
+        const int lr = lane & 31, h = lane >> 5;
 #pragma unroll
         for (int p = 0; p < 4; ++p) *(LDS_AS v4u*)at16(ep, 8 * p + (lane >> 3), 16 * (lane & 7)) = held[p];
         lds_done();
@@ -453,54 +502,80 @@ private:
         *(LDS_AS uint32_t*)(ep + r * 64 + ((((byte >> 4) ^ ((r >> 2) & 3)) << 4) | (byte & 15))) = w;
     }
 
-    static __device__ __forceinline__ void drain8(uint8_t* base, LDS_AS uint8_t* ep, int row0, int col0, int M, int N) {
-        const int lane = threadIdx.x & 63;
+    static __device__ __forceinline__ void drain8(uint8_t* base, LDS_AS uint8_t* ep, int lane, int row0, int col0, int M, int N) {
+        const int seg = lane & 3, col = col0 + 16 * seg;
         lds_done();
+        uint8_t* d = base + (int64_t)(row0 + (lane >> 2)) * N + col;
+        v4u w[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const int r = 16 * p + (lane >> 2), seg = lane & 3, row = row0 + r, col = col0 + 16 * seg;
-            const v4u w = *(const LDS_AS v4u*)(ep + r * 64 + 16 * (seg ^ ((r >> 2) & 3)));
-            if (row >= M || col >= N) continue;
-            uint8_t* d = base + (int64_t)row * N + col;
-            if (col + 16 <= N) {
-                *reinterpret_cast<v4u_b1*>(d) = w;
-            } else {
+            const int r = 16 * p + (lane >> 2);
+            w[p] = *(const LDS_AS v4u*)(ep + r * 64 + 16 * (seg ^ ((r >> 2) & 3)));
+        }
+        if ((N & 15) == 0) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                if (row0 + 16 * p + (lane >> 2) < M && col < N) *reinterpret_cast<v4u_b1*>(d + (int64_t)(16 * p) * N) = w[p];
+        } else {
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (col + e < N) d[e] = (uint8_t)(w[e / 4] >> (8 * (e % 4)));
-            }
+                    if (row0 + 16 * p + (lane >> 2) < M && col + e < N)
+                        d[(int64_t)(16 * p) * N + e] = (uint8_t)(w[p][e / 4] >> (8 * (e % 4)));
         }
         lds_done();
     }
 
     // 8-bit values of z: a row's block of 32 columns is in two lanes.
-    __device__ __forceinline__ void put_mx(const float (&v)[2][16], LDS_AS uint8_t* ep, int row0, int col0, int M,
+    __device__ __forceinline__ void put_mx(float (&v)[2][16], LDS_AS uint8_t* ep, int lane, int row0, int col0, int M,
                                            int N) const {
-        const int lane = threadIdx.x & 63, lr = lane & 31, h = lane >> 5, row = row0 + lr;
-        const bool whole = col0 + 64 <= N;
+        const int lr = lane & 31, h = lane >> 5, row = row0 + lr;
+        if (col0 + 64 > N) {   // columns past N take no part
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int x = 0; x < 16; ++x)
+                    v[j][x] = col0 + 32 * j + 8 * (x >> 2) + 4 * h + (x & 3) < N ? v[j][x] : 0.0f;
+        }
+        uint32_t both = 0;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             float m = 0.0f;
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const float a = finite_abs(v[j][x]);
-                if (whole || col0 + 32 * j + 8 * (x >> 2) + 4 * h + (x & 3) < N) m = fmaxf(m, a);
+            for (int x = 0; x < 16; ++x) m = fmaxf(m, __builtin_fabsf(v[j][x]));
+            if (__builtin_amdgcn_ballot_w64(!(m < __builtin_inff())) != 0) {   // (fmaxf passes NaN over)
+                m = 0.0f;
+#pragma unroll
+                for (int x = 0; x < 16; ++x) m = fmaxf(m, finite_abs(v[j][x]));
             }
             m = fmaxf(m, __shfl_xor(m, 32, 64));
             const int e = exponent(m);
             const float inv = mx_inverse(e);
+            both |= (uint32_t)(e + 127) << (8 * j);
+            if (z_dtype == OUT_E5M2) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                stage8(ep, lr, 32 * j + 8 * q + 4 * h,
-                       codes4(v[j][4 * q] * inv, v[j][4 * q + 1] * inv, v[j][4 * q + 2] * inv, v[j][4 * q + 3] * inv));
-            if (h == 0 && row < M && col0 + 32 * j < N) put_exponent(row, col0 + 32 * j, N, e);
+                for (int q = 0; q < 4; ++q)
+                    stage8(ep, lr, 32 * j + 8 * q + 4 * h,
+                           mx_pack4<FMT_E5M2>(v[j][4 * q] * inv, v[j][4 * q + 1] * inv, v[j][4 * q + 2] * inv, v[j][4 * q + 3] * inv));
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    stage8(ep, lr, 32 * j + 8 * q + 4 * h,
+                           mx_pack4<FMT_E4M3>(v[j][4 * q] * inv, v[j][4 * q + 1] * inv, v[j][4 * q + 2] * inv, v[j][4 * q + 3] * inv));
+            }
         }
-        drain8(reinterpret_cast<uint8_t*>(Z), ep, row0, col0, M, N);
+        // lane h of a row stores the scale of its half of the columns
+        const int col = col0 + 32 * h;
+        if (row < M && col < N)
+            zscale[(int64_t)row * ((N + kMxBlock - 1) / kMxBlock) + col / kMxBlock] = (uint8_t)(both >> (8 * h));
+        drain8(reinterpret_cast<uint8_t*>(Z), ep, lane, row0, col0, M, N);
     }
 };
 
-inline BiasActExtra bias_act_extra(const BiasActArgs& a) {
-    return BiasActExtra{a.sA, a.sB, a.sOut, a.bias, a.residual, a.C, a.Z, a.zscale, a.act, a.res_dtype, a.out_dtype,
+template <bool LINES = false>
+BiasActExtra<LINES> bias_act_extra(const BiasActArgs& a) {
+    return BiasActExtra<LINES>{a.sA, a.sB, a.sOut, a.bias, a.residual, a.C, a.Z, a.zscale, a.act, a.res_dtype, a.out_dtype,
                         a.z_dtype, a.channel};
 }
 

@@ -8,26 +8,37 @@
 namespace libgemm {
 namespace bias_act {
 
-template <int ES, int FA, int FB, bool BT, int BM>
+template <int ES, int FA, int FB, bool BT, int BM, bool LINES>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void bias_act_pp_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tiles_m, int tiles_n,
-    BiasActExtra ext) {
+    BiasActExtra<LINES> ext) {
     using T = pp::Pp<ES, BM>;
     LIBGEMM_PP_LDS(T);
     if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
     tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
-    pp::pp_body<ES, OUT_F32, FA, FB, BT, false, BM, true, BiasActExtra>(A, B, nullptr, M, N, K, nullptr, nullptr, nullptr,
+    pp::pp_body<ES, OUT_F32, FA, FB, BT, false, BM, true, BiasActExtra<LINES>>(A, B, nullptr, M, N, K, nullptr, nullptr, nullptr,
                                                                         tm * BM, tn * 256, 0, 0, lds, ext);
+}
+
+// Rows of whole 128-byte lines in every FP16 and FP32 matrix of the epilogue.
+inline bool whole_lines(const BiasActArgs& a) {
+    auto line = [](const void* p) { return ((uintptr_t)p & 127) == 0; };
+    return a.N % 64 == 0 && line(a.C) && line(a.residual) && line(a.Z);
 }
 
 template <int ES, int FA, int FB, bool BT, int BM>
 hipError_t launch_pp(const BiasActArgs& a) {
     const int64_t tiles_m = (a.M + BM - 1) / BM, tiles_n = (a.N + 255) / 256;
     if (tiles_m * tiles_n > kMostWorkgroups) return hipErrorInvalidValue;
-    bias_act_pp_kernel<ES, FA, FB, BT, BM><<<wide_grid(tiles_m * tiles_n), 512, 0, a.stream>>>(
-        reinterpret_cast<const uint8_t*>(a.A), reinterpret_cast<const uint8_t*>(a.B), (int)a.M, (int)a.N, (int)a.K,
-        (int)tiles_m, (int)tiles_n, bias_act_extra(a));
+    const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
+    const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
+#define LIBGEMM_GO(LINES)                                                                              \
+    bias_act_pp_kernel<ES, FA, FB, BT, BM, LINES><<<wide_grid(tiles_m * tiles_n), 512, 0, a.stream>>>( \
+        A, B, (int)a.M, (int)a.N, (int)a.K, (int)tiles_m, (int)tiles_n, bias_act_extra<LINES>(a))
+    if (whole_lines(a)) LIBGEMM_GO(true);
+    else LIBGEMM_GO(false);
+#undef LIBGEMM_GO
     return hipGetLastError();
 }
 

@@ -18,7 +18,7 @@ struct RingShape {
 template <int ES, int BM, int BN, int FA, int FB, bool BT>
 __global__ __launch_bounds__(256) void bias_act_ring_kernel(const uint8_t* __restrict__ A,
                                                             const uint8_t* __restrict__ B, int M, int N, int K,
-                                                            int tiles_m, int tiles_n, BiasActExtra ext) {
+                                                            int tiles_m, int tiles_n, BiasActExtra<> ext) {
     constexpr int S = RingShape<BM, BN>::S, P = RingShape<BM, BN>::P;
     using T = ring::Ring<ES, BM, BN, BT, S>;
     __shared__ __attribute__((aligned(1024))) uint8_t ring[T::S * T::STAGE];
@@ -26,7 +26,7 @@ __global__ __launch_bounds__(256) void bias_act_ring_kernel(const uint8_t* __res
     if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
     tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
-    ring::ring_body<ES, BM, BN, OUT_F32, FA, FB, BT, S, true, BiasActExtra, P>(
+    ring::ring_body<ES, BM, BN, OUT_F32, FA, FB, BT, S, true, BiasActExtra<>, P>(
         A, B, nullptr, M, N, K, nullptr, nullptr, nullptr, tm * BM, tn * BN, 0, 0, ring, red, ext);
 }
 

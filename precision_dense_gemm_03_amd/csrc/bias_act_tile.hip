@@ -11,11 +11,11 @@ namespace {
 template <int ES, int BM, int FA, int FB, bool BT>
 __global__ __launch_bounds__(256) void bias_act_tile_kernel(const uint8_t* __restrict__ A,
                                                             const uint8_t* __restrict__ B, int M, int N, int K,
-                                                            int tiles_m, int tiles_n, BiasActExtra ext) {
+                                                            int tiles_m, int tiles_n, BiasActExtra<> ext) {
     if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
     tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
-    tile::tile_body<ES, OUT_F32, BM, BM, 128 / ES, 2, 2, FA, FB, BT, ES, true, BiasActExtra>(
+    tile::tile_body<ES, OUT_F32, BM, BM, 128 / ES, 2, 2, FA, FB, BT, ES, true, BiasActExtra<>>(
         A, B, nullptr, M, N, K, nullptr, nullptr, nullptr, tm * BM, tn * BM, 1, 0, K, 0, ext);
 }
 

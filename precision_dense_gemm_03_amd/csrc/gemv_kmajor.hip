@@ -371,12 +371,12 @@ const GemmConfig* gemv_kmajor_configs(int* count) {
 // The products with bias and activation at decode sizes (kBiasActGemvF16, Fp8 rows):
 // for each bound M the kernel that the table has first.
 hipError_t launch_bias_act_gemv_f16(const BiasActArgs& a) {
-    const BiasActExtra ext = bias_act_extra(a);
+    const BiasActExtra<> ext = bias_act_extra(a);
     return launch_gemv_kmajor_coop<2, 1, 4, 8>(a, ext);
 }
 
 hipError_t launch_bias_act_gemv_fp8(const BiasActArgs& a) {
-    const BiasActExtra ext = bias_act_extra(a);
+    const BiasActExtra<> ext = bias_act_extra(a);
     if (a.M <= 1) return gemv_kmajor_fp8<1, 1, 4>(a, ext);
     return gemv_kmajor_coop_fp8<4, 4, 4>(a, ext);
 }
