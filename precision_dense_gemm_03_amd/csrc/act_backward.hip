@@ -38,7 +38,35 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackwardArgs a, in
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     const int64_t step = (int64_t)gridDim.y * subs * kRows;
-    for (int64_t r0 = (int64_t)blockIdx.y * subs * kRows + sub; r0 < a.rows; r0 += step) {
+    int64_t r0 = (int64_t)blockIdx.y * subs * kRows + sub;
+    const int64_t blocks = (a.cols + kMxBlock - 1) / kMxBlock;
+    // Whole sets of rows and whole pieces of eight: every load first.
+    if (n >= 8) {
+        for (; r0 + (kRows - 1) * subs < a.rows; r0 += step) {
+            Raw8<T> dy[kRows];
+            Raw8<Z> z[kRows];
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int64_t r = r0 + u * subs;
+                fetch8<T>(dy[u], a.dy, r * a.cols + c, nullptr);
+                if constexpr (ACT != ACT_NONE)
+                    fetch8<Z>(z[u], a.z, r * a.cols + c, Z >= OUT_E4M3 ? a.zscale + r * blocks + c / kMxBlock : nullptr);
+            }
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                float d[8], x[8];
+                values8<T>(dy[u], d);
+                if constexpr (ACT != ACT_NONE) values8<Z>(z[u], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (ACT != ACT_NONE) d[i] *= slope<ACT>(x[i]);
+                    acc[i] += d[i];
+                }
+                if (a.dz) store8<T>(a.dz, (r0 + u * subs) * a.cols + c, 8, d);
+            }
+        }
+    }
+    for (; r0 < a.rows; r0 += step) {
         float dy[kRows][8], z[kRows][8];
 #pragma unroll
         for (int u = 0; u < kRows; ++u) {

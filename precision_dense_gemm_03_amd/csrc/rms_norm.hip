@@ -97,9 +97,45 @@ __device__ __forceinline__ int count8(int64_t c, int64_t width) {
     return left >= 8 ? 8 : (left > 0 ? (int)left : 0);
 }
 
+// A row's chunks in a lane's registers: eight values from column c on, c = first +
+// 512 W k. V8: rows of whole chunks, which are loaded without conditions (a chunk past
+// the row's end is its last one) and all before the first is looked at.
+template <int T, int W, int CH, bool V8>
+struct Chunks {
+    Raw8<T> raw[V8 ? CH : 1];
+    float v[CH][8];
+
+    __device__ __forceinline__ void fetch(const void* base, const uint8_t* scales, int64_t r, int64_t width, int first) {
+#pragma unroll
+        for (int k = 0; k < CH; ++k) {
+            const int c = first + k * 512 * W;
+            if constexpr (V8) {
+                const int at = min(c, (int)width - 8);
+                fetch8<T>(raw[k], base, r * width + at,
+                          T >= OUT_E4M3 ? scales + r * ((width + kMxBlock - 1) / kMxBlock) + at / kMxBlock : nullptr);
+            } else {
+                load_row8<T>(base, scales, r, c, width, v[k]);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void values(int64_t width, int first) {
+        if constexpr (V8) {
+#pragma unroll
+            for (int k = 0; k < CH; ++k) {
+                values8<T>(raw[k], v[k]);
+                if (first + k * 512 * W >= width) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
+                }
+            }
+        }
+    }
+};
+
 // W waves per row (W = 1: four rows per workgroup), CH chunks per lane. Lane l of
 // the row's W * 64 takes chunks l, l + 64 W, ..
-template <int T, int OUT, int W, int CH>
+template <int T, int OUT, int W, int CH, bool V8>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArgs a) {
     constexpr int RPW = W == 1 ? 4 : 1;
     __shared__ float red[2][W][2];
@@ -111,20 +147,15 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArg
     int half = 0;
     for (int64_t r = (int64_t)blockIdx.x * RPW + (W == 1 ? wave : 0); r < a.rows; r += (int64_t)gridDim.x * RPW) {
         const int64_t base = r * a.width;
-        float v[CH][8];
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-            const int c = first + k * 512 * W;
-            load8<T>(a.x, base + c, count8(c, a.width), 1.0f, v[k]);
-        }
+        Chunks<T, W, CH, V8> x, res;
+        x.fetch(a.x, nullptr, r, a.width, first);
+        if (a.residual) res.fetch(a.residual, nullptr, r, a.width, first);
+        x.values(a.width, first);
+        float (&v)[CH][8] = x.v;
         if (a.residual) {
+            res.values(a.width, first);
 #pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int c = first + k * 512 * W;
-                float s[8];
-                load8<T>(a.residual, base + c, count8(c, a.width), 1.0f, s);
-                add8<T>(v[k], s);
-            }
+            for (int k = 0; k < CH; ++k) add8<T>(v[k], res.v[k]);
         }
         float sum = 0.0f, most = 0.0f;
 #pragma unroll
@@ -212,7 +243,7 @@ __global__ __launch_bounds__(512) void rms_norm_long_kernel(NormArgs a) {
 // ---------------------------------------------------------------- gradient
 
 // T: type of dy, dh and dx; H: of h (8-bit values with scales among them).
-template <int T, int H, int W, int CH>
+template <int T, int H, int W, int CH, bool V8>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kernel(NormBackwardArgs a) {
     constexpr int RPW = W == 1 ? 4 : 1;
     __shared__ float red[2][W];
@@ -229,21 +260,16 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kerne
     int half = 0;
     for (int64_t r = (int64_t)blockIdx.x * RPW + (W == 1 ? wave : 0); r < a.rows; r += (int64_t)gridDim.x * RPW) {
         const int64_t base = r * a.width;
-        float n[CH][8], g[CH][8], d[CH][8];
+        Chunks<H, W, CH, V8> hh;
+        Chunks<T, W, CH, V8> gg, dd;
         const float rstd = a.rstd[r];
-#pragma unroll
-        for (int k = 0; k < CH; ++k) {
-            const int c = first + k * 512 * W;
-            load_row8<H>(a.h, a.hscale, r, c, a.width, n[k]);
-            load8<T>(a.dy, base + c, count8(c, a.width), 1.0f, g[k]);
-        }
-        if (a.dh) {
-#pragma unroll
-            for (int k = 0; k < CH; ++k) {
-                const int c = first + k * 512 * W;
-                load8<T>(a.dh, base + c, count8(c, a.width), 1.0f, d[k]);
-            }
-        }
+        hh.fetch(a.h, a.hscale, r, a.width, first);
+        gg.fetch(a.dy, nullptr, r, a.width, first);
+        if (a.dh) dd.fetch(a.dh, nullptr, r, a.width, first);
+        hh.values(a.width, first);
+        gg.values(a.width, first);
+        float (&n)[CH][8] = hh.v;
+        float (&g)[CH][8] = gg.v;
         float sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < CH; ++k)
@@ -256,6 +282,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kerne
             }
         const float mean = row_sum<W>(sum, red[half], wave) * a.inv_width;
         half ^= 1;
+        if (a.dh) dd.values(a.width, first);
+        float (&d)[CH][8] = dd.v;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = first + k * 512 * W;
@@ -355,7 +383,7 @@ void by_width(int64_t width, F f) {
     else if (width <= 2048) f(IntC<4>{}, IntC<1>{});
     else if (width <= 4096) f(IntC<4>{}, IntC<2>{});
     else if (width <= 8192) f(IntC<8>{}, IntC<2>{});
-    else f(IntC<8>{}, IntC<4>{});
+    else f(IntC<8>{}, IntC<4>{});   // (16 waves and 2 chunks: the gradient 158 us for 118 at 4096 x 16384)
 }
 
 template <int T, int OUT>
@@ -368,7 +396,9 @@ hipError_t norm_forward(const NormArgs& a, hipStream_t s) {
     by_width(a.width, [&](auto w, auto ch) {
         constexpr int W = decltype(w)::value, CH = decltype(ch)::value, RPW = W == 1 ? 4 : 1;
         const int64_t blocks = (a.rows + RPW - 1) / RPW;
-        rms_norm_kernel<T, OUT, W, CH><<<(unsigned)(blocks < most ? blocks : most), W == 1 ? 256 : 64 * W, 0, s>>>(a);
+        const unsigned grid = (unsigned)(blocks < most ? blocks : most), nt = W == 1 ? 256 : 64 * W;
+        if (a.width % 8 == 0) rms_norm_kernel<T, OUT, W, CH, true><<<grid, nt, 0, s>>>(a);
+        else rms_norm_kernel<T, OUT, W, CH, false><<<grid, nt, 0, s>>>(a);
     });
     return hipGetLastError();
 }
@@ -389,7 +419,9 @@ hipError_t norm_backward(const NormBackwardArgs& a, float* dweight, hipStream_t 
         by_width(a.width, [&](auto w, auto ch) {
             constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
             parts = norm_backward_parts(a.rows, a.width);
-            rms_norm_backward_kernel<T, H, W, CH><<<(unsigned)parts, W == 1 ? 256 : 64 * W, 0, s>>>(b);
+            constexpr unsigned nt = W == 1 ? 256 : 64 * W;
+            if (a.width % 8 == 0) rms_norm_backward_kernel<T, H, W, CH, true><<<(unsigned)parts, nt, 0, s>>>(b);
+            else rms_norm_backward_kernel<T, H, W, CH, false><<<(unsigned)parts, nt, 0, s>>>(b);
         });
     }
     hipError_t e = hipGetLastError();
@@ -405,7 +437,11 @@ int64_t norm_backward_parts(int64_t rows, int64_t width) {
         return rows < want ? rows : want;
     }
     const int64_t sets = width <= 1024 ? (rows + 3) / 4 : rows;   // (four rows per workgroup)
-    return sets < 1024 ? sets : 1024;
+    // Each part is a row of sums written and read again. 16384 x 4096, FP16 / 8-bit h: 101
+    // / 70 us with 512, 111 / 81 with 1024, 117 / 111 with 256; 4096 x 16384: 118 / 121
+    // with 256, 129 / 131 with 512.
+    const int64_t most = width <= 8192 ? 512 : 256;
+    return sets < most ? sets : most;
 }
 
 int64_t norm_backward_words(int64_t rows, int64_t width) {

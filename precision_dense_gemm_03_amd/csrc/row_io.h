@@ -107,6 +107,54 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float
     }
 }
 
+// The same in two steps, so that many loads can be in flight: eight whole values as
+// they lie in memory, and what they are.
+template <int T>
+struct Raw8 {
+    v4u w[T == OUT_F32 ? 2 : 1];   // (codes: two words)
+    uint32_t e;                    // the block's scale
+};
+
+template <int T>
+__device__ __forceinline__ void fetch8(Raw8<T>& x, const void* base, int64_t at, const uint8_t* scale) {
+    if constexpr (T == OUT_F32) {
+        const float* p = reinterpret_cast<const float*>(base) + at;
+        x.w[0] = *reinterpret_cast<const v4u_b1*>(p);
+        x.w[1] = *reinterpret_cast<const v4u_b1*>(p + 4);
+    } else if constexpr (T == OUT_F16) {
+        x.w[0] = *reinterpret_cast<const v4u_b1*>(reinterpret_cast<const _Float16*>(base) + at);
+    } else {
+        const v2u c = *reinterpret_cast<const v2u_b1*>(reinterpret_cast<const uint8_t*>(base) + at);
+        x.w[0] = v4u{c[0], c[1], 0u, 0u};
+        x.e = *scale;
+    }
+}
+
+template <int T>
+__device__ __forceinline__ void values8(const Raw8<T>& x, float (&v)[8]) {
+    if constexpr (T == OUT_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bits_f32(x.w[i / 4][i % 4]);
+    } else if constexpr (T == OUT_F16) {
+        const v8h h = __builtin_bit_cast(v8h, x.w[0]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
+    } else {
+        const float s = mx_scale(x.e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int w = (int)x.w[0][i / 2];
+            if constexpr (T == OUT_E5M2) {
+                const auto p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_bf8(w, true) : __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
+                v[2 * i] = p[0] * s, v[2 * i + 1] = p[1] * s;
+            } else {
+                const auto p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
+                v[2 * i] = p[0] * s, v[2 * i + 1] = p[1] * s;
+            }
+        }
+    }
+}
+
 // Values of row r from column c (a multiple of 8) on; scales as above (8-bit only).
 template <int T>
 __device__ __forceinline__ void load_row8(const void* base, const uint8_t* scales, int64_t r, int64_t c, int64_t width,
