@@ -27,65 +27,60 @@ int lanes_of(int64_t cols) {
     return n;
 }
 
-template <int T, int Z, int ACT>
+// MODE: rows of whole pieces of eight, rows that cut the last one (Piece8), rows of
+// fewer than eight columns.
+enum { WHOLE = 0, CUT = 1, NARROW = 2 };
+
+template <int T, int Z, int ACT, int MODE>
 __global__ __launch_bounds__(256) void act_backward_kernel(ActBackwardArgs a, int lpr) {
     __shared__ float sums[256][8];
     const int tid = threadIdx.x, sub = tid / lpr, subs = 256 / lpr;   // rows side by side in the workgroup
-    const int64_t c = ((int64_t)blockIdx.x * lpr + tid % lpr) * 8;
-    const int64_t left = a.cols - c;
-    const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
+    const int64_t first = (int64_t)blockIdx.x * lpr * 8;              // of the strip's columns
+    const Piece8 p(first + tid % lpr * 8, MODE == NARROW ? 8 : a.cols);
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
     const int64_t step = (int64_t)gridDim.y * subs * kRows;
     int64_t r0 = (int64_t)blockIdx.y * subs * kRows + sub;
-    const int64_t blocks = (a.cols + kMxBlock - 1) / kMxBlock;
-    // Whole sets of rows and whole pieces of eight: every load first.
-    if (n >= 8) {
-        for (; r0 + (kRows - 1) * subs < a.rows; r0 += step) {
-            Raw8<T> dy[kRows];
-            Raw8<Z> z[kRows];
-#pragma unroll
+    if constexpr (MODE == NARROW) {
+        const int n = (int)a.cols;
+        for (; r0 < a.rows; r0 += step)
             for (int u = 0; u < kRows; ++u) {
                 const int64_t r = r0 + u * subs;
-                fetch8<T>(dy[u], a.dy, r * a.cols + c, nullptr);
-                if constexpr (ACT != ACT_NONE)
-                    fetch8<Z>(z[u], a.z, r * a.cols + c, Z >= OUT_E4M3 ? a.zscale + r * blocks + c / kMxBlock : nullptr);
-            }
-#pragma unroll
-            for (int u = 0; u < kRows; ++u) {
+                if (r >= a.rows) break;
                 float d[8], x[8];
-                values8<T>(dy[u], d);
-                if constexpr (ACT != ACT_NONE) values8<Z>(z[u], x);
+                load8<T>(a.dy, r * n, n, 1.0f, d);
+                if constexpr (ACT != ACT_NONE) load_row8<Z>(a.z, a.zscale, r, 0, n, x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if constexpr (ACT != ACT_NONE) d[i] *= slope<ACT>(x[i]);
                     acc[i] += d[i];
                 }
-                if (a.dz) store8<T>(a.dz, (r0 + u * subs) * a.cols + c, 8, d);
+                if (a.dz) store8<T>(a.dz, r * n, n, d);
             }
-        }
-    }
-    for (; r0 < a.rows; r0 += step) {
-        float dy[kRows][8], z[kRows][8];
+    } else if (p.skip < 8) {
+        // every load first; rows past the end are the last one and count for nothing
+        for (; r0 < a.rows; r0 += step) {
+            Raw8<T> dy[kRows];
+            Raw8<Z> z[kRows];
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = r0 + u * subs;
-            if (r < a.rows) {
-                load8<T>(a.dy, r * a.cols + c, n, 1.0f, dy[u]);
-                if constexpr (ACT != ACT_NONE) load_row8<Z>(a.z, a.zscale, r, c, a.cols, z[u]);
+            for (int u = 0; u < kRows; ++u) {
+                const int64_t r = min(r0 + u * subs, a.rows - 1);
+                fetch8<T, MODE == CUT>(dy[u], a.dy, nullptr, r, a.cols, p);
+                if constexpr (ACT != ACT_NONE) fetch8<Z, MODE == CUT>(z[u], a.z, a.zscale, r, a.cols, p);
             }
-        }
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-            const int64_t r = r0 + u * subs;
-            if (r < a.rows) {
+            for (int u = 0; u < kRows; ++u) {
+                if (r0 + u * subs >= a.rows) break;
+                float d[8], x[8];
+                values8<T, MODE == CUT>(dy[u], p.skip, d);
+                if constexpr (ACT != ACT_NONE) values8<Z, MODE == CUT>(z[u], p.skip, x);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    if constexpr (ACT != ACT_NONE) dy[u][i] *= slope<ACT>(z[u][i]);
-                    acc[i] += dy[u][i];
+                    if constexpr (ACT != ACT_NONE) d[i] *= slope<ACT>(x[i]);
+                    acc[i] += d[i];
                 }
-                if (a.dz) store8<T>(a.dz, r * a.cols + c, n, dy[u]);
+                if (a.dz) store8<T>(a.dz, (r0 + u * subs) * a.cols + p.at, 8, d);
             }
         }
     }
@@ -94,10 +89,14 @@ __global__ __launch_bounds__(256) void act_backward_kernel(ActBackwardArgs a, in
     for (int i = 0; i < 8; ++i) sums[tid][i] = acc[i];
     __syncthreads();
     for (int j = tid; j < 8 * lpr; j += 256) {
+        const int64_t col = first + j;
+        if (col >= a.cols) break;
+        // (a cut piece's own columns are its last)
+        const int64_t past = first + j / 8 * 8 + 8 - a.cols;
+        const int e = j % 8 + (MODE == CUT && past > 0 ? (int)past : 0);
         float s = 0.0f;
-        for (int g = 0; g < subs; ++g) s += sums[g * lpr + j / 8][j % 8];
-        const int64_t col = (int64_t)blockIdx.x * lpr * 8 + j;
-        if (col < a.cols) a.partial[(int64_t)blockIdx.y * a.cols + col] = s;
+        for (int g = 0; g < subs; ++g) s += sums[g * lpr + j / 8][e];
+        a.partial[(int64_t)blockIdx.y * a.cols + col] = s;
     }
 }
 
@@ -138,7 +137,12 @@ hipError_t act_backward(const ActBackwardArgs& a, int act, float* dbias, hipStre
     const int lpr = lanes_of(a.cols);
     const int64_t strips = (a.cols + 8 * lpr - 1) / (8 * lpr), parts = act_backward_parts(a.rows, a.cols);
     const dim3 grid((unsigned)strips, (unsigned)parts);
-#define LIBGEMM_GO(ACT) act_backward_kernel<T, Z, ACT><<<grid, 256, 0, s>>>(a, lpr)
+#define LIBGEMM_GO(ACT)                                                                            \
+    do {                                                                                           \
+        if (a.cols < 8) act_backward_kernel<T, Z, ACT, NARROW><<<grid, 256, 0, s>>>(a, lpr);       \
+        else if (a.cols % 8) act_backward_kernel<T, Z, ACT, CUT><<<grid, 256, 0, s>>>(a, lpr);     \
+        else act_backward_kernel<T, Z, ACT, WHOLE><<<grid, 256, 0, s>>>(a, lpr);                   \
+    } while (0)
     switch (act) {
         case ACT_RELU: LIBGEMM_GO(ACT_RELU); break;
         case ACT_GELU: LIBGEMM_GO(ACT_GELU); break;

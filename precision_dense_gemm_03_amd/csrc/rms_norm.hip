@@ -97,34 +97,34 @@ __device__ __forceinline__ int count8(int64_t c, int64_t width) {
     return left >= 8 ? 8 : (left > 0 ? (int)left : 0);
 }
 
-// A row's chunks in a lane's registers: eight values from column c on, c = first +
-// 512 W k. V8: rows of whole chunks, which are loaded without conditions (a chunk past
-// the row's end is its last one) and all before the first is looked at.
-template <int T, int W, int CH, bool V8>
+// MODE: rows of whole pieces of eight columns, rows that cut the last one (Piece8),
+// rows of fewer than eight.
+enum { WHOLE = 0, CUT = 1, NARROW = 2 };
+
+// A row's pieces in a lane's registers: piece k at column first + 512 W k. They are
+// loaded without conditions (one past the row's end is its last) and all before the
+// first is looked at; what is no piece is zeros.
+template <int T, int W, int CH, int MODE>
 struct Chunks {
-    Raw8<T> raw[V8 ? CH : 1];
+    Raw8<T> raw[MODE == NARROW ? 1 : CH];
     float v[CH][8];
 
     __device__ __forceinline__ void fetch(const void* base, const uint8_t* scales, int64_t r, int64_t width, int first) {
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const int c = first + k * 512 * W;
-            if constexpr (V8) {
-                const int at = min(c, (int)width - 8);
-                fetch8<T>(raw[k], base, r * width + at,
-                          T >= OUT_E4M3 ? scales + r * ((width + kMxBlock - 1) / kMxBlock) + at / kMxBlock : nullptr);
-            } else {
-                load_row8<T>(base, scales, r, c, width, v[k]);
-            }
+            if constexpr (MODE == NARROW) load_row8<T>(base, scales, r, c, width, v[k]);
+            else fetch8<T, MODE == CUT>(raw[k], base, scales, r, width, Piece8(c, width));
         }
     }
 
     __device__ __forceinline__ void values(int64_t width, int first) {
-        if constexpr (V8) {
+        if constexpr (MODE != NARROW) {
 #pragma unroll
             for (int k = 0; k < CH; ++k) {
-                values8<T>(raw[k], v[k]);
-                if (first + k * 512 * W >= width) {
+                const Piece8 p(first + k * 512 * W, width);
+                values8<T, MODE == CUT>(raw[k], p.skip, v[k]);
+                if (p.skip >= 8) {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[k][i] = 0.0f;
                 }
@@ -133,21 +133,44 @@ struct Chunks {
     }
 };
 
+// Where a lane's piece k is stored and how many values of it; and whether value i
+// counts in a row's sums (a cut piece's first values are another lane's).
+template <int W, int MODE>
+struct Place {
+    int64_t at;
+    int n, skip;
+    __device__ __forceinline__ Place(int first, int k, int64_t width) {
+        const int c = first + k * 512 * W;
+        if constexpr (MODE == NARROW) {
+            at = c;
+            n = c < width ? (int)width : 0;
+            skip = 0;
+        } else {
+            const Piece8 p(c, width);
+            at = p.at;
+            skip = p.skip;
+            n = skip < 8 ? 8 : 0;
+        }
+    }
+    __device__ __forceinline__ bool counts(int i) const { return MODE != CUT || i >= skip; }
+};
+
 // W waves per row (W = 1: four rows per workgroup), CH chunks per lane. Lane l of
 // the row's W * 64 takes chunks l, l + 64 W, ..
-template <int T, int OUT, int W, int CH, bool V8>
+template <int T, int OUT, int W, int CH, int MODE>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArgs a) {
     constexpr int RPW = W == 1 ? 4 : 1;
     __shared__ float red[2][W][2];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int first = 8 * (W == 1 ? lane : (int)threadIdx.x);
-    float w[CH][8];
-#pragma unroll
-    for (int k = 0; k < CH; ++k) load8<OUT_F32>(a.weight, first + k * 512 * W, count8(first + k * 512 * W, a.width), 1.0f, w[k]);
+    Chunks<OUT_F32, W, CH, MODE> weight;
+    weight.fetch(a.weight, nullptr, 0, a.width, first);
+    weight.values(a.width, first);
+    float (&w)[CH][8] = weight.v;
     int half = 0;
     for (int64_t r = (int64_t)blockIdx.x * RPW + (W == 1 ? wave : 0); r < a.rows; r += (int64_t)gridDim.x * RPW) {
         const int64_t base = r * a.width;
-        Chunks<T, W, CH, V8> x, res;
+        Chunks<T, W, CH, MODE> x, res;
         x.fetch(a.x, nullptr, r, a.width, first);
         if (a.residual) res.fetch(a.residual, nullptr, r, a.width, first);
         x.values(a.width, first);
@@ -160,13 +183,11 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArg
         float sum = 0.0f, most = 0.0f;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            if (a.h) {
-                const int c = first + k * 512 * W;
-                store8<T>(a.h, base + c, count8(c, a.width), v[k]);
-            }
+            const Place<W, MODE> p(first, k, a.width);
+            if (a.h && p.n) store8<T>(a.h, base + p.at, MODE == NARROW ? p.n : 8, v[k]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sum = __builtin_fmaf(v[k][i], v[k][i], sum);
+                sum = __builtin_fmaf(v[k][i], p.counts(i) ? v[k][i] : 0.0f, sum);
                 v[k][i] *= w[k][i];
                 if constexpr (is_fp8<OUT>) most = max_nan(most, __builtin_fabsf(v[k][i]));
             }
@@ -179,8 +200,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArg
         const float factor = row_factor<OUT>(rstd, most, a.pow2, scale);
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = first + k * 512 * W;
-            store_y<OUT>(a.y, base + c, count8(c, a.width), v[k], factor);
+            const Place<W, MODE> p(first, k, a.width);
+            if (p.n) store_y<OUT>(a.y, base + p.at, MODE == NARROW ? p.n : 8, v[k], factor);
         }
         if (first == 0) {
             if (a.rstd) a.rstd[r] = rstd;
@@ -243,25 +264,26 @@ __global__ __launch_bounds__(512) void rms_norm_long_kernel(NormArgs a) {
 // ---------------------------------------------------------------- gradient
 
 // T: type of dy, dh and dx; H: of h (8-bit values with scales among them).
-template <int T, int H, int W, int CH, bool V8>
+template <int T, int H, int W, int CH, int MODE>
 __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kernel(NormBackwardArgs a) {
     constexpr int RPW = W == 1 ? 4 : 1;
     __shared__ float red[2][W];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     const int first = 8 * (W == 1 ? lane : (int)threadIdx.x);
-    float w[CH][8], dw[CH][8];
+    Chunks<OUT_F32, W, CH, MODE> weight;
+    weight.fetch(a.weight, nullptr, 0, a.width, first);
+    weight.values(a.width, first);
+    float (&w)[CH][8] = weight.v;
+    float dw[CH][8];   // (of a cut piece's first values both lanes have the whole sum)
 #pragma unroll
-    for (int k = 0; k < CH; ++k) {
-        const int c = first + k * 512 * W;
-        load8<OUT_F32>(a.weight, c, count8(c, a.width), 1.0f, w[k]);
+    for (int k = 0; k < CH; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[k][i] = 0.0f;
-    }
     int half = 0;
     for (int64_t r = (int64_t)blockIdx.x * RPW + (W == 1 ? wave : 0); r < a.rows; r += (int64_t)gridDim.x * RPW) {
         const int64_t base = r * a.width;
-        Chunks<H, W, CH, V8> hh;
-        Chunks<T, W, CH, V8> gg, dd;
+        Chunks<H, W, CH, MODE> hh;
+        Chunks<T, W, CH, MODE> gg, dd;
         const float rstd = a.rstd[r];
         hh.fetch(a.h, a.hscale, r, a.width, first);
         gg.fetch(a.dy, nullptr, r, a.width, first);
@@ -272,28 +294,30 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kerne
         float (&g)[CH][8] = gg.v;
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < CH; ++k)
+        for (int k = 0; k < CH; ++k) {
+            const Place<W, MODE> p(first, k, a.width);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 n[k][i] *= rstd;
                 dw[k][i] = __builtin_fmaf(g[k][i], n[k][i], dw[k][i]);
                 g[k][i] *= w[k][i];
-                sum = __builtin_fmaf(g[k][i], n[k][i], sum);
+                sum = __builtin_fmaf(g[k][i], p.counts(i) ? n[k][i] : 0.0f, sum);
             }
+        }
         const float mean = row_sum<W>(sum, red[half], wave) * a.inv_width;
         half ^= 1;
         if (a.dh) dd.values(a.width, first);
         float (&d)[CH][8] = dd.v;
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
-            const int c = first + k * 512 * W;
+            const Place<W, MODE> p(first, k, a.width);
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 o[i] = rstd * __builtin_fmaf(-n[k][i], mean, g[k][i]);
                 if (a.dh) o[i] += d[k][i];
             }
-            store8<T>(a.dx, base + c, count8(c, a.width), o);
+            if (p.n) store8<T>(a.dx, base + p.at, MODE == NARROW ? p.n : 8, o);
         }
     }
     if (!a.partial) return;
@@ -316,8 +340,8 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kerne
     }
 #pragma unroll
     for (int k = 0; k < CH; ++k) {
-        const int c = first + k * 512 * W;
-        store8<OUT_F32>(a.partial, (int64_t)blockIdx.x * a.width + c, count8(c, a.width), dw[k]);
+        const Place<W, MODE> p(first, k, a.width);
+        if (p.n) store8<OUT_F32>(a.partial, (int64_t)blockIdx.x * a.width + p.at, MODE == NARROW ? p.n : 8, dw[k]);
     }
 }
 
@@ -382,7 +406,9 @@ void by_width(int64_t width, F f) {
     else if (width <= 1024) f(IntC<1>{}, IntC<2>{});
     else if (width <= 2048) f(IntC<4>{}, IntC<1>{});
     else if (width <= 4096) f(IntC<4>{}, IntC<2>{});
+    else if (width <= 6144) f(IntC<4>{}, IntC<3>{});
     else if (width <= 8192) f(IntC<8>{}, IntC<2>{});
+    else if (width <= 12288) f(IntC<8>{}, IntC<3>{});
     else f(IntC<8>{}, IntC<4>{});   // (16 waves and 2 chunks: the gradient 158 us for 118 at 4096 x 16384)
 }
 
@@ -397,8 +423,13 @@ hipError_t norm_forward(const NormArgs& a, hipStream_t s) {
         constexpr int W = decltype(w)::value, CH = decltype(ch)::value, RPW = W == 1 ? 4 : 1;
         const int64_t blocks = (a.rows + RPW - 1) / RPW;
         const unsigned grid = (unsigned)(blocks < most ? blocks : most), nt = W == 1 ? 256 : 64 * W;
-        if (a.width % 8 == 0) rms_norm_kernel<T, OUT, W, CH, true><<<grid, nt, 0, s>>>(a);
-        else rms_norm_kernel<T, OUT, W, CH, false><<<grid, nt, 0, s>>>(a);
+        if (a.width % 8 == 0) {
+            rms_norm_kernel<T, OUT, W, CH, WHOLE><<<grid, nt, 0, s>>>(a);
+        } else if (a.width > 8) {
+            rms_norm_kernel<T, OUT, W, CH, CUT><<<grid, nt, 0, s>>>(a);
+        } else {
+            if constexpr (W * CH == 1) rms_norm_kernel<T, OUT, W, CH, NARROW><<<grid, nt, 0, s>>>(a);
+        }
     });
     return hipGetLastError();
 }
@@ -420,8 +451,13 @@ hipError_t norm_backward(const NormBackwardArgs& a, float* dweight, hipStream_t 
             constexpr int W = decltype(w)::value, CH = decltype(ch)::value;
             parts = norm_backward_parts(a.rows, a.width);
             constexpr unsigned nt = W == 1 ? 256 : 64 * W;
-            if (a.width % 8 == 0) rms_norm_backward_kernel<T, H, W, CH, true><<<(unsigned)parts, nt, 0, s>>>(b);
-            else rms_norm_backward_kernel<T, H, W, CH, false><<<(unsigned)parts, nt, 0, s>>>(b);
+            if (a.width % 8 == 0) {
+                rms_norm_backward_kernel<T, H, W, CH, WHOLE><<<(unsigned)parts, nt, 0, s>>>(b);
+            } else if (a.width > 8) {
+                rms_norm_backward_kernel<T, H, W, CH, CUT><<<(unsigned)parts, nt, 0, s>>>(b);
+            } else {
+                if constexpr (W * CH == 1) rms_norm_backward_kernel<T, H, W, CH, NARROW><<<(unsigned)parts, nt, 0, s>>>(b);
+            }
         });
     }
     hipError_t e = hipGetLastError();

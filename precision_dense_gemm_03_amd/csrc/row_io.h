@@ -107,31 +107,46 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float
     }
 }
 
-// The same in two steps, so that many loads can be in flight: eight whole values as
-// they lie in memory, and what they are.
+// A row in pieces of eight columns: piece c (c a multiple of 8) of a row of 8 columns
+// and more is read and written whole. The last one, where the row cuts it, is the
+// eight columns that end the row: the first `skip` of them are the piece's before it
+// (whose lane computes and stores the same). skip of 8 and more: no piece.
+struct Piece8 {
+    int64_t at;
+    int skip;
+    __device__ __forceinline__ Piece8(int64_t c, int64_t width) : at(min(c, width - 8)), skip((int)min(c - at, (int64_t)8)) {}
+};
+
+// The values above in two steps, so that many loads can be in flight: eight whole
+// values as they lie in memory, and what they are.
 template <int T>
 struct Raw8 {
     v4u w[T == OUT_F32 ? 2 : 1];   // (codes: two words)
-    uint32_t e;                    // the block's scale
+    uint32_t e, before;            // the block's scale, and that of a cut piece's first `skip`
 };
 
-template <int T>
-__device__ __forceinline__ void fetch8(Raw8<T>& x, const void* base, int64_t at, const uint8_t* scale) {
+// CUT: rows that may cut a piece. Row r of `width` columns, scales of 8-bit values.
+template <int T, bool CUT>
+__device__ __forceinline__ void fetch8(Raw8<T>& x, const void* base, const uint8_t* scales, int64_t r, int64_t width,
+                                       Piece8 p) {
+    const int64_t at = r * width + p.at;
     if constexpr (T == OUT_F32) {
-        const float* p = reinterpret_cast<const float*>(base) + at;
-        x.w[0] = *reinterpret_cast<const v4u_b1*>(p);
-        x.w[1] = *reinterpret_cast<const v4u_b1*>(p + 4);
+        const float* q = reinterpret_cast<const float*>(base) + at;
+        x.w[0] = *reinterpret_cast<const v4u_b1*>(q);
+        x.w[1] = *reinterpret_cast<const v4u_b1*>(q + 4);
     } else if constexpr (T == OUT_F16) {
         x.w[0] = *reinterpret_cast<const v4u_b1*>(reinterpret_cast<const _Float16*>(base) + at);
     } else {
         const v2u c = *reinterpret_cast<const v2u_b1*>(reinterpret_cast<const uint8_t*>(base) + at);
         x.w[0] = v4u{c[0], c[1], 0u, 0u};
-        x.e = *scale;
+        const uint8_t* s = scales + r * ((width + kMxBlock - 1) / kMxBlock);
+        x.before = s[p.at / kMxBlock];
+        x.e = CUT ? s[(p.at + 7) / kMxBlock] : x.before;
     }
 }
 
-template <int T>
-__device__ __forceinline__ void values8(const Raw8<T>& x, float (&v)[8]) {
+template <int T, bool CUT>
+__device__ __forceinline__ void values8(const Raw8<T>& x, int skip, float (&v)[8]) {
     if constexpr (T == OUT_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = bits_f32(x.w[i / 4][i % 4]);
@@ -140,16 +155,17 @@ __device__ __forceinline__ void values8(const Raw8<T>& x, float (&v)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
     } else {
-        const float s = mx_scale(x.e);
+        const float s = mx_scale(x.e), before = CUT ? mx_scale(x.before) : s;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int w = (int)x.w[0][i / 2];
+            const float s0 = CUT && 2 * i < skip ? before : s, s1 = CUT && 2 * i + 1 < skip ? before : s;
             if constexpr (T == OUT_E5M2) {
                 const auto p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_bf8(w, true) : __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
-                v[2 * i] = p[0] * s, v[2 * i + 1] = p[1] * s;
+                v[2 * i] = p[0] * s0, v[2 * i + 1] = p[1] * s1;
             } else {
                 const auto p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-                v[2 * i] = p[0] * s, v[2 * i + 1] = p[1] * s;
+                v[2 * i] = p[0] * s0, v[2 * i + 1] = p[1] * s1;
             }
         }
     }
