@@ -104,8 +104,8 @@ struct BiasActExtra {
     __device__ __forceinline__ int exponent(float m) const {
         return z_dtype == OUT_E5M2 ? mx_exponent<FMT_E5M2>(m) : mx_exponent<FMT_E4M3>(m);
     }
-    __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) const {
-        return z_dtype == OUT_E5M2 ? mx_pack4<FMT_E5M2>(a, b, c, d) : mx_pack4<FMT_E4M3>(a, b, c, d);
+    __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float power) const {
+        return z_dtype == OUT_E5M2 ? mx_pack4<FMT_E5M2>(a, b, c, d, power) : mx_pack4<FMT_E4M3>(a, b, c, d, power);
     }
     __device__ __forceinline__ void put_exponent(int row, int col, int N, int e) const {
         zscale[(int64_t)row * ((N + kMxBlock - 1) / kMxBlock) + col / kMxBlock] = (uint8_t)(e + 127);
@@ -165,11 +165,11 @@ struct BiasActExtra {
                     m = fmaxf(m, __shfl_xor(m, 16, 64));
                     m = fmaxf(m, __shfl_xor(m, 32, 64));
                     const int e = exponent(m);
-                    const float inv = mx_inverse(e);
+                    const float power = mx_power(e);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const v4f v = acc[t + u] * inv;
-                        const uint32_t w = codes4(v[0], v[1], v[2], v[3]);
+                        const v4f v = acc[t + u];
+                        const uint32_t w = codes4(v[0], v[1], v[2], v[3], power);
                         const int col = col0 + 16 * (t + u);
                         uint8_t* p = reinterpret_cast<uint8_t*>(Z) + (int64_t)row * N + col;
                         if (col + 4 <= N) {
@@ -240,14 +240,14 @@ struct BiasActExtra {
 #pragma unroll
                         for (int d = 1; d < 16; d <<= 1) m = fmaxf(m, __shfl_xor(m, d, 64));
                         const int e = exponent(m);
-                        const float inv = mx_inverse(e);
+                        const float power = mx_power(e);
                         if (row >= M) continue;
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int col = col0 + 16 * (t + u);
                             if (col < N)
                                 reinterpret_cast<uint8_t*>(Z)[(int64_t)row * N + col] =
-                                    (uint8_t)codes4(acc[tm][t + u][r] * inv, 0.0f, 0.0f, 0.0f);
+                                    (uint8_t)codes4(acc[tm][t + u][r], 0.0f, 0.0f, 0.0f, power);
                         }
                         if ((threadIdx.x & 15) == 0 && col0 + 16 * t < N) put_exponent(row, col0 + 16 * t, N, e);
                     }
@@ -551,18 +551,18 @@ private:
             }
             m = fmaxf(m, __shfl_xor(m, 32, 64));
             const int e = exponent(m);
-            const float inv = mx_inverse(e);
+            const float power = mx_power(e);
             both |= (uint32_t)(e + 127) << (8 * j);
             if (z_dtype == OUT_E5M2) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     stage8(ep, lr, 32 * j + 8 * q + 4 * h,
-                           mx_pack4<FMT_E5M2>(v[j][4 * q] * inv, v[j][4 * q + 1] * inv, v[j][4 * q + 2] * inv, v[j][4 * q + 3] * inv));
+                           mx_pack4<FMT_E5M2>(v[j][4 * q], v[j][4 * q + 1], v[j][4 * q + 2], v[j][4 * q + 3], power));
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     stage8(ep, lr, 32 * j + 8 * q + 4 * h,
-                           mx_pack4<FMT_E4M3>(v[j][4 * q] * inv, v[j][4 * q + 1] * inv, v[j][4 * q + 2] * inv, v[j][4 * q + 3] * inv));
+                           mx_pack4<FMT_E4M3>(v[j][4 * q], v[j][4 * q + 1], v[j][4 * q + 2], v[j][4 * q + 3], power));
             }
         }
         // lane h of a row stores the scale of its half of the columns

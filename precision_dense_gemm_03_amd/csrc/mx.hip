@@ -11,26 +11,81 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// The lanes of a wave that hold one block agree on its exponent, and each gives its
-// 8 codes. T: the source's type.
-template <int T, int FMT>
-__device__ __forceinline__ int block_codes(float (&v)[8], uint32_t& lo, uint32_t& hi) {
-    if constexpr (T == OUT_F16) {
-        constexpr float top = FMT == FMT_E5M2 ? 57344.0f : 61440.0f;
+// Eight values as they lie in memory (n of them exist, the others are zeros).
+template <int T>
+__device__ __forceinline__ void load_raw(const void* base, int64_t at, int n, uint32_t (&w)[T == OUT_F16 ? 4 : 8]) {
+    constexpr int W = T == OUT_F16 ? 4 : 8;
+    if (n >= 8) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)   // (infinities and NaN stay)
-            if (__builtin_fabsf(v[i]) > top && __builtin_fabsf(v[i]) < __builtin_inff()) v[i] = __builtin_copysignf(top, v[i]);
+        for (int k = 0; k < W / 4; ++k) {
+            const v4u v = T == OUT_F16 ? *reinterpret_cast<const v4u_b1*>(reinterpret_cast<const _Float16*>(base) + at)
+                                       : *reinterpret_cast<const v4u_b1*>(reinterpret_cast<const float*>(base) + at + 4 * k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 * k + i] = v[i];
+        }
+        return;
     }
-    float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i]));
-    m = fmaxf(m, __shfl_xor(m, 1, 64));
-    m = fmaxf(m, __shfl_xor(m, 2, 64));
-    const int e = mx_exponent<FMT>(m);
-    const float inv = mx_inverse(e);
-    lo = mx_pack4<FMT>(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-    hi = mx_pack4<FMT>(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-    return e;
+    for (int i = 0; i < W; ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (i >= n) continue;
+        if constexpr (T == OUT_F16)
+            w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(base)[at + i] << (16 * (i & 1));
+        else
+            w[i] = reinterpret_cast<const uint32_t*>(base)[at + i];
+    }
+}
+
+// The four lanes that hold a block of 32 agree on its exponent, and each gives its 8
+// codes. FP16 magnitudes are compared as 16-bit integers, two at a time; a block with
+// an infinity, a NaN or a value above the format's bound is looked at again.
+template <int T, int FMT>
+__device__ __forceinline__ int block_codes(uint32_t (&w)[T == OUT_F16 ? 4 : 8], uint32_t& lo, uint32_t& hi) {
+    if constexpr (T == OUT_F16) {
+        typedef uint16_t v2u16 __attribute__((ext_vector_type(2)));
+        constexpr uint32_t top = FMT == FMT_E5M2 ? 0x7B00u : 0x7B80u;   // 57344, 61440
+        auto largest = [&]() __attribute__((always_inline)) -> uint32_t {
+            v2u16 m = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = __builtin_elementwise_max(m, __builtin_bit_cast(v2u16, w[i] & 0x7FFF7FFFu));
+            return max((uint32_t)m[0], (uint32_t)m[1]);
+        };
+        uint32_t m = largest();
+        const uint32_t before[4] = {w[0], w[1], w[2], w[3]};
+        if (__builtin_amdgcn_ballot_w64(m > top) != 0) {
+            m = 0u;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int sh = 16 * (i & 1);
+                const uint32_t x = before[i / 2] >> sh & 0xFFFFu, a = x & 0x7FFFu;
+                const uint32_t y = a > top && a < 0x7C00u ? (x & 0x8000u) | top : x;
+                w[i / 2] = (w[i / 2] & ~(0xFFFFu << sh)) | (y << sh);
+                if (a < 0x7C00u) m = max(m, y & 0x7FFFu);
+            }
+        }
+        m = max(m, (uint32_t)__shfl_xor((int)m, 1, 64));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 2, 64));
+        const int e = mx_exponent<FMT>((float)__builtin_bit_cast(_Float16, (uint16_t)m));
+        const float power = mx_power(e);
+        lo = mx_pack4_f16<FMT>(w[0], w[1], power);
+        hi = mx_pack4_f16<FMT>(w[2], w[3], power);
+        return e;
+    } else {
+        float v[8], m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = bits_f32(w[i]);
+            m = fmaxf(m, finite_abs(v[i]));
+        }
+        m = fmaxf(m, __shfl_xor(m, 1, 64));
+        m = fmaxf(m, __shfl_xor(m, 2, 64));
+        const int e = mx_exponent<FMT>(m);
+        const float power = mx_power(e);
+        lo = mx_pack4<FMT>(v[0], v[1], v[2], v[3], power);
+        hi = mx_pack4<FMT>(v[4], v[5], v[6], v[7], power);
+        return e;
+    }
 }
 
 // Whole blocks in a row (cols % 32 == 0): x and q are one run of blocks, U units of
@@ -39,17 +94,15 @@ template <int T, int FMT, int U>
 __global__ __launch_bounds__(kThreads) void mx_flat_kernel(const void* __restrict__ x, int64_t units,
                                                            uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
     const int64_t first = wide_block() * (kThreads * U) + threadIdx.x;
-    float v[U][8];
+    uint32_t w[U][T == OUT_F16 ? 4 : 8];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        const int64_t at = first + u * kThreads;
-        load8<T>(x, at * 8, at < units ? 8 : 0, 1.0f, v[u]);
-    }
+    for (int u = 0; u < U; ++u)   // (past the end: the last unit again)
+        load_raw<T>(x, min(first + u * kThreads, units - 1) * 8, 8, w[u]);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t at = first + u * kThreads;
         uint32_t lo, hi;
-        const int e = block_codes<T, FMT>(v[u], lo, hi);
+        const int e = block_codes<T, FMT>(w[u], lo, hi);
         if (at >= units) continue;
         *reinterpret_cast<v2u_b1*>(q + at * 8) = v2u{lo, hi};
         if ((threadIdx.x & 3) == 0) scale[at >> 2] = (uint8_t)(e + 127);
@@ -66,10 +119,9 @@ __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const void* __restric
         for (int64_t c0 = 0; c0 < cols; c0 += 512) {
             const int64_t c = c0 + 8 * lane, left = cols - c;
             const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-            float v[8];
-            load8<T>(x, r * cols + c, n, 1.0f, v);
-            uint32_t lo, hi;
-            const int e = block_codes<T, FMT>(v, lo, hi);
+            uint32_t w[T == OUT_F16 ? 4 : 8], lo, hi;
+            load_raw<T>(x, r * cols + c, n, w);
+            const int e = block_codes<T, FMT>(w, lo, hi);
             if (n > 0) {
                 store_codes8(q + r * cols + c, n, lo, hi);
                 if ((lane & 3) == 0) scale[r * blocks + c / kMxBlock] = (uint8_t)(e + 127);

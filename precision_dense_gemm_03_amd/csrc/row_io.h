@@ -31,21 +31,48 @@ __device__ __forceinline__ int mx_exponent(float m) {
     return m > 0.0f ? max(e, -127) : 0;
 }
 
-// 2^-e for e in [-127, 127].
-__device__ __forceinline__ float mx_inverse(int e) { return e == 127 ? bits_f32(0x00400000u) : bits_f32((uint32_t)(127 - e) << 23); }
+// 2^e for e in [-127, 127].
+__device__ __forceinline__ float mx_power(int e) { return mx_scale((uint32_t)(e + 127)); }
 
-// Four codes of values that are in the format's range, infinite or NaN.
+// Four codes of values / 2^e (given as mx_power) that are in the format's range,
+// infinite or NaN. The scaled conversions round to nearest even (checked against the
+// plain ones for every FP16 value and every scale that leaves it in range).
 template <int FMT>
-__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d) {
-    uint32_t w = 0u;
+__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d, float power) {
+    typedef short v2s __attribute__((ext_vector_type(2)));
+    v2s w = {0, 0};
     if constexpr (FMT == FMT_E5M2) {
-        w = (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(a, b, (int)w, false);
-        w = (uint32_t)__builtin_amdgcn_cvt_pk_bf8_f32(c, d, (int)w, true);
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, a, b, power, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f32(w, c, d, power, true);
     } else {
-        w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(a, b, (int)w, false);
-        w = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, (int)w, true);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, a, b, power, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(w, c, d, power, true);
     }
-    return w;
+    return __builtin_bit_cast(uint32_t, w);
+}
+
+// The same of four FP16 values, two to a word.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_pack4_f16(uint32_t lo, uint32_t hi, float power) {
+    typedef short v2s __attribute__((ext_vector_type(2)));
+    typedef _Float16 v2hh __attribute__((ext_vector_type(2)));
+    const v2hh a = __builtin_bit_cast(v2hh, lo), b = __builtin_bit_cast(v2hh, hi);
+    v2s w = {0, 0};
+    if constexpr (FMT == FMT_E5M2) {
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(w, a, power, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_bf8_f16(w, b, power, true);
+    } else {
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, a, power, false);
+        w = __builtin_amdgcn_cvt_scalef32_pk_fp8_f16(w, b, power, true);
+    }
+    return __builtin_bit_cast(uint32_t, w);
+}
+
+// Two codes of a word (its upper half: HI) times a scale.
+template <int FMT, bool HI>
+__device__ __forceinline__ auto mx_pair(uint32_t w, float scale) {
+    if constexpr (FMT == FMT_E5M2) return __builtin_amdgcn_cvt_scalef32_pk_f32_bf8(w, scale, HI);
+    else return __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(w, scale, HI);
 }
 
 // |x| of a finite x, 0 of others.
@@ -78,20 +105,12 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float
             for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
         } else {
             const v2u w = *reinterpret_cast<const v2u_b1*>(reinterpret_cast<const uint8_t*>(base) + at);
+            constexpr int F = T == OUT_E5M2 ? FMT_E5M2 : FMT_E4M3;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                if constexpr (T == OUT_E5M2) {
-                    const auto lo = __builtin_amdgcn_cvt_pk_f32_bf8((int)w[i], false);
-                    const auto hi = __builtin_amdgcn_cvt_pk_f32_bf8((int)w[i], true);
-                    v[4 * i] = lo[0], v[4 * i + 1] = lo[1], v[4 * i + 2] = hi[0], v[4 * i + 3] = hi[1];
-                } else {
-                    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
-                    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-                    v[4 * i] = lo[0], v[4 * i + 1] = lo[1], v[4 * i + 2] = hi[0], v[4 * i + 3] = hi[1];
-                }
+                const auto lo = mx_pair<F, false>(w[i], scale), hi = mx_pair<F, true>(w[i], scale);
+                v[4 * i] = lo[0], v[4 * i + 1] = lo[1], v[4 * i + 2] = hi[0], v[4 * i + 3] = hi[1];
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= scale;
         }
         return;
     }
@@ -155,17 +174,16 @@ __device__ __forceinline__ void values8(const Raw8<T>& x, int skip, float (&v)[8
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
     } else {
+        constexpr int F = T == OUT_E5M2 ? FMT_E5M2 : FMT_E4M3;
         const float s = mx_scale(x.e), before = CUT ? mx_scale(x.before) : s;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int w = (int)x.w[0][i / 2];
-            const float s0 = CUT && 2 * i < skip ? before : s, s1 = CUT && 2 * i + 1 < skip ? before : s;
-            if constexpr (T == OUT_E5M2) {
-                const auto p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_bf8(w, true) : __builtin_amdgcn_cvt_pk_f32_bf8(w, false);
-                v[2 * i] = p[0] * s0, v[2 * i + 1] = p[1] * s1;
-            } else {
-                const auto p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8(w, true) : __builtin_amdgcn_cvt_pk_f32_fp8(w, false);
-                v[2 * i] = p[0] * s0, v[2 * i + 1] = p[1] * s1;
+        for (int i = 0; i < 2; ++i) {
+            const auto lo = mx_pair<F, false>(x.w[0][i], s), hi = mx_pair<F, true>(x.w[0][i], s);
+            v[4 * i] = lo[0], v[4 * i + 1] = lo[1], v[4 * i + 2] = hi[0], v[4 * i + 3] = hi[1];
+            if constexpr (CUT) {
+                const auto lb = mx_pair<F, false>(x.w[0][i], before), hb = mx_pair<F, true>(x.w[0][i], before);
+                v[4 * i] = 4 * i < skip ? lb[0] : lo[0], v[4 * i + 1] = 4 * i + 1 < skip ? lb[1] : lo[1];
+                v[4 * i + 2] = 4 * i + 2 < skip ? hb[0] : hi[0], v[4 * i + 3] = 4 * i + 3 < skip ? hb[1] : hi[1];
             }
         }
     }
