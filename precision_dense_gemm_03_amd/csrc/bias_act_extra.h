@@ -310,12 +310,13 @@ struct BiasActExtra {
             asm volatile("" : "+v"(lane), "+s"(N) : : "memory");
             const int lr = lane & 31, h = lane >> 5, lcol = col0 + 4 * h;   // this lane's columns: + 32 j + 8 q
             const int row = min(row0 + lr, M - 1);
+            const bool whole = col0 + 64 <= N;
             v4u held[4];
             if (res16) fetch16(held, lane, row0, col0, M, N);
             float v[2][16];
             if (channel) {
                 const float sa = sA[row];
-                each_run(sB, lcol, N, [&](int j, int q, v4f t) __attribute__((always_inline)) {
+                each_run(sB, lcol, N, whole, [&](int j, int q, v4f t) __attribute__((always_inline)) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[j][4 * q + e] = acc[0][j][4 * q + e] * (sa * t[e]);
                 });
@@ -326,7 +327,7 @@ struct BiasActExtra {
                     for (int x = 0; x < 16; ++x) v[j][x] = acc[0][j][x] * s;
             }
             if (bias) {
-                each_run(bias, lcol, N, [&](int j, int q, v4f t) __attribute__((always_inline)) {
+                each_run(bias, lcol, N, whole, [&](int j, int q, v4f t) __attribute__((always_inline)) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) v[j][4 * q + e] += t[e];
                 });
@@ -344,7 +345,7 @@ struct BiasActExtra {
             if (res16) {
                 add16(v, held, ep + kPart, lane);
             } else if (residual) {
-                each_run(reinterpret_cast<const float*>(residual) + (int64_t)row * N, lcol, N,
+                each_run(reinterpret_cast<const float*>(residual) + (int64_t)row * N, lcol, N, whole,
                          [&](int j, int q, v4f t) __attribute__((always_inline)) {
 #pragma unroll
                              for (int e = 0; e < 4; ++e) v[j][4 * q + e] += t[e];
@@ -381,11 +382,11 @@ private:
     static __device__ __forceinline__ void lds_done() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
     // f(j, q, values) for the lane's eight runs of four columns of a row of FP32s;
-    // what lies past N is some value of the row.
+    // what lies past N is some value of the row. whole: the wave's columns all exist.
     template <class F>
-    static __device__ __forceinline__ void each_run(const float* p, int lcol, int N, F f) {
+    static __device__ __forceinline__ void each_run(const float* p, int lcol, int N, bool whole, F f) {
         v4f t[8];
-        if ((N & 3) == 0) {
+        if (whole || (N & 3) == 0) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 t[k] = __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + min(lcol + 32 * (k / 4) + 8 * (k % 4), N - 4))));
@@ -441,19 +442,18 @@ private:
         v4u w[4];
 #pragma unroll
         for (int p = 0; p < 4; ++p) w[p] = *(const LDS_AS v4u*)at16(ep, 8 * p + (lane >> 3), 16 * seg);
-        if (N % VE == 0) {
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-                if (row0 + 8 * p + (lane >> 3) < M && col < N) {
-                    if constexpr (LINES) __builtin_nontemporal_store(w[p], reinterpret_cast<v4u*>(d + (int64_t)(8 * p) * N * ES));
-                    else *reinterpret_cast<v4u_b1*>(d + (int64_t)(8 * p) * N * ES) = w[p];
-                }
-        } else {
+        for (int p = 0; p < 4; ++p)
+            if (row0 + 8 * p + (lane >> 3) < M && col + VE <= N) {
+                if constexpr (LINES) __builtin_nontemporal_store(w[p], reinterpret_cast<v4u*>(d + (int64_t)(8 * p) * N * ES));
+                else *reinterpret_cast<v4u_b1*>(d + (int64_t)(8 * p) * N * ES) = w[p];
+            }
+        if (N % VE != 0) {   // the piece that ends a row
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
                 for (int e = 0; e < VE; ++e)
-                    if (row0 + 8 * p + (lane >> 3) < M && col + e < N) {
+                    if (row0 + 8 * p + (lane >> 3) < M && col + e < N && col + VE > N) {
                         uint8_t* at = d + ((int64_t)(8 * p) * N + e) * ES;
                         if constexpr (ES == 4) *reinterpret_cast<uint32_t*>(at) = w[p][e];
                         else *reinterpret_cast<uint16_t*>(at) = (uint16_t)(w[p][e / 2] >> (16 * (e & 1)));
@@ -465,11 +465,12 @@ private:
     // 32 rows of the FP16 residual, in 16-byte pieces of rows.
     __device__ __forceinline__ void fetch16(v4u (&held)[4], int lane, int row0, int col0, int M, int N) const {
         const int col = col0 + 8 * (lane & 7);
+        const bool whole = col0 + 64 <= N;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
             const _Float16* s =
                 reinterpret_cast<const _Float16*>(residual) + (int64_t)min(row0 + 8 * p + (lane >> 3), M - 1) * N;
-            if ((N & 7) == 0) {
+            if (whole || (N & 7) == 0) {
                 if constexpr (LINES) held[p] = __builtin_nontemporal_load(reinterpret_cast<const v4u*>(s + min(col, N - 8)));
                 else held[p] = *reinterpret_cast<const v4u_b1*>(s + min(col, N - 8));
             } else {
@@ -512,16 +513,15 @@ private:
             const int r = 16 * p + (lane >> 2);
             w[p] = *(const LDS_AS v4u*)(ep + r * 64 + 16 * (seg ^ ((r >> 2) & 3)));
         }
-        if ((N & 15) == 0) {
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                if (row0 + 16 * p + (lane >> 2) < M && col < N) *reinterpret_cast<v4u_b1*>(d + (int64_t)(16 * p) * N) = w[p];
-        } else {
+        for (int p = 0; p < 2; ++p)
+            if (row0 + 16 * p + (lane >> 2) < M && col + 16 <= N) *reinterpret_cast<v4u_b1*>(d + (int64_t)(16 * p) * N) = w[p];
+        if ((N & 15) != 0) {
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    if (row0 + 16 * p + (lane >> 2) < M && col + e < N)
+                    if (row0 + 16 * p + (lane >> 2) < M && col + e < N && col + 16 > N)
                         d[(int64_t)(16 * p) * N + e] = (uint8_t)(w[p][e / 4] >> (8 * (e % 4)));
         }
         lds_done();

@@ -78,22 +78,16 @@ __device__ __forceinline__ float elem(const uint8_t* p, int64_t idx) {
     else return fp8x2<F, false>((uint32_t)p[idx])[0];
 }
 
-// What becomes of an element's sum: scaled and stored, or with kFinish handed to
-// BiasActExtra (bias_act_extra.h).
-struct PlainStore {
-    static constexpr bool kFinish = false;
-};
-
 // ES: element bytes (2 FP16, 1 FP8). MMAX: largest M served. R: weight rows
 // per wave. U: 16-byte chunks of each row in flight per lane. NT: threads per
 // workgroup. FA, FB: FP8 formats of A and B (0 for FP16).
-template <int ES, int MMAX, int R, int U, int NT, int FA, int FB, class Ext>
+template <int ES, int MMAX, int R, int U, int NT, int FA, int FB>
 __global__ __launch_bounds__(NT) void gemv_kmajor_kernel(const uint8_t* __restrict__ A,
                                                                const uint8_t* __restrict__ B, void* __restrict__ C,
                                                                int M, int N, int64_t K, const float* __restrict__ sA,
                                                                const float* __restrict__ sB,
                                                                const float* __restrict__ sOut, int out_dtype,
-                                                               int vec, int eflags, Ext ext) {
+                                                               int vec, int eflags) {
     constexpr int VE = 16 / ES;
     const int lane = threadIdx.x & 63;
     const int64_t n0l = ((int64_t)blockIdx.x * (NT / 64) + (threadIdx.x >> 6)) * R;
@@ -164,8 +158,7 @@ __global__ __launch_bounds__(NT) void gemv_kmajor_kernel(const uint8_t* __restri
             for (int r = 0; r < R; ++r) acc[m][r] += __shfl_xor(acc[m][r], off, 64);
 
     const bool channel = (eflags & EPI_CHANNEL) != 0;
-    const float scale =
-        epilogue_base(sA, sB, sOut, !Ext::kFinish && (out_dtype == OUT_E4M3 || out_dtype == OUT_E5M2), channel);
+    const float scale = epilogue_base(sA, sB, sOut, out_dtype == OUT_E4M3 || out_dtype == OUT_E5M2, channel);
 #pragma unroll
     for (int m = 0; m < MMAX; ++m)
 #pragma unroll
@@ -174,11 +167,16 @@ __global__ __launch_bounds__(NT) void gemv_kmajor_kernel(const uint8_t* __restri
             if (lane == m * R + r && m < M && n < N) {
                 float y = acc[m][r] * scale;
                 if (channel) y *= sA[m] * sB[n];
-                if constexpr (Ext::kFinish) ext.finish1(y, m, (int)n, N);
-                else store_out(C, (int64_t)m * N + n, y, out_dtype);
+                store_out(C, (int64_t)m * N + n, y, out_dtype);
             }
         }
 }
+
+// What becomes of an element: stored, or with kFinish handed to BiasActExtra
+// (bias_act_extra.h).
+struct PlainStore {
+    static constexpr bool kFinish = false;
+};
 
 // Workgroup-cooperative variant: the W waves of a workgroup read the same R
 // weight rows together (wave w takes chunks w*64 + lane + i*64*W), so each
@@ -244,8 +242,7 @@ __global__ __launch_bounds__(64 * W) void gemv_kmajor_coop_kernel(const uint8_t*
     }
     __syncthreads();
     const bool channel = (eflags & EPI_CHANNEL) != 0;
-    const float scale =
-        epilogue_base(sA, sB, sOut, !Ext::kFinish && (out_dtype == OUT_E4M3 || out_dtype == OUT_E5M2), channel);
+    const float scale = epilogue_base(sA, sB, sOut, out_dtype == OUT_E4M3 || out_dtype == OUT_E5M2, channel);
     for (int o = threadIdx.x; o < MMAX * R; o += 64 * W) {
         const int m = o / R, r = o % R;
         const int64_t n = (int64_t)n0 + r;
@@ -263,8 +260,8 @@ __global__ __launch_bounds__(64 * W) void gemv_kmajor_coop_kernel(const uint8_t*
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
-template <int ES, int MMAX, int R, int W, int FA = 0, int FB = 0, class Ext = PlainStore>
-hipError_t launch_gemv_kmajor_coop(const GemmArgs& a, const Ext& ext = Ext{}) {
+template <int ES, int MMAX, int R, int W, int FA = 0, int FB = 0, class Ext>
+hipError_t coop(const GemmArgs& a, const Ext& ext) {
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
     if (a.M > MMAX || !a.b_kmajor || a.splits > 1) return hipErrorInvalidValue;
     if (ES == 1 && (a.fmt_a != FA || a.fmt_b != FB)) return hipErrorInvalidValue;
@@ -278,8 +275,13 @@ hipError_t launch_gemv_kmajor_coop(const GemmArgs& a, const Ext& ext = Ext{}) {
     return hipGetLastError();
 }
 
-template <int ES, int MMAX, int R, int U, int NT = 256, int FA = 0, int FB = 0, class Ext = PlainStore>
-hipError_t launch_gemv_kmajor(const GemmArgs& a, const Ext& ext = Ext{}) {
+template <int ES, int MMAX, int R, int W, int FA = 0, int FB = 0>
+hipError_t launch_gemv_kmajor_coop(const GemmArgs& a) {
+    return coop<ES, MMAX, R, W, FA, FB>(a, PlainStore{});
+}
+
+template <int ES, int MMAX, int R, int U, int NT = 256, int FA = 0, int FB = 0>
+hipError_t launch_gemv_kmajor(const GemmArgs& a) {
     static_assert(MMAX * R <= 64, "one lane stores each output");
     if (a.M <= 0 || a.N <= 0) return hipSuccess;
     if (a.M > MMAX || !a.b_kmajor || a.splits > 1) return hipErrorInvalidValue;
@@ -289,42 +291,32 @@ hipError_t launch_gemv_kmajor(const GemmArgs& a, const Ext& ext = Ext{}) {
     if (!launch_holds(blocks, NT)) return hipErrorInvalidValue;
     const int vec = aligned16(a.A) && aligned16(a.B) && ((a.K * ES) % 16 == 0);
     const int eflags = a.channel ? EPI_CHANNEL : 0;
-    gemv_kmajor_kernel<ES, MMAX, R, U, NT, FA, FB, Ext><<<(unsigned)blocks, NT, 0, a.stream>>>(
+    gemv_kmajor_kernel<ES, MMAX, R, U, NT, FA, FB><<<(unsigned)blocks, NT, 0, a.stream>>>(
         reinterpret_cast<const uint8_t*>(a.A), reinterpret_cast<const uint8_t*>(a.B), a.C, (int)a.M, (int)a.N, a.K,
-        a.sA, a.sB, a.sOut, a.out_dtype, vec, eflags, ext);
+        a.sA, a.sB, a.sOut, a.out_dtype, vec, eflags);
     return hipGetLastError();
 }
 
 // FP8 operand-format dispatch (every pair of E4M3 / E5M2).
-template <int MMAX, int R, int U, class Ext>
-hipError_t gemv_kmajor_fp8(const GemmArgs& a, const Ext& ext) {
+template <int MMAX, int R, int U>
+hipError_t launch_gemv_kmajor_fp8(const GemmArgs& a) {
     switch (a.fmt_a * 2 + a.fmt_b) {
-        case 0: return launch_gemv_kmajor<1, MMAX, R, U, 256, 0, 0>(a, ext);
-        case 1: return launch_gemv_kmajor<1, MMAX, R, U, 256, 0, 1>(a, ext);
-        case 2: return launch_gemv_kmajor<1, MMAX, R, U, 256, 1, 0>(a, ext);
-        default: return launch_gemv_kmajor<1, MMAX, R, U, 256, 1, 1>(a, ext);
+        case 0: return launch_gemv_kmajor<1, MMAX, R, U, 256, 0, 0>(a);
+        case 1: return launch_gemv_kmajor<1, MMAX, R, U, 256, 0, 1>(a);
+        case 2: return launch_gemv_kmajor<1, MMAX, R, U, 256, 1, 0>(a);
+        default: return launch_gemv_kmajor<1, MMAX, R, U, 256, 1, 1>(a);
     }
 }
 
-template <int MMAX, int R, int W, class Ext>
-hipError_t gemv_kmajor_coop_fp8(const GemmArgs& a, const Ext& ext) {
+template <int MMAX, int R, int W>
+hipError_t launch_gemv_kmajor_coop_fp8(const GemmArgs& a) {
     switch (a.fmt_a * 2 + a.fmt_b) {
-        case 0: return launch_gemv_kmajor_coop<1, MMAX, R, W, 0, 0>(a, ext);
-        case 1: return launch_gemv_kmajor_coop<1, MMAX, R, W, 0, 1>(a, ext);
-        case 2: return launch_gemv_kmajor_coop<1, MMAX, R, W, 1, 0>(a, ext);
-        default: return launch_gemv_kmajor_coop<1, MMAX, R, W, 1, 1>(a, ext);
+        case 0: return launch_gemv_kmajor_coop<1, MMAX, R, W, 0, 0>(a);
+        case 1: return launch_gemv_kmajor_coop<1, MMAX, R, W, 0, 1>(a);
+        case 2: return launch_gemv_kmajor_coop<1, MMAX, R, W, 1, 0>(a);
+        default: return launch_gemv_kmajor_coop<1, MMAX, R, W, 1, 1>(a);
     }
 }
-
-// The table's launchers.
-template <int MMAX, int R, int W>
-hipError_t coop_f16(const GemmArgs& a) { return launch_gemv_kmajor_coop<2, MMAX, R, W>(a); }
-template <int MMAX, int R, int U>
-hipError_t wave_f16(const GemmArgs& a) { return launch_gemv_kmajor<2, MMAX, R, U>(a); }
-template <int MMAX, int R, int U>
-hipError_t launch_gemv_kmajor_fp8(const GemmArgs& a) { return gemv_kmajor_fp8<MMAX, R, U>(a, PlainStore{}); }
-template <int MMAX, int R, int W>
-hipError_t launch_gemv_kmajor_coop_fp8(const GemmArgs& a) { return gemv_kmajor_coop_fp8<MMAX, R, W>(a, PlainStore{}); }
 
 }  // namespace
 
@@ -346,13 +338,13 @@ hipError_t launch_gemv_kmajor_coop_fp8(const GemmArgs& a) { return gemv_kmajor_c
 // instantiated for the device while the table itself stays host data.
 const GemmConfig* gemv_kmajor_configs(int* count) {
     static const GemmConfig table[] = {
-        {"gemv_coop_f16_m1_r4_w8", KIND_F16, 3, 1, 4, 8, coop_f16<1, 4, 8>, 0, 0, 1},
-        {"gemv_bt_f16_m1_r4_u4", KIND_F16, 3, 1, 16, 4, wave_f16<1, 4, 4>, 0, 0, 1},
-        {"gemv_bt_f16_m4_r2_u4", KIND_F16, 3, 4, 8, 4, wave_f16<4, 2, 4>, 0, 0, 1},
-        {"gemv_bt_f16_m4_r4_u2", KIND_F16, 3, 4, 16, 2, wave_f16<4, 4, 2>, 0, 0, 1},
-        {"gemv_coop_f16_m4_r2_w8", KIND_F16, 3, 4, 2, 8, coop_f16<4, 2, 8>, 0, 0, 1},
-        {"gemv_bt_f16_m8_r4_u2", KIND_F16, 3, 8, 16, 2, wave_f16<8, 4, 2>, 0, 0, 1},
-        {"gemv_bt_f16_m8_r2_u2", KIND_F16, 3, 8, 8, 2, wave_f16<8, 2, 2>, 0, 0, 1},
+        {"gemv_coop_f16_m1_r4_w8", KIND_F16, 3, 1, 4, 8, launch_gemv_kmajor_coop<2, 1, 4, 8>, 0, 0, 1},
+        {"gemv_bt_f16_m1_r4_u4", KIND_F16, 3, 1, 16, 4, launch_gemv_kmajor<2, 1, 4, 4>, 0, 0, 1},
+        {"gemv_bt_f16_m4_r2_u4", KIND_F16, 3, 4, 8, 4, launch_gemv_kmajor<2, 4, 2, 4>, 0, 0, 1},
+        {"gemv_bt_f16_m4_r4_u2", KIND_F16, 3, 4, 16, 2, launch_gemv_kmajor<2, 4, 4, 2>, 0, 0, 1},
+        {"gemv_coop_f16_m4_r2_w8", KIND_F16, 3, 4, 2, 8, launch_gemv_kmajor_coop<2, 4, 2, 8>, 0, 0, 1},
+        {"gemv_bt_f16_m8_r4_u2", KIND_F16, 3, 8, 16, 2, launch_gemv_kmajor<2, 8, 4, 2>, 0, 0, 1},
+        {"gemv_bt_f16_m8_r2_u2", KIND_F16, 3, 8, 8, 2, launch_gemv_kmajor<2, 8, 2, 2>, 0, 0, 1},
         // E4M3 M = 1, N = K = 4096, rotated cold weights: one row per wave
         // (1024 workgroups) 11.05 us, two 11.15, four 12.12
         {"gemv_bt_fp8_m1_r1_u4", KIND_FP8, 3, 1, 4, 4, launch_gemv_kmajor_fp8<1, 1, 4>, kAllFp8Pairs, 0, 1},
@@ -368,17 +360,8 @@ const GemmConfig* gemv_kmajor_configs(int* count) {
     return table;
 }
 
-// The products with bias and activation at decode sizes (kBiasActGemvF16, Fp8 rows):
-// for each bound M the kernel that the table has first.
-hipError_t launch_bias_act_gemv_f16(const BiasActArgs& a) {
-    const BiasActExtra<> ext = bias_act_extra(a);
-    return launch_gemv_kmajor_coop<2, 1, 4, 8>(a, ext);
-}
-
-hipError_t launch_bias_act_gemv_fp8(const BiasActArgs& a) {
-    const BiasActExtra<> ext = bias_act_extra(a);
-    if (a.M <= 1) return gemv_kmajor_fp8<1, 1, 4>(a, ext);
-    return gemv_kmajor_coop_fp8<4, 4, 4>(a, ext);
-}
+// The FP16 product of one row with bias and activation, on the kernel that the table
+// has first.
+hipError_t launch_bias_act_gemv_f16(const BiasActArgs& a) { return coop<2, 1, 4, 8>(a, bias_act_extra(a)); }
 
 }  // namespace libgemm

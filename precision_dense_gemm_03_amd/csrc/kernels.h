@@ -190,9 +190,7 @@ hipError_t launch_lora_pp_mixed(const LoraArgs& a);
 // Products with bias, activation and residual (bias_act.cpp chooses the kernel).
 hipError_t launch_bias_act(int kind, const BiasActArgs& a);
 const char* bias_act_kernel_name(int kind, const BiasActArgs& a);
-constexpr int64_t kBiasActGemvF16 = 1, kBiasActGemvFp8 = 4;   // rows up to which the decode kernels run
 hipError_t launch_bias_act_gemv_f16(const BiasActArgs& a);
-hipError_t launch_bias_act_gemv_fp8(const BiasActArgs& a);
 bool bias_act_ring_takes(int kind, const BiasActArgs& a);
 hipError_t launch_bias_act_ring_f16(const BiasActArgs& a, int shape);
 hipError_t launch_bias_act_ring_fp8(const BiasActArgs& a, int shape);   // shape: of kLoraRingShapes

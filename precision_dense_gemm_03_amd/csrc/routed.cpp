@@ -7,11 +7,14 @@
 #include <cstring>
 
 #include "kernels.h"
-#include "product_cost.h"
 
 namespace libgemm {
 
 namespace {
+
+constexpr int64_t kCus = 256;
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Whether the environment names this kernel (looked up once per call).
 struct Named {
@@ -85,6 +88,47 @@ bool shorter_tiles(const GroupedArgs& a) {
     return 0.91 * rounds(192.0) < rounds(256.0);
 }
 
+// Adapters: the sizes are known. 256-column tiles come in whole rounds; the
+// low-rank term costs `term` us a round and 32 of rank; the deep ring's rounds
+// are the bytes of its chosen tile (ring_cost, 64 x 64: 128) and its term us
+// per million of rows x columns x rank.
+struct LoraCost {
+    int bm, bn;
+    double per_k, least, more, term, fixed;
+};
+
+enum { L_PP_256, L_PP_192, L_RING, L_TILE_128, L_TILE_64, N_LORA };
+
+constexpr LoraCost kLora[2][N_LORA] = {{{256, 256, 30.3, 0, 0, 1.4, 18.0},
+                                        {192, 256, 21.1, 0, 0, 4.0, 18.0},
+                                        {0, 0, 8.3, 0.32, 0, 0.40, 9.9},
+                                        {128, 128, 10.8, 0.21, 1.16, 2.1, 18.0},
+                                        {64, 64, 4.9, 1.49, 0.09, 0.64, 13.0}},
+                                       {{256, 256, 21.8, 0, 0, 0.15, 18.0},
+                                        {192, 256, 16.0, 0, 0, 4.0, 18.0},
+                                        {0, 0, 5.1, 0.20, 0, 0.45, 12.9},
+                                        {128, 128, 8.6, 0.96, 0.01, 4.0, 18.0},
+                                        {64, 64, 3.1, 1.46, 0.48, 0.23, 12.9}}};
+
+double estimate(int which, const LoraCost& c, const LoraArgs& a, int64_t ring_cost) {
+    const double k = (double)a.K * 1e-3;
+    if (which == L_RING) {
+        double rounds = (double)ring_cost / 128.0;
+        if (rounds < c.least) rounds = c.least;
+        return rounds * k * c.per_k + c.fixed + (double)a.M * (double)a.N * (double)a.rank * c.term * 1e-6;
+    }
+    const int64_t tiles = ceil_div(a.M, c.bm) * ceil_div(a.N, c.bn);
+    double rounds;
+    if (c.bn == 256) {
+        rounds = (double)ceil_div(tiles, kCus);
+    } else {
+        rounds = (double)tiles / (double)kCus + c.more;
+        if (rounds < c.least) rounds = c.least;
+    }
+    const double share = tiles > kCus ? (double)tiles / (double)kCus : 1.0;
+    return rounds * k * c.per_k + c.fixed + share * (double)ceil_div(a.rank, 32) * c.term;
+}
+
 // The kernels by name, in the order of the enums.
 enum GroupedKernel { G_PP_256, G_PP_192, G_PP_128, G_RING, G_TILE_128, G_TILE_64 };
 constexpr const char* kGroupedNames[] = {"grouped_pp_256", "grouped_pp_192", "grouped_pp_128",
@@ -141,7 +185,7 @@ int choose_lora(int kind, const LoraArgs& a) {
         if ((i == L_PP_256 || i == L_PP_192) && !pp_ok) continue;
         if (i == L_PP_256 && mixed) continue;
         if (i == L_RING && !ring_ok) continue;
-        const double t = estimate(i, kLora[f16 ? 0 : 1][i], a.M, a.N, a.K, a.rank, cost);
+        const double t = estimate(i, kLora[f16 ? 0 : 1][i], a, cost);
         if (best < 0 || t < least) {
             best = i;
             least = t;

@@ -181,7 +181,7 @@ def test_binding_refusals():
 def test_queries():
     q = g.select_config_bias_act
     assert q(g.KIND_F16, g.OUT_F16, 1, 4096, 4096, b_kmajor=1) == "bias_act_gemv"
-    assert q(g.KIND_FP8, g.OUT_F16, 4, 4096, 4096, b_kmajor=1) == "bias_act_gemv"
+    assert q(g.KIND_FP8, g.OUT_F16, 1, 4096, 4096, b_kmajor=1) == "bias_act_ring"
     assert q(g.KIND_F16, g.OUT_F16, 1, 4096, 4096, b_kmajor=1, z_dtype=g.OUT_E4M3) != "bias_act_gemv"
     assert q(g.KIND_F16, g.OUT_F16, 1, 4096, 4096) == "bias_act_ring"
     assert q(g.KIND_F16, g.OUT_F16, 16, 4096, 4096, b_kmajor=1) == "bias_act_ring"
