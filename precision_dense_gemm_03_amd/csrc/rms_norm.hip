@@ -187,7 +187,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArg
             if (a.h && p.n) store8<T>(a.h, base + p.at, MODE == NARROW ? p.n : 8, v[k]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sum = __builtin_fmaf(v[k][i], p.counts(i) ? v[k][i] : 0.0f, sum);
+                if (p.counts(i)) sum = __builtin_fmaf(v[k][i], v[k][i], sum);
                 v[k][i] *= w[k][i];
                 if constexpr (is_fp8<OUT>) most = max_nan(most, __builtin_fabsf(v[k][i]));
             }
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_backward_kerne
                 n[k][i] *= rstd;
                 dw[k][i] = __builtin_fmaf(g[k][i], n[k][i], dw[k][i]);
                 g[k][i] *= w[k][i];
-                sum = __builtin_fmaf(g[k][i], p.counts(i) ? n[k][i] : 0.0f, sum);
+                if (p.counts(i)) sum = __builtin_fmaf(g[k][i], n[k][i], sum);
             }
         }
         const float mean = row_sum<W>(sum, red[half], wave) * a.inv_width;

@@ -258,3 +258,29 @@ def test_gradient_against_differences(width):
     size = (dx.double() * vx).abs().sum().item() + (dw.double() * vw).abs().sum().item()
     # REL of the terms' magnitudes for the kernels, 1e-6 of them for the difference (e^2 and rounding 2^-52 / e)
     assert abs(slope - along) <= 2 * REL * size
+
+
+@pytest.mark.parametrize("width", [67, 100, 1001, 4099, 12003])
+def test_infinity_at_a_cut_row_end(width):
+    """An infinity in one of the last eight columns, which two lanes read: the row is zeros beside it (its norm is
+    infinite) and NaN at it, as the formula says; in the gradient the other columns are infinite, of either sign."""
+    x = normal(gen(width), (9, width))
+    w = torch.ones(width, device=DEV)
+    for i in range(8):
+        x[i, width - 1 - i] = float("inf")
+    say(f"infinity at a row's end, width {width}")
+    y, rstd = torch.empty_like(x), torch.empty(9, device=DEV)
+    g.rms_norm(x, w, y, eps=EPS, rstd=rstd)
+    at = x.isinf()
+    assert bool(y[at].isnan().all()) and bool((y[:8][~at[:8]] == 0).all()) and bool((rstd[:8] == 0).all())
+    assert bool(y[8].isfinite().all()) and bool((y[8] != 0).any())
+    h = normal(gen(width + 1), (9, width))
+    h[h == 0] = 1.0
+    dx, _ = g.rms_norm_backward(x, h, w, torch.ones(9, device=DEV))
+    for i in range(8):
+        j = width - 1 - i
+        other = torch.arange(width, device=DEV) != j
+        want = -h[i].sign() * h[i, j].sign() * float("inf")
+        assert torch.equal(dx[i][other], want[other]), i
+        assert bool(dx[i, j].isnan())
+    assert bool(dx[8].isfinite().all())
