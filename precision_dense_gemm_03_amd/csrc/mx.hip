@@ -109,14 +109,15 @@ __global__ __launch_bounds__(kThreads) void mx_flat_kernel(const void* __restric
     }
 }
 
-// Any width: a wave goes along a row, 512 values at a time.
+// Any width: a wave goes along a row, 512 values at a time (its strip's, where rows
+// are few: row_grid).
 template <int T, int FMT>
 __global__ __launch_bounds__(kThreads) void mx_rows_kernel(const void* __restrict__ x, int64_t rows, int64_t cols,
                                                            uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
     const int lane = threadIdx.x & 63;
     const int64_t blocks = (cols + kMxBlock - 1) / kMxBlock, step = (int64_t)gridDim.x * (kThreads / 64);
     for (int64_t r = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); r < rows; r += step)
-        for (int64_t c0 = 0; c0 < cols; c0 += 512) {
+        for (int64_t c0 = 512 * (int64_t)blockIdx.y; c0 < cols; c0 += 512 * (int64_t)gridDim.y) {
             const int64_t c = c0 + 8 * lane, left = cols - c;
             const int n = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
             uint32_t w[T == OUT_F16 ? 4 : 8], lo, hi;
@@ -136,17 +137,20 @@ __global__ __launch_bounds__(kThreads) void mx_unpack_kernel(const uint8_t* __re
     const int lane = threadIdx.x & 63;
     const int64_t step = (int64_t)gridDim.x * (kThreads / 64);
     for (int64_t r = (int64_t)blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6); r < rows; r += step)
-        for (int64_t c = 8 * lane; c < cols; c += 512) {
+        for (int64_t c = 512 * (int64_t)blockIdx.y + 8 * lane; c < cols; c += 512 * (int64_t)gridDim.y) {
             float v[8];
             load_row8<FMT == FMT_E5M2 ? OUT_E5M2 : OUT_E4M3>(q, scale, r, c, cols, v);
             store8<T>(y, r * cols + c, cols - c >= 8 ? 8 : (int)(cols - c), v);
         }
 }
 
-// Workgroups of four rows each, as many as keep the chip busy.
-unsigned row_blocks(int64_t rows) {
-    const int64_t n = (rows + 3) / 4;
-    return (unsigned)(n < 256 * 16 ? n : 256 * 16);
+// Workgroups of four rows each, as many as keep the chip busy; few rows are cut into
+// strips of 512 columns and more.
+dim3 row_grid(int64_t rows, int64_t cols) {
+    const int64_t most = 256 * 16, n = (rows + 3) / 4, strips = (cols + 511) / 512;
+    if (n >= most) return dim3((unsigned)most);
+    const int64_t room = most / n;
+    return dim3((unsigned)n, (unsigned)(strips < room ? strips : room));
 }
 
 template <int T, int FMT>
@@ -160,7 +164,7 @@ hipError_t pack(const void* x, int64_t rows, int64_t cols, uint8_t* q, uint8_t* 
         if (few) mx_flat_kernel<T, FMT, 1><<<wide_grid(blocks), kThreads, 0, s>>>(x, units, q, scale);
         else mx_flat_kernel<T, FMT, U><<<wide_grid(blocks), kThreads, 0, s>>>(x, units, q, scale);
     } else {
-        mx_rows_kernel<T, FMT><<<row_blocks(rows), kThreads, 0, s>>>(x, rows, cols, q, scale);
+        mx_rows_kernel<T, FMT><<<row_grid(rows, cols), kThreads, 0, s>>>(x, rows, cols, q, scale);
     }
     return hipGetLastError();
 }
@@ -178,7 +182,7 @@ hipError_t launch_quantize_mx(const void* x, int dtype, int64_t rows, int64_t co
 
 hipError_t launch_dequantize_mx(const uint8_t* q, const uint8_t* scale, int fmt, int64_t rows, int64_t cols, void* y,
                                 int dtype, hipStream_t s) {
-    const unsigned grid = row_blocks(rows);
+    const dim3 grid = row_grid(rows, cols);
 #define LIBGEMM_GO(FMT, T) mx_unpack_kernel<FMT, T><<<grid, kThreads, 0, s>>>(q, scale, rows, cols, y)
     if (fmt == FMT_E5M2) {
         if (dtype == OUT_F16) LIBGEMM_GO(FMT_E5M2, OUT_F16);
