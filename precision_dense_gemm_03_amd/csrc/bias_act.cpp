@@ -20,7 +20,7 @@ constexpr const char* kNames[] = {"bias_act_pp_256", "bias_act_pp_192", "bias_ac
 
 // Estimated us, fits to measured times of 2600 shapes (1 to 16384 rows, 128 to 12288
 // columns, K from 128 to 8192, odd sizes among them, weights from beyond the caches):
-// choosing by them costs 1.1 % over the fastest of each shape, by the adapters'
+// choosing by them costs 1.0 to 1.2 % over the fastest of each shape, by the adapters'
 // constants (routed.cpp) 2.4 %. Rounds of tiles over compute units (the ping-pong
 // kernel's whole, one workgroup per unit; the others' with `more` for the uneven end
 // and no less than `least`; the deep ring's by its tile's bytes, 64 x 64: 1) take per_k

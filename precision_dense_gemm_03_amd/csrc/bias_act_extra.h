@@ -52,10 +52,9 @@ struct BiasActExtra {
     __device__ __forceinline__ float common() const { return channel ? 1.0f : (sA ? *sA : 1.0f) * (sB ? *sB : 1.0f); }
     __device__ __forceinline__ float out_factor() const { return out_dtype >= OUT_E4M3 ? 1.0f / *sOut : 1.0f; }
 
-    // Four neighbouring values of a row of FP32s, zero from N on (FULL: all below N).
-    template <bool FULL = false>
+    // Four neighbouring values of a row of FP32s, zero from N on.
     static __device__ __forceinline__ v4f row4(const float* p, int col, int N) {
-        if (FULL || col + 4 <= N) return __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + col)));
+        if (col + 4 <= N) return __builtin_bit_cast(v4f, v4u(*reinterpret_cast<const v4u_b1*>(p + col)));
         v4f v;
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = col + e < N ? p[col + e] : 0.0f;
@@ -111,7 +110,7 @@ struct BiasActExtra {
         zscale[(int64_t)row * ((N + kMxBlock - 1) / kMxBlock) + col / kMxBlock] = (uint8_t)(e + 127);
     }
 
-    // One element (decode kernels): acc is scaled already, per-channel factors too.
+    // One element (decode kernel): z is scaled already.
     __device__ __forceinline__ void finish1(float z, int row, int col, int N) const {
         if (bias) z += bias[col];
         const int64_t at = (int64_t)row * N + col;
