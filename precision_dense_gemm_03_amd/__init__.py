@@ -1194,6 +1194,15 @@ def moe_combine_backward(dy, z, row, weight, dZ=None, dweight=None, stream=None)
 
 # ------------------------------------------- a dense layer around its products
 
+def _codes_ptr(t, fmt=None):
+    """_ptr(_u8(t, fmt)) without making the view (1 us of a call)."""
+    torch = _torch()
+    have = FMT_E4M3 if t.dtype is torch.float8_e4m3fn else (FMT_E5M2 if t.dtype is torch.float8_e5m2 else None)
+    if t.dtype is torch.uint8 or (have is not None and (fmt is None or int(fmt) == have)):
+        return _ptr(t)
+    return _ptr(_u8(t, fmt))
+
+
 def _mx_codes(q, scale, fmt, what):
     """Pointers of 8-bit values q[rows, cols] and their scales [rows, ceil(cols / 32)]."""
     torch = _torch()
@@ -1206,7 +1215,7 @@ def _mx_codes(q, scale, fmt, what):
             raise ValueError(f"{what}'s scales must be uint8 or float8_e8m0fnu, not {scale.dtype}")
         scale = scale.view(torch.uint8)
     shape = (q.shape[0], (q.shape[1] + 31) // 32)
-    return _ptr(_u8(q, fmt)), _arg(scale, torch.uint8, shape, f"{what}'s scales")
+    return _codes_ptr(q, fmt), _arg(scale, torch.uint8, shape, f"{what}'s scales")
 
 
 def _held(t, scale, fmt, shape, what):
@@ -1214,10 +1223,10 @@ def _held(t, scale, fmt, shape, what):
     torch = _torch()
     dt = _out_dtype(t, fmt)
     if dt in (OUT_E4M3, OUT_E5M2):
-        if tuple(t.shape) != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{what} must have shape {tuple(shape)}, not {tuple(t.shape)}")
         return (*_mx_codes(t, scale, None, what), dt)
-    return _arg(t, t.dtype, torch.Size(shape), what), None, dt
+    return _arg(t, t.dtype, shape, what), None, dt
 
 
 def _opt(t, dtype, shape, what):
@@ -1241,7 +1250,7 @@ def rms_norm(x, weight, y, eps=1e-5, residual=None, h=None, scale=None, rstd=Non
         raise ValueError("FP8 output needs scale[rows]")
     f32 = torch.float32
     _check(lib().rms_norm(_ptr(x), _opt(residual, x.dtype, shape, "residual"), dt, _arg(weight, f32, (width,), "weight"),
-                          eps, _opt(h, x.dtype, shape, "h"), _ptr(_u8(y) if codes else y), yt,
+                          eps, _opt(h, x.dtype, shape, "h"), _ptr(y), yt,
                           _opt(scale if codes else None, f32, (rows,), "scale"), 1 if pow2 else 0,
                           _opt(rstd, f32, (rows,), "rstd"), rows, width, _stream_handle(stream)), "rms_norm")
     return y
@@ -1315,18 +1324,17 @@ def gemm_f16_bias_act_bt(A, Bt, C, bias=None, act=ACT_NONE, residual=None, Z=Non
 def _bias_act_fp8(name, A, fmt_a, B, fmt_b, sA, sB, C, bias, act, residual, Z, Zscale, channel, sOut, out_fmt, z_fmt,
                   stream, bt):
     torch = _torch()
-    A, B = _u8(A, fmt_a), _u8(B, fmt_b)
+    pa, pw = _codes_ptr(A, fmt_a), _codes_ptr(B, fmt_b)
     out = _out_dtype(C, out_fmt)
     codes = out in (OUT_E4M3, OUT_E5M2)
-    Cv = _u8(C) if codes else C
-    M, N, K = _dims_bt(A, B, Cv) if bt else _dims(A, B, Cv)
+    M, N, K = _dims_bt(A, B, C) if bt else _dims(A, B, C)
     for what, s, n in (("sA", sA, M if channel else 1), ("sB", sB, N if channel else 1),
                        ("sOut", sOut if codes else None, 1)):
         if s is not None and (s.dtype != torch.float32 or s.numel() != n):
             raise ValueError(f"{what} must hold {n} float32 scales")
-    pb, pr, rt, pz, ps, zt = _epilogue(Cv, bias, residual, Z, Zscale, z_fmt)
-    _check(getattr(lib(), name)(_ptr(A), int(fmt_a), _ptr(B), int(fmt_b), _ptr(sA), _ptr(sB), 1 if channel else 0,
-                                _ptr(sOut) if codes else None, pb, pr, rt, _ptr(Cv), out, int(act), pz, ps, zt, M, N,
+    pb, pr, rt, pz, ps, zt = _epilogue(C, bias, residual, Z, Zscale, z_fmt)
+    _check(getattr(lib(), name)(pa, int(fmt_a), pw, int(fmt_b), _ptr(sA), _ptr(sB), 1 if channel else 0,
+                                _ptr(sOut) if codes else None, pb, pr, rt, _ptr(C), out, int(act), pz, ps, zt, M, N,
                                 K, _stream_handle(stream)), name)
     return C
 
