@@ -24,10 +24,15 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
     wgrad_pp_kernel<OUT, LINES><<<grid, 512, 0, a.stream>>>(                                                \
         (const uint8_t*)a.A, (const uint8_t*)a.B, a.C, a.offsets, groups, rows, M, N, (int)tiles_m,        \
         (int)tiles_n, vec_out, MxOperand{})
-#define LIBGEMM_TILE(OUT, TS)                                                                                       \
-    wgrad_tile_kernel<OUT, TS><<<grid, 256, 0, a.stream>>>((const _Float16*)a.A, (const _Float16*)a.B, \
-                                                                       a.C, a.offsets, groups, rows, M, N,          \
-                                                                       (int)tiles_m, (int)tiles_n, MxOperand{})
+#define LIBGEMM_CUT(OUT, TS, CUT)                                                                     \
+    wgrad_tile_kernel<OUT, TS, CUT><<<grid, 256, 0, a.stream>>>(                                      \
+        (const _Float16*)a.A, (const _Float16*)a.B, a.C, a.offsets, groups, rows, M, N, (int)tiles_m, \
+        (int)tiles_n, MxOperand{})
+#define LIBGEMM_TILE(OUT, TS)                          \
+    do {                                               \
+        if (M % 8 || N % 8) LIBGEMM_CUT(OUT, TS, true); \
+        else LIBGEMM_CUT(OUT, TS, false);              \
+    } while (0)
     const bool f32 = a.out_dtype == OUT_F32;
     if (size == 256) {
         if (f32 && lines) LIBGEMM_PP(OUT_F32, true);
@@ -43,6 +48,7 @@ hipError_t launch_grouped_wgrad(const GroupedArgs& a) {
     }
 #undef LIBGEMM_PP
 #undef LIBGEMM_TILE
+#undef LIBGEMM_CUT
     return hipGetLastError();
 }
 

@@ -16,7 +16,11 @@
 //
 // wgrad_tile_kernel (operands of any alignment): 128 x 128 or 64 x 64 tiles, 4
 // waves, 64 rows at a time, one (128) or four (64) steps in registers ahead of
-// two LDS stages (the layout and padding of gemm_tile_impl.h's row-major B).
+// two LDS stages (the layout and padding of gemm_tile_impl.h's row-major B). A step
+// takes as long as its one wave per matrix core issues and waits in turn, so the
+// loop has no address products, no shifts for rows of whole pieces and no ways out
+// (10580 rows, 2304 x 216, 64 x 64: 125 -> 97 us with A in 8 bits; 7240 rows, 128 x
+// 3504, FP16: 48 -> 40).
 // A product of few tiles is bound by the steps one tile takes one after
 // another, so the smaller tile wins there: 1819 rows in 23 groups, 304 x 208:
 // 9.5 us with 64, 15.3 with 128, 19.5 ping-pong; 8192 rows in 8 groups, 2048 x
@@ -494,9 +498,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     }
 }
 
-// TS: tile rows and columns, 128 or 64.
-template <int OUT, int TS, int QS = 0, int FMT = 0>
-__global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restrict__ A,
+// TS: tile rows and columns, 128 or 64. KG: groups of four waves, each with its own
+// LDS stages, that take every KG-th step of 64 rows; their sums meet in the LDS, each
+// group storing one of the four blocks of a wave (in a fixed order: results repeat).
+template <int OUT, int TS, bool CUT, int QS = 0, int FMT = 0, int KG = 1>
+__global__ __launch_bounds__(256 * KG) void wgrad_tile_kernel(const _Float16* __restrict__ A,
                                                          const _Float16* __restrict__ B, void* __restrict__ C,
                                                          const int32_t* __restrict__ offsets, int groups, int rows,
                                                          int M, int N, int tiles_m, int tiles_n, MxOperand mx) {
@@ -504,49 +510,68 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
     constexpr int BK = 64, OP = WT::B_BYTES;   // one operand's stage
     constexpr int CPR = TS / 8, RPP = 256 / CPR, NC = BK / RPP;   // chunks of a row, rows of a pass, passes
     constexpr int WS = TS / 2, TB = TS / 32;   // a wave's rows and columns, in blocks of 16
-    __shared__ __attribute__((aligned(16))) uint8_t smem_raw[4 * OP];
-    LDS_AS uint8_t* smem = (LDS_AS uint8_t*)smem_raw;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
+    constexpr int ST = KG > 1 ? 1 : 2;         // LDS stages (of four groups two each do not fit)
+    static_assert(KG == 1 || KG == TB * TB, "a block of a wave for each group");
+    __shared__ __attribute__((aligned(16))) uint8_t smem_raw[2 * ST * OP * KG];
+    const int kg = KG > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 8) : 0;
+    LDS_AS uint8_t* smem = (LDS_AS uint8_t*)smem_raw + 2 * ST * OP * kg;
+    const int tid = threadIdx.x & 255, lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
     const WgradTile w = wgrad_tile<QS != 0>((int)wide_block(), offsets, groups, rows, tiles_m, tiles_n);
     if (w.group < 0) return;
     const int grp = w.group, m0 = w.tm * TS, n0 = w.tn * TS, lo = w.lo, hi = w.hi;
-    const int nk = (hi - lo + BK - 1) / BK;
+    const int nk = (hi - lo + BK * KG - 1) / (BK * KG);   // of a group: step kt KG + kg of all
 
     const int srow = tid / CPR, scol = tid % CPR;   // staged chunk: rows srow + RPP i, 16-byte column scol
-    constexpr int D = TS == 64 ? 4 : 1, U = D < 2 ? 2 : D;   // steps in registers ahead of the LDS; steps unrolled
+    // steps in registers ahead of the LDS (three of sixteen waves' fit); steps unrolled
+    constexpr int D = KG > 1 ? 3 : (TS == 64 ? 4 : 1), U = D < 2 ? 2 : D;
     v4u ra[D][NC], rb[D][NC];
-    // Loads go out without conditions: rows past the group's end are its last
-    // row and column chunks past the operand's end the last whole one (M, N of
-    // at least 8); store() clears the one and shifts the other down.
+    // Loads go out without conditions, in the order of the steps: a lane's pointers go
+    // down its rows and stay at the last that the group has, and column chunks past the
+    // operand's end are the last whole one (M, N of at least 8); store() clears the one
+    // and shifts the other down (CUT: M or N no multiple of 8).
     const int ca = m0 + 8 * scol, cb = n0 + 8 * scol, past_a = ca + 8 - M, past_b = cb + 8 - N;
-    const bool cut = (m0 + TS > M && M % 8 != 0) || (n0 + TS > N && N % 8 != 0);
-    const int64_t at_a = (int64_t)lo * M + max(min(ca, M - 8), 0), at_b = (int64_t)lo * N + max(min(cb, N - 8), 0);
-    const _Float16* src_a = A + at_a;
-    const _Float16* src_b = B + at_b;
     const int last = hi - lo - 1;
+    constexpr int ESA = QS == 1 ? 1 : 2, ESB = QS == 2 ? 1 : 2;   // bytes of an element
+    const uint8_t* pa[NC];
+    const uint8_t* pb[NC];
+    const uint8_t* ps[NC];   // scales of 8-bit values
+    int row[NC];
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+        row[i] = kg * BK + srow + RPP * i;
+        const int64_t r = lo + max(min(row[i], last), 0);
+        pa[i] = reinterpret_cast<const uint8_t*>(A) + (r * M + max(min(ca, M - 8), 0)) * ESA;
+        pb[i] = reinterpret_cast<const uint8_t*>(B) + (r * N + max(min(cb, N - 8), 0)) * ESB;
+        if constexpr (QS != 0) ps[i] = mx.scale + r * mx.blocks + min((QS == 1 ? ca : cb) / kMxBlock, (int)mx.blocks - 1);
+    }
+    const int64_t step_a = (int64_t)BK * KG * M * ESA, step_b = (int64_t)BK * KG * N * ESB,
+                  step_s = (int64_t)BK * KG * mx.blocks;
     // An operand of 8-bit values: eight codes and their scale's byte in a v4u.
-    const uint8_t* codes = QS == 1 ? (const uint8_t*)A + at_a : (const uint8_t*)B + at_b;
-    const int64_t qw = QS == 1 ? M : N;
-    const uint8_t* qscale =
-        QS ? mx.scale + (int64_t)lo * mx.blocks + min((QS == 1 ? ca : cb) / kMxBlock, (int)mx.blocks - 1) : nullptr;
-    auto load8 = [&](int64_t r) __attribute__((always_inline)) -> v4u {
-        const v2u c = *reinterpret_cast<const v2u_b1*>(codes + r * qw);
-        return v4u{c[0], c[1], (uint32_t)qscale[r * mx.blocks], 0u};
+    auto load8 = [](const uint8_t* p, const uint8_t* scale) __attribute__((always_inline)) -> v4u {
+        const v2u c = *reinterpret_cast<const v2u_b1*>(p);
+        return v4u{c[0], c[1], (uint32_t)*scale, 0u};
     };
-    auto widened = [&](v4u v, int past) __attribute__((always_inline)) -> v4u {
+    auto widened = [](v4u v, int past) __attribute__((always_inline)) -> v4u {
         uint64_t c = (uint64_t)v[0] | ((uint64_t)v[1] << 32);
-        c = past >= 8 ? 0 : (past > 0 ? c >> (8 * past) : c);
+        if constexpr (CUT) c = past >= 8 ? 0 : (past > 0 ? c >> (8 * past) : c);
         return mx_halves<FMT>((uint32_t)c, (uint32_t)(c >> 32), mx_scale(v[2]));
     };
-    auto load = [&](int kt, int set) __attribute__((always_inline)) {
+    auto load = [&](int set) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const int64_t r = min(kt * BK + srow + RPP * i, last);
-            if constexpr (QS == 1) ra[set][i] = load8(r);
-            else ra[set][i] = *reinterpret_cast<const tile::v4u_any*>(src_a + r * M);
-            if constexpr (QS == 2) rb[set][i] = load8(r);
-            else rb[set][i] = *reinterpret_cast<const tile::v4u_any*>(src_b + r * N);
+            if constexpr (QS == 1) ra[set][i] = load8(pa[i], ps[i]);
+            else ra[set][i] = *reinterpret_cast<const tile::v4u_any*>(pa[i]);
+            if constexpr (QS == 2) rb[set][i] = load8(pb[i], ps[i]);
+            else rb[set][i] = *reinterpret_cast<const tile::v4u_any*>(pb[i]);
+            row[i] += BK * KG;
+            const bool more = row[i] <= last;
+            pa[i] += more ? step_a : 0;
+            pb[i] += more ? step_b : 0;
+            if constexpr (QS != 0) ps[i] += more ? step_s : 0;
         }
+        // (Loads of two steps mixed before the loop would make every turn of it wait for the
+        // newest; so would a way out of its middle.)
+        __builtin_amdgcn_sched_barrier(0);
     };
     auto shifted = [](v4u v, int elements) __attribute__((always_inline)) -> v4u {
         if (elements <= 0) return v;
@@ -554,19 +579,28 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
         return __builtin_bit_cast(v4u, __builtin_bit_cast(unsigned __int128, v) >> (16 * elements));
     };
     auto store = [&](int kt, int st, int set) __attribute__((always_inline)) {
+        const int left = last + 1 - (kt * KG + kg) * BK;   // rows of the group from this step on
+        v4u a[NC], b[NC];
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            v4u a = ra[set][i], b = rb[set][i];
-            if constexpr (QS == 1) a = widened(a, past_a);
-            if constexpr (QS == 2) b = widened(b, past_b);
-            if (cut) {
-                if constexpr (QS != 1) a = shifted(a, past_a);
-                if constexpr (QS != 2) b = shifted(b, past_b);
-            }
-            if (kt * BK + srow + RPP * i > last) a = b = v4u{0u, 0u, 0u, 0u};
+            a[i] = ra[set][i];
+            b[i] = rb[set][i];
+            if constexpr (QS == 1) a[i] = widened(a[i], past_a);
+            else if constexpr (CUT) a[i] = shifted(a[i], past_a);
+            if constexpr (QS == 2) b[i] = widened(b[i], past_b);
+            else if constexpr (CUT) b[i] = shifted(b[i], past_b);
+        }
+        if (left < BK) {
+            asm volatile("");   // (a branch: selects would take their time in every step)
+#pragma unroll
+            for (int i = 0; i < NC; ++i)
+                if (srow + RPP * i >= left) a[i] = b[i] = v4u{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
             const int at = WT::b_row(srow + RPP * i) + scol * 16;
-            *(LDS_AS v4u*)(smem + 2 * st * OP + at) = a;
-            *(LDS_AS v4u*)(smem + (2 * st + 1) * OP + at) = b;
+            *(LDS_AS v4u*)(smem + 2 * st * OP + at) = a[i];
+            *(LDS_AS v4u*)(smem + (2 * st + 1) * OP + at) = b[i];
         }
     };
     // (M or N below 8) element by element, straight to the LDS
@@ -617,7 +651,7 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
             }
         }
     };
-    if (M < 8 || N < 8) {
+    if (KG == 1 && (M < 8 || N < 8)) {
 #pragma unroll 1
         for (int kt = 0; kt < nk; ++kt) {
             narrow(kt);
@@ -625,23 +659,65 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
             multiply(0);
             __syncthreads();
         }
-    } else if (nk > 0) {
+    } else if (KG > 1 && nk > 0) {
 #pragma unroll
-        for (int u = 0; u < D; ++u) load(u, u);
-        store(0, 0, 0);
-        load(D, 0);
-        __syncthreads();
-        for (int k0 = 0; k0 < nk; k0 += U) {
+        for (int u = 0; u < D; ++u) load(u);
+        int k0 = 0;
+#pragma unroll 1
+        for (; k0 + D <= nk; k0 += D) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {   // step k0 + u, in LDS stage u % 2
-                if (k0 + u >= nk) break;
-                multiply(u & 1);
-                if (k0 + u + 1 >= nk) break;
-                store(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
-                load(k0 + u + 1 + D, (u + 1) % D);
+            for (int u = 0; u < D; ++u) {
+                store(k0 + u, 0, u);
+                load(u);
+                __syncthreads();
+                multiply(0);
                 __syncthreads();
             }
         }
+#pragma unroll
+        for (int u = 0; u < D - 1; ++u) {
+            if (k0 + u >= nk) break;
+            store(k0 + u, 0, u);
+            __syncthreads();
+            multiply(0);
+            __syncthreads();
+        }
+    } else if (nk > 0) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) load(u);
+        store(0, 0, 0);
+        load(0);
+        __syncthreads();
+        int k0 = 0;
+#pragma unroll 1
+        for (; k0 + U < nk; k0 += U) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {   // step k0 + u, in LDS stage u % 2
+                multiply(u & 1);
+                store(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
+                load((u + 1) % D);
+                __syncthreads();
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {   // (loaded already)
+            multiply(u & 1);
+            if (k0 + u + 1 >= nk) break;
+            store(k0 + u + 1, (u + 1) & 1, (u + 1) % D);
+            __syncthreads();
+        }
+    }
+    if constexpr (KG > 1) {
+        LDS_AS v4f* sums = (LDS_AS v4f*)smem_raw;   // [group][block][256]
+#pragma unroll
+        for (int b = 0; b < KG; ++b) sums[(kg * KG + b) * 256 + tid] = acc[b / TB][b % TB];
+        __syncthreads();
+        v4f s = sums[kg * 256 + tid];
+#pragma unroll
+        for (int q = 1; q < KG; ++q) s += sums[(q * KG + kg) * 256 + tid];
+#pragma unroll
+        for (int b = 0; b < KG; ++b)
+            if (b == kg) acc[b / TB][b % TB] = s;
     }
     const int64_t base = (int64_t)grp * M * N;
 #pragma unroll
@@ -650,17 +726,20 @@ __global__ __launch_bounds__(256) void wgrad_tile_kernel(const _Float16* __restr
         for (int j = 0; j < TB; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
+                if (KG > 1 && i * TB + j != kg) continue;
                 const int row = m0 + WS * wm + 16 * i + 4 * g + r, col = n0 + WS * wn + 16 * j + j16;
                 if (row < M && col < N) tile::store_one<OUT>(C, base + (int64_t)row * N + col, acc[i][j][r], 0);
             }
 }
 
-// Rows and columns of a tile: 256 (the ping-pong kernel), 128 or 64.
-// qs: the operand of 8-bit values (0: none).
+// Rows and columns of a tile: 256 (the ping-pong kernel), 128 or 64, and 4 for 64 with
+// the steps split. qs: the operand of 8-bit values (0: none).
+constexpr int kSplit64 = 4;
 int choose_wgrad(const GroupedArgs& a, int qs = 0) {
     // 16-byte pieces of both operands' rows, and 32-bit offsets over 8 steps
     const bool pp_ok = pp::aligned16(a.A) && pp::aligned16(a.B) && a.M % (qs == 1 ? 16 : 8) == 0 &&
                        a.N % (qs == 2 ? 16 : 8) == 0 && a.M < (1 << 21) && a.N < (1 << 21);
+    const bool split_ok = qs && a.M >= 8 && a.N >= 8;
     // Estimated us, fits to measured times of 90 shapes (choosing by them costs
     // 2 % over the fastest of each shape; the ping-pong kernel wherever it is
     // possible 24 %): tiles over compute units, `more` for the uneven end, no
@@ -670,15 +749,25 @@ int choose_wgrad(const GroupedArgs& a, int qs = 0) {
         int size;
         double per_k, least, more, tb, fixed;
     };
-    static constexpr Cost costs[] = {{256, 36.8, 0.56, 0.08, 4.8, 9.8},
-                                     {128, 14.8, 1.48, 0.04, 3.2, 6.2},
-                                     {64, 5.4, 1.50, 0.05, 2.2, 5.6}};
+    static constexpr Cost f16_costs[] = {{256, 36.8, 0.56, 0.08, 4.8, 9.8},
+                                         {128, 14.8, 1.48, 0.04, 3.2, 6.2},
+                                         {64, 5.4, 1.50, 0.05, 2.2, 5.6}};
+    // With 8-bit values (2100 shapes, 1 to 16384 rows, M and N from 64 to 8192, up to
+    // eight groups: 1.7 % over the fastest of each; by the constants above 4.3 %). Splitting
+    // the steps pays for few tiles of many rows: 8155 rows, 464 x 72, 38 us for 56; not
+    // where tiles fill the chip (3305 rows, 1280 x 656: 45 for 34).
+    static constexpr Cost mx_costs[] = {{256, 41.7, 0.545, 0.060, 6.36, 6.98},
+                                        {128, 14.7, 1.08, 0.125, 6.37, 6.98},
+                                        {64, 4.78, 0.964, 0.307, 5.76, 6.90},
+                                        {kSplit64, 8.99, 0.496, 0.013, 1.28, 6.87}};
     int size = 0;
     double least = 0.0;
     const double live = (double)(a.K < a.groups ? (a.K > 0 ? a.K : 1) : a.groups);
-    for (const Cost& c : costs) {
-        if (c.size == 256 && !pp_ok) continue;
-        const double tiles = (double)a.groups * (double)((a.M + c.size - 1) / c.size) * (double)((a.N + c.size - 1) / c.size);
+    for (int i = 0; i < (qs ? 4 : 3); ++i) {
+        const Cost& c = qs ? mx_costs[i] : f16_costs[i];
+        if ((c.size == 256 && !pp_ok) || (c.size == kSplit64 && !split_ok)) continue;
+        const int side = c.size == kSplit64 ? 64 : c.size;
+        const double tiles = (double)a.groups * (double)((a.M + side - 1) / side) * (double)((a.N + side - 1) / side);
         double rounds = tiles / 256.0 + c.more;
         if (rounds < c.least) rounds = c.least;
         const double t = rounds * (double)a.K / live * c.per_k * 1e-3 + c.fixed +
@@ -692,6 +781,7 @@ int choose_wgrad(const GroupedArgs& a, int qs = 0) {
         if (pp_ok && std::strcmp(env, "wgrad_pp") == 0) size = 256;
         if (std::strcmp(env, "wgrad_tile_128") == 0) size = 128;
         if (std::strcmp(env, "wgrad_tile_64") == 0) size = 64;
+        if (split_ok && std::strcmp(env, "wgrad_tile_64_split") == 0) size = kSplit64;
     }
     return size;
 }

@@ -151,7 +151,7 @@ def test_wgrad(m, n, fmt, second):
         run_wgrad(sizes, m, n, fmt, second, out)
 
 
-@pytest.mark.parametrize("config", ["wgrad_pp", "wgrad_tile_128", "wgrad_tile_64"])
+@pytest.mark.parametrize("config", ["wgrad_pp", "wgrad_tile_128", "wgrad_tile_64", "wgrad_tile_64_split"])
 @pytest.mark.parametrize("second", [False, True])
 def test_wgrad_kernels(config, second, monkeypatch):
     monkeypatch.setenv("LIBGEMM_CONFIG", config)
@@ -178,7 +178,7 @@ def test_wgrad_unaligned(second):
         run_wgrad([70, 9], m, n, "e4m3", second, F16, offset=1)
 
 
-@pytest.mark.parametrize("config", ["wgrad_pp", "wgrad_tile_128", "wgrad_tile_64"])
+@pytest.mark.parametrize("config", ["wgrad_pp", "wgrad_tile_128", "wgrad_tile_64", "wgrad_tile_64_split"])
 def test_wgrad_special(config, monkeypatch):
     """A NaN and a scale that is NaN reach their own weights only; values past FP16's range are infinities."""
     monkeypatch.setenv("LIBGEMM_CONFIG", config)
