@@ -70,12 +70,18 @@ __device__ __forceinline__ void add8(float (&v)[8], const float (&r)[8]) {
     for (int i = 0; i < 8; ++i) v[i] = T == OUT_F16 ? (float)(_Float16)(v[i] + r[i]) : v[i] + r[i];
 }
 
-// The row's scale and the factor that takes h w to what is stored.
+// The row's scale and the factor that takes h w to what is stored. lift: h w is so
+// small that the factor would pass FP32's range; it is then for h w 2^100 (the
+// quotient is below 2^125 even with the least scale).
+constexpr float kLift = 0x1p100f;
 template <int OUT>
-__device__ __forceinline__ float row_factor(float rstd, float most, int pow2, float& scale) {
+__device__ __forceinline__ float row_factor(float rstd, float most, int pow2, float& scale, bool& lift) {
+    lift = false;
     if constexpr (!is_fp8<OUT>) return rstd;
     scale = scale_for_format(most * rstd, OUT == OUT_E5M2 ? FMT_E5M2 : FMT_E4M3, pow2);
-    return rstd / scale;
+    const float factor = rstd / scale;
+    lift = factor == __builtin_inff() && rstd < __builtin_inff();
+    return lift ? rstd * (1.0f / kLift) / scale : factor;
 }
 
 template <int OUT>
@@ -197,7 +203,14 @@ __global__ __launch_bounds__(W == 1 ? 256 : 64 * W) void rms_norm_kernel(NormArg
         half ^= 1;
         const float rstd = 1.0f / __builtin_sqrtf(sum * a.inv_width + a.eps);
         float scale = 1.0f;
-        const float factor = row_factor<OUT>(rstd, most, a.pow2, scale);
+        bool lift;
+        const float factor = row_factor<OUT>(rstd, most, a.pow2, scale, lift);
+        if (is_fp8<OUT> && lift) {
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] *= kLift;
+        }
 #pragma unroll
         for (int k = 0; k < CH; ++k) {
             const Place<W, MODE> p(first, k, a.width);
@@ -244,14 +257,15 @@ __global__ __launch_bounds__(512) void rms_norm_long_kernel(NormArgs a) {
         half ^= 1;
         const float rstd = 1.0f / __builtin_sqrtf(sum * a.inv_width + a.eps);
         float scale = 1.0f;
-        const float factor = row_factor<OUT>(rstd, most, a.pow2, scale);
+        bool lift;
+        const float factor = row_factor<OUT>(rstd, most, a.pow2, scale, lift);
         for (int64_t c = 8 * threadIdx.x; c < a.width; c += 8 * 512) {
             const int n = count8(c, a.width);
             float v[8], w[8];
             value(c, n, v);
             load8<OUT_F32>(a.weight, c, n, 1.0f, w);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= w[i];
+            for (int i = 0; i < 8; ++i) v[i] *= lift ? w[i] * kLift : w[i];
             store_y<OUT>(a.y, base + c, n, v, factor);
         }
         if (threadIdx.x == 0) {

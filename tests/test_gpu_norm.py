@@ -284,3 +284,28 @@ def test_infinity_at_a_cut_row_end(width):
         assert torch.equal(dx[i][other], want[other]), i
         assert bool(dx[i, j].isnan())
     assert bool(dx[8].isfinite().all())
+
+
+@pytest.mark.parametrize("width", [64, 1000, 4099, 20000])
+@pytest.mark.parametrize("pow2", [False, True])
+def test_rows_near_the_least_numbers(width, pow2):
+    """FP32 rows, and weights, so small that 1 / scale is beyond FP32: codes as of any other row."""
+    gn = gen(width)
+    x = normal(gn, (6, width))
+    x[0:2] *= 1e-37
+    x[4:] = 0.0
+    w = 1.0 + normal(gn, (width,), 0.2)
+    for out, fmt, top in ((torch.float8_e4m3fn, "e4m3", 448.0), (torch.float8_e5m2, "e5m2", 57344.0)):
+        for weight in (w, w * (1e-35 if fmt == "e4m3" else 1e-33)):
+            say(f"norm of least numbers, width {width} {fmt} pow2 {pow2}")
+            y, scale = torch.empty((6, width), dtype=out, device=DEV), torch.empty(6, device=DEV)
+            rows = slice(0, 4) if weight is w else slice(2, 4)
+            if weight is w and fmt == "e5m2":
+                rows = slice(2, 4)   # (the small rows' scale is no normal number)
+            g.rms_norm(x, weight, y, eps=EPS, scale=scale, pow2=pow2)
+            v, _ = norm(x.double(), weight.double(), EPS)
+            s = scale.double()[:, None]
+            if not pow2:
+                check(s[rows, 0], v[rows].abs().amax(dim=1) / top, v[rows].abs().amax(dim=1) / top * REL, "scale")
+            check((y.double() * s)[rows], v[rows], (code_step(v, s, fmt) * (1 + 2 * REL) + v.abs() * 2 * REL)[rows], "codes")
+            assert bool((y[4:].float() == 0).all()) and bool((scale[4:] == 1.0).all())
