@@ -6,16 +6,16 @@
 //              0.5 z (1 + tanh(u / 2)) with one exponential
 //   SILU       z s(z)
 // NaN gives NaN (RELU's derivative: 0); +inf gives +inf, and -inf NaN where the
-// formula is -inf * 0.
+// formula is -inf * 0. Derivatives at infinities are their limits, 1 and 0.
 //
 // P(-a), a >= 0, is 2 to the power of a polynomial in a (activate), fitted here for
 // the least error over [0, 7]: 7e-7 of P, and with FP32's rounding of the exponent,
 // which grows to 40, 4.5e-6; beyond 7, where P is below 1.3e-12, it falls to 0. The
-// derivative needs exp(-a^2 / 2) as well, so there P(-a) is exp(-a^2 / 2) times a function that falls from 1/2 like 1 /
-// (a sqrt(2 pi)): a polynomial without constant in t = 1 / (1 + 0.35 a), fitted here
-// for the least relative error over a in [0, 7]: 2.5e-7 there, 4.5e-5 beyond, where
-// P is below 1.3e-12. So small tails keep their relative precision; the exponent's
-// rounding adds a^2 2^-24.
+// derivative needs exp(-a^2 / 2) as well, so there P(-a) is exp(-a^2 / 2) times a
+// function that falls from 1/2 like 1 / (a sqrt(2 pi)): a polynomial without constant
+// in t = 1 / (1 + 0.35 a), fitted here for the least relative error over a in [0, 7]:
+// 2.5e-7 there, 4.5e-5 beyond, where P is below 1.3e-12. So small tails keep their
+// relative precision; the exponent's rounding adds a^2 2^-24.
 #pragma once
 
 #include "device_common.h"
@@ -77,9 +77,15 @@ __device__ __forceinline__ float activate(float z) {
 }
 
 // The derivative. (1 - s is exp(-u) s: the difference would lose its bits.
-// Exponents stop at 2^115, where s is 0 against every other term.)
+// Exponents stop at 2^115, where s is 0 against every other term, z standing for no
+// more than 1000 in magnitude: beyond, the derivative is 0 or 1 and z^3 may not be a
+// number. Selects, which keep NaN.)
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
+    if constexpr (ACT == ACT_GELU || ACT == ACT_GELU_TANH || ACT == ACT_SILU) {
+        z = z > 1000.0f ? 1000.0f : z;
+        z = z < -1000.0f ? -1000.0f : z;
+    }
     if constexpr (ACT == ACT_RELU) {
         return z > 0.0f ? 1.0f : 0.0f;
     } else if constexpr (ACT == ACT_GELU) {

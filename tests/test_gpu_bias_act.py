@@ -372,3 +372,24 @@ def test_gradient_against_differences(name):
     # e^2 / 6 times the third derivative (at most 2), the difference's rounding |z| 2^-52 / e, and the kernel's own
     tol = dy.double().abs() * (slope_error(z.double(), name) + 1e-9 + z.double().abs() * 2.0 ** -51 / e) + d.abs() * 2.0 ** -22
     check(dz, d, tol, name)
+
+
+@pytest.mark.parametrize("name", ["relu", "gelu", "gelu_tanh", "silu"])
+def test_slope_range(name):
+    """Derivatives from -40 to 40, at the largest numbers and at infinities (1 and 0); NaN gives NaN (relu: 0)."""
+    large = torch.tensor([1e3, 1e4, 65504.0, 1e8, 1e10, 1e13, 1e19, 1e30, 3e38, float("inf")])
+    z = torch.cat([torch.linspace(-40, 40, 8000), large, -large, torch.tensor([float("nan"), 0.0])]).to(DEV)
+    for zt in (F32, F16):
+        for cols in (z.numel(), 7):
+            say(f"slope {name} {zt} {cols}")
+            zz = (z if cols != 7 else z[-7 * 3:].reshape(3, 7)).reshape(-1, cols).to(zt)
+            dy = torch.ones(zz.shape, device=DEV)
+            dz, _ = g.bias_act_backward(dy, zz, ACT[name])
+            nan = zz.isnan()
+            assert torch.equal(dz[nan], torch.zeros_like(dz[nan])) if name == "relu" else bool(dz[nan].isnan().all())
+            zd = torch.where(nan, torch.zeros_like(zz), zz).double()
+            far = zd.abs() > 500
+            ref = torch.where(far, (zd > 0).double(), slope(zd.clamp(-500, 500), name))
+            err = torch.where(far, torch.zeros_like(zd), slope_error(zd.clamp(-500, 500), name)) + 2.0 ** -23
+            ok = ~nan
+            check(dz[ok], ref[ok], err[ok], "slope")

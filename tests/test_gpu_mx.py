@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import precision_dense_gemm_03_amd as g
-from dense_ref import CODE, FP8_MAX, as_bytes, codes_of, mx_pack, scale_bytes, spread, stored, values
+from dense_ref import CODE, FP8_MAX, as_bytes, codes_of, mx_pack, powers, scale_bytes, spread, stored, values
 from routed_ref import REL, check, cut
 from test_gpu_norm import _gpu, gen, guarded, input_of, normal, say  # noqa: F401
 
@@ -220,3 +220,16 @@ def test_pack_keeps_what_fits():
     y = torch.empty((50, 320), dtype=F16, device=DEV)
     g.dequantize_mx_fp8(q, s, g.FMT_E4M3, y)
     assert torch.equal(y.float(), x) and float(spread(s.float(), 320).max()) < 255 and FP8_MAX["e4m3"] == 448.0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
+def test_pack_least_and_largest_numbers(fmt):
+    """FP32 blocks from the least subnormal numbers to the largest: codes and scales as for any others."""
+    gn = gen(12)
+    x = normal(gn, (256, 96)) * torch.ldexp(torch.ones(256, 1, device=DEV), torch.arange(-150, 106, device=DEV)[:, None])
+    x[0, 0], x[255, 40] = 2.0 ** -149, 3.4e38
+    say(f"pack from the least to the largest numbers {fmt}")
+    q, s = g.quantize_mx_fp8(x, FMT[fmt])
+    u, sc = mx_pack(x, fmt)
+    assert torch.equal(powers(s), sc), "scales"
+    assert torch.equal(q, as_bytes(codes_of(u, fmt))), "codes"
