@@ -8,6 +8,9 @@
 // flight; the column sums stay in registers (FP32, of dz before it is rounded), the
 // waves' sums meet in LDS, and each workgroup leaves one row of partial sums that a
 // second launch adds in a fixed order.
+//
+// 8192 x 12288 FP16 from E4M3 z, GELU: 102 to 106 us with the column sums, 5.0 TB/s
+// (FP16 z 120, 5.0 TB/s); without an activation 79. 1001 x 1416: 6 + 3.4 us, latency.
 #include "act.h"
 #include "kernels.h"
 #include "norm.h"

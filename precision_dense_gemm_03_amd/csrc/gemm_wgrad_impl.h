@@ -739,7 +739,8 @@ int choose_wgrad(const GroupedArgs& a, int qs = 0) {
     // 16-byte pieces of both operands' rows, and 32-bit offsets over 8 steps
     const bool pp_ok = pp::aligned16(a.A) && pp::aligned16(a.B) && a.M % (qs == 1 ? 16 : 8) == 0 &&
                        a.N % (qs == 2 ? 16 : 8) == 0 && a.M < (1 << 21) && a.N < (1 << 21);
-    const bool split_ok = qs && a.M >= 8 && a.N >= 8;
+    // (launches of 1024 threads in a workgroup: far below 2^32 of them)
+    const bool split_ok = qs && a.M >= 8 && a.N >= 8 && wgrad_blocks(a.groups, (a.M + 63) / 64, (a.N + 63) / 64) < (1 << 20);
     // Estimated us, fits to measured times of 90 shapes (choosing by them costs
     // 2 % over the fastest of each shape; the ping-pong kernel wherever it is
     // possible 24 %): tiles over compute units, `more` for the uneven end, no

@@ -1,5 +1,7 @@
 // 8-bit values with a power-of-two scale per 32 (row_io.h): from FP32 or FP16, and
-// back. One pass, bound by bytes: a lane takes 8 values, four lanes a block.
+// back. One pass, bound by bytes: a lane takes 8 values, four lanes a block. 8192 x
+// 4096 FP16: 18.5 us, 5.5 TB/s (16.4 with the input in the Infinity Cache, back 16.8);
+// 4099 columns 21.
 #include "kernels.h"
 #include "norm.h"
 #include "row_io.h"

@@ -196,3 +196,17 @@ def test_queries():
               lambda: g.select_config_mx_wgrad(2, 1, 1, 1), lambda: g.select_config_mx_wgrad(0, 1, 1, 1, 5000)):
         with pytest.raises(g.GemmError):
             f()
+
+
+def test_split_stays_small(monkeypatch):
+    """Sixteen waves per workgroup only where a launch of them stays far below 2^32 threads, and not for fewer than
+    eight columns of either operand."""
+    q = g.select_config_mx_wgrad
+    monkeypatch.setenv("LIBGEMM_CONFIG", "wgrad_tile_64_split")
+    assert q(g.OUT_F32, 5000, 400, 72) == "wgrad_tile_64_split"
+    assert q(g.OUT_F32, 4, 1 << 17, 1 << 16) != "wgrad_tile_64_split"
+    assert q(g.OUT_F32, 4, 1 << 12, 1 << 12, 4096) != "wgrad_tile_64_split"
+    assert q(g.OUT_F32, 5000, 7, 72) != "wgrad_tile_64_split" and q(g.OUT_F32, 5000, 72, 7) != "wgrad_tile_64_split"
+    monkeypatch.delenv("LIBGEMM_CONFIG")
+    assert q(g.OUT_F32, 8155, 464, 72) == "wgrad_tile_64_split"
+    assert q(g.OUT_F32, 8192, 4096, 4096) == "wgrad_pp"
