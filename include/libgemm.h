@@ -597,7 +597,8 @@ int gemm_f16_bias_act_bt(const void* A, const void* Bt, const float* bias, const
  *   A, fmt_a, B, fmt_b  as gemm_fp8_fmt
  *   sA, sB   device, one float each (channel = 0), or float[M] and float[N]
  *   sOut     device, one float: required iff out_dtype is an FP8 output, which is
- *            FP8((act(z) + residual) / sOut)
+ *            FP8((act(z) + residual) / sOut), the quotient formed as a product with
+ *            1 / sOut (an FP32 ulp or two from it), for every positive sOut
  *   C        F32, F16, E4M3 or E5M2
  */
 int gemm_fp8_bias_act(const uint8_t* A, int fmt_a, const uint8_t* B, int fmt_b, const float* sA, const float* sB,

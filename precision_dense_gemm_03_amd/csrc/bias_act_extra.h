@@ -50,7 +50,19 @@ struct BiasActExtra {
 
     // The factor of every element (per channel: beside sA[i] sB[j]).
     __device__ __forceinline__ float common() const { return channel ? 1.0f : (sA ? *sA : 1.0f) * (sB ? *sB : 1.0f); }
-    __device__ __forceinline__ float out_factor() const { return out_dtype >= OUT_E4M3 ? 1.0f / *sOut : 1.0f; }
+    // What y is multiplied by: y / sOut for FP8 outputs, in one factor (as the plain
+    // products'), or in two where sOut is so small (2^-128) that its reciprocal is no FP32
+    // number and a zero's product with it none. (rest is below 2^50 with the least sOut.)
+    struct OutFactor {
+        float lift, rest;
+        __device__ __forceinline__ float operator()(float y) const { return y * lift * rest; }
+    };
+    __device__ __forceinline__ OutFactor out_factor() const {
+        if (out_dtype < OUT_E4M3) return {1.0f, 1.0f};
+        const float f = 1.0f / *sOut;
+        if (__builtin_fabsf(f) < __builtin_inff()) return {1.0f, f};
+        return {0x1p100f, 0x1p-100f / *sOut};
+    }
 
     // Four neighbouring values of a row of FP32s, zero from N on.
     static __device__ __forceinline__ v4f row4(const float* p, int col, int N) {
@@ -120,7 +132,7 @@ struct BiasActExtra {
         if (residual)
             y += res_dtype == OUT_F32 ? reinterpret_cast<const float*>(residual)[at]
                                       : (float)reinterpret_cast<const _Float16*>(residual)[at];
-        store_out(C, at, y * out_factor(), out_dtype);
+        store_out(C, at, out_factor()(y), out_dtype);
     }
 
     // The deep-ring kernel: four neighbouring columns per lane and block, block tn at
@@ -190,9 +202,10 @@ struct BiasActExtra {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[tn][e] = activate<decltype(a)::value>(acc[tn][e]);
         });
-        const float f = out_factor();
+        const OutFactor f = out_factor();
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn) put4(C, out_dtype, row, col0 + 16 * tn, N, (acc[tn] + piece[tn].residual) * f);
+        for (int tn = 0; tn < TN; ++tn)
+            put4(C, out_dtype, row, col0 + 16 * tn, N, (acc[tn] + piece[tn].residual) * f.lift * f.rest);
     }
 
     // The register-staged kernel: acc[tm][tn][r] is row row0 + 16 tm + r, column
@@ -200,7 +213,8 @@ struct BiasActExtra {
     template <int TM, int TN>
     __device__ __forceinline__ void finish_tile16(v4f (&acc)[TM][TN], int row0, int col0, int M, int N) const {
         static_assert(TN % 2 == 0, "blocks of 32 columns");
-        const float s = common(), f = out_factor();
+        const float s = common();
+        const OutFactor f = out_factor();
 #pragma unroll
         for (int tn = 0; tn < TN; ++tn) {
             const int col = min(col0 + 16 * tn, N - 1);
@@ -272,7 +286,7 @@ struct BiasActExtra {
                     if (residual)
                         y += res_dtype == OUT_F32 ? reinterpret_cast<const float*>(residual)[at]
                                                   : (float)reinterpret_cast<const _Float16*>(residual)[at];
-                    store_out(C, at, y * f, out_dtype);
+                    store_out(C, at, f(y), out_dtype);
                 }
     }
 
@@ -296,7 +310,8 @@ struct BiasActExtra {
         if (col0 >= cols) return;
         LDS_AS uint8_t* ep = G == 0 ? (wj == 0 ? lds.b[0] : wj == 1 ? lds.b[1] : wj == 2 ? lds.b[2] : lds.b[3])
                                     : (wj < 2 ? lds.a[0] : lds.a[1]) + (wj & 1) * STAGE;
-        const float s = common(), f = out_factor();
+        const float s = common();
+        const OutFactor f = out_factor();
         const bool res16 = residual && res_dtype == OUT_F16;
 #pragma unroll 1
         for (int i = 0; i < MI; ++i) {
@@ -357,7 +372,7 @@ struct BiasActExtra {
                     for (int q = 0; q < 4; ++q) {
                         float y[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[e] = v[j][4 * q + e] * f;
+                        for (int e = 0; e < 4; ++e) y[e] = f(v[j][4 * q + e]);
                         stage8(ep + 2 * kPart, lr, 32 * j + 8 * q + 4 * h,
                                out_dtype == OUT_E5M2 ? e5m2_pack4(y[0], y[1], y[2], y[3])
                                                      : e4m3_pack4(y[0], y[1], y[2], y[3]));
