@@ -8,14 +8,24 @@
 // NaN gives NaN (RELU's derivative: 0); +inf gives +inf, and -inf NaN where the
 // formula is -inf * 0. Derivatives at infinities are their limits, 1 and 0.
 //
-// P(-a), a >= 0, is 2 to the power of a polynomial in a (activate), fitted here for
-// the least error over [0, 7]: 7e-7 of P, and with FP32's rounding of the exponent,
-// which grows to 40, 4.5e-6; beyond 7, where P is below 1.3e-12, it falls to 0. The
-// derivative needs exp(-a^2 / 2) as well, so there P(-a) is exp(-a^2 / 2) times a
-// function that falls from 1/2 like 1 / (a sqrt(2 pi)): a polynomial without constant
-// in t = 1 / (1 + 0.35 a), fitted here for the least relative error over a in [0, 7]:
-// 2.5e-7 there, 4.5e-5 beyond, where P is below 1.3e-12. So small tails keep their
-// relative precision; the exponent's rounding adds a^2 2^-24.
+// Two forms of each function (FINE). An FP32 result keeps FP32's precision over the
+// whole range, small tails among it: arguments of exponentials are held in two FP32
+// numbers, and GELU's P(-a), a >= 0, is exp(-a^2 / 2) times a function that falls from
+// 1/2 like 1 / (a sqrt(2 pi)), fitted here as a polynomial without constant in t = 1 /
+// (1 + 0.35 a): 6.7e-8 over [0, 13.5] with its coefficients in FP32. In all GELU is
+// within 4.2e-7 of its value, SILU and GELU_TANH within 2.2e-7.
+//
+// Results that are rounded to FP16 or FP8 (half a step of 4.9e-4 and more) take shorter
+// forms (4096^3 FP16 into FP32, us: GELU 127 with them and 131 with the fine ones,
+// GELU_TANH 124 and 132, SILU 124 and 126): arguments of exponentials are rounded to
+// FP32, which costs a value their size times 2^-24, and P(-a) is 2 to the power of a
+// polynomial in a, fitted here over [0, 7]: with its coefficients in FP32 off by 1.4e-6
+// of P, evaluated in FP32 by 5.2e-6 (1.4e-6 below 3); beyond 7, where P is below
+// 1.3e-12, it falls to 0.
+//
+// The derivative needs exp(-a^2 / 2) as well; there P(-a) is of the fine form with a
+// shorter polynomial: 2.7e-7 over [0, 7], 4.5e-5 beyond. Small tails keep their
+// relative precision; the exponent's roundings add up to 1.5 a^2 2^-24.
 #pragma once
 
 #include "device_common.h"
@@ -27,6 +37,12 @@ enum Activation { ACT_NONE = 0, ACT_RELU = 1, ACT_GELU = 2, ACT_GELU_TANH = 3, A
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTanhScale = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
+
+// A constant as the sum of two FP32 numbers.
+struct TwoFloats {
+    float hi, lo;
+};
+constexpr TwoFloats two_floats(double c) { return {(float)c, (float)(c - (double)(float)c)}; }
 
 // exp(-a^2 / 2) and P(-a) for a = |z|.
 __device__ __forceinline__ float normal_tail(float a, float& e) {
@@ -57,16 +73,70 @@ __device__ __forceinline__ float normal_below(float a) {
     return __builtin_amdgcn_exp2f(p);
 }
 
+// 2^(x + low) for a low that is small beside 1. (An infinity stays one.)
+__device__ __forceinline__ float exp2_fine(float x, float low) {
+    return __builtin_amdgcn_exp2f(x) * __builtin_fmaf(low, 0.6931471805599453f, 1.0f);
+}
+
+// P(-a) with FP32's precision. (Where a passes 100 it is 0.)
+__device__ __forceinline__ float normal_below_fine(float a) {
+    a = fminf(a, 100.0f);
+    constexpr TwoFloats c = two_floats(-0.5 * 1.4426950408889634);
+    const float s = a * a, x = s * c.hi;
+    float low = __builtin_fmaf(s, c.hi, -x);
+    low = __builtin_fmaf(s, c.lo, low);
+    low = __builtin_fmaf(__builtin_fmaf(a, a, -s), c.hi, low);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(a, 0.35f, 1.0f));
+    float p = -0.029125856f;
+    p = __builtin_fmaf(p, t, 0.1438722f);
+    p = __builtin_fmaf(p, t, -0.2555045f);
+    p = __builtin_fmaf(p, t, 0.15892924f);
+    p = __builtin_fmaf(p, t, -0.022937113f);
+    p = __builtin_fmaf(p, t, 0.10543293f);
+    p = __builtin_fmaf(p, t, 0.11985244f);
+    p = __builtin_fmaf(p, t, 0.13985908f);
+    p = __builtin_fmaf(p, t, 0.13962157f);
+    return p * t * exp2_fine(x, low);
+}
+
+// -log2(e) times SILU's argument and the tanh form's, as x + low. v is of at most 100
+// in magnitude, so that nothing passes FP32's range.
+__device__ __forceinline__ void silu_exponent(float v, float& x, float& low) {
+    constexpr TwoFloats c = two_floats(-1.4426950408889634);
+    x = v * c.hi;
+    low = __builtin_fmaf(v, c.lo, __builtin_fmaf(v, c.hi, -x));
+}
+
+__device__ __forceinline__ void tanh_exponent(float v, float& x, float& low) {
+#pragma clang fp contract(off)   // (p is the rounded product wherever it stands)
+    constexpr double scale = -1.4426950408889634 * 1.5957691216057308;
+    constexpr TwoFloats c1 = two_floats(scale), c3 = two_floats(scale * 0.044715);
+    const float w = v * v, p = w * c3.hi;
+    float pl = __builtin_fmaf(w, c3.hi, -p);
+    pl = __builtin_fmaf(w, c3.lo, pl);
+    pl = __builtin_fmaf(__builtin_fmaf(v, v, -w), c3.hi, pl);
+    const float k = c1.hi + p, b = k - c1.hi;   // k and what its rounding left
+    const float kl = (c1.hi - (k - b)) + (p - b) + (pl + c1.lo);
+    x = v * k;
+    low = __builtin_fmaf(v, kl, __builtin_fmaf(v, k, -x));
+}
+
 // 1 / (1 + 2^u)
 __device__ __forceinline__ float logistic2(float u) { return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u)); }
 
-template <int ACT>
+template <int ACT, bool FINE>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (ACT == ACT_RELU) {
         return z < 0.0f ? 0.0f : z;
     } else if constexpr (ACT == ACT_GELU) {
-        const float q = normal_below(__builtin_fabsf(z));
+        const float a = __builtin_fabsf(z), q = FINE ? normal_below_fine(a) : normal_below(a);
         return z * (z < 0.0f ? q : 1.0f - q);
+    } else if constexpr (FINE && (ACT == ACT_GELU_TANH || ACT == ACT_SILU)) {
+        const float v = fminf(fmaxf(z, -100.0f), 100.0f);   // (NaN: z itself keeps it)
+        float x, low;
+        if constexpr (ACT == ACT_SILU) silu_exponent(v, x, low);
+        else tanh_exponent(v, x, low);
+        return z * __builtin_amdgcn_rcpf(1.0f + exp2_fine(x, low));
     } else if constexpr (ACT == ACT_GELU_TANH) {
         return z * logistic2(z * __builtin_fmaf(z * z, -kLog2e * kTanhScale * kTanhCubic, -kLog2e * kTanhScale));
     } else if constexpr (ACT == ACT_SILU) {

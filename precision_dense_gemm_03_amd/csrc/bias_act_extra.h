@@ -16,16 +16,32 @@
 
 namespace libgemm {
 
-// f(IntC<ACT>) for the activation of a call.
-template <class F>
-__device__ __forceinline__ void with_activation(int act, F f) {
-    switch (act) {
-        case ACT_RELU: f(IntC<ACT_RELU>{}); break;
-        case ACT_GELU: f(IntC<ACT_GELU>{}); break;
-        case ACT_GELU_TANH: f(IntC<ACT_GELU_TANH>{}); break;
-        case ACT_SILU: f(IntC<ACT_SILU>{}); break;
-        default: break;
-    }
+// Which form of the activations (act.h) a kernel has: the one for FP16 and FP8
+// results, the fine one for FP32 results, or both, chosen at run time. (Both in the
+// ping-pong kernel cost its FP16 and FP8 results 1.4 to 2.7 %; in the others nothing,
+// but 0.06 us of 11.3 for 4 rows of FP8.)
+enum Fineness { COARSE = 0, FINE = 1, EITHER = 2 };
+
+// apply(f), f(z) = activate(z) for the activation of a call.
+template <int ACT, bool FINE>
+struct Activate {
+    __device__ __forceinline__ float operator()(float z) const { return activate<ACT, FINE>(z); }
+};
+
+template <int HOW, class F>
+__device__ __forceinline__ void with_activation(int act, int out_dtype, F apply) {
+    auto go = [&](auto fine) __attribute__((always_inline)) {
+        constexpr bool fine_form = decltype(fine)::value;
+        switch (act) {
+            case ACT_GELU: apply(Activate<ACT_GELU, fine_form>{}); break;
+            case ACT_GELU_TANH: apply(Activate<ACT_GELU_TANH, fine_form>{}); break;
+            case ACT_SILU: apply(Activate<ACT_SILU, fine_form>{}); break;
+            default: break;
+        }
+    };
+    if (act == ACT_RELU) apply(Activate<ACT_RELU, false>{});
+    else if (HOW == FINE || (HOW == EITHER && out_dtype == OUT_F32)) go(BoolC<true>{});
+    else go(BoolC<false>{});
 }
 
 typedef unsigned int u32_b1 __attribute__((aligned(1)));
@@ -34,7 +50,7 @@ typedef unsigned int u32_b1 __attribute__((aligned(1)));
 // past the caches, in whole 128-byte lines (16384 x 12288 x 4096 FP8 with bias and
 // GELU_TANH 751 -> 707 us, with a residual too 808 -> 770: the caches' room is the
 // operands').
-template <bool LINES = false>
+template <bool LINES = false, int HOW = EITHER>
 struct BiasActExtra {
     static constexpr bool kActive = false, kStores = false, kFinish = true;
     const float* sA;
@@ -128,7 +144,7 @@ struct BiasActExtra {
         const int64_t at = (int64_t)row * N + col;
         if (Z) store_out(Z, at, z, z_dtype);
         float y = z;
-        with_activation(act, [&](auto a) __attribute__((always_inline)) { y = activate<decltype(a)::value>(z); });
+        with_activation<HOW>(act, out_dtype, [&](auto f) __attribute__((always_inline)) { y = f(z); });
         if (residual)
             y += res_dtype == OUT_F32 ? reinterpret_cast<const float*>(residual)[at]
                                       : (float)reinterpret_cast<const _Float16*>(residual)[at];
@@ -196,11 +212,11 @@ struct BiasActExtra {
                 }
             }
         }
-        with_activation(act, [&](auto a) __attribute__((always_inline)) {
+        with_activation<HOW>(act, out_dtype, [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
             for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[tn][e] = activate<decltype(a)::value>(acc[tn][e]);
+                for (int e = 0; e < 4; ++e) acc[tn][e] = f(acc[tn][e]);
         });
         const OutFactor f = out_factor();
 #pragma unroll
@@ -265,13 +281,13 @@ struct BiasActExtra {
                         if ((threadIdx.x & 15) == 0 && col0 + 16 * t < N) put_exponent(row, col0 + 16 * t, N, e);
                     }
         }
-        with_activation(act, [&](auto a) __attribute__((always_inline)) {
+        with_activation<HOW>(act, out_dtype, [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
             for (int tm = 0; tm < TM; ++tm)
 #pragma unroll
                 for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) acc[tm][tn][r] = activate<decltype(a)::value>(acc[tm][tn][r]);
+                    for (int r = 0; r < 4; ++r) acc[tm][tn][r] = f(acc[tm][tn][r]);
         });
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
@@ -350,11 +366,11 @@ struct BiasActExtra {
                 if (z_dtype >= OUT_E4M3) put_mx(v, ep, lane, row0, col0, M, N);
                 else put_any(Z, z_dtype, v, ep, lane, row0, col0, M, N);
             }
-            with_activation(act, [&](auto a) __attribute__((always_inline)) {
+            with_activation<HOW>(act, out_dtype, [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) v[j][x] = activate<decltype(a)::value>(v[j][x]);
+                    for (int x = 0; x < 16; ++x) v[j][x] = f(v[j][x]);
             });
             if (res16) {
                 add16(v, held, ep + kPart, lane);
@@ -587,10 +603,10 @@ private:
     }
 };
 
-template <bool LINES = false>
-BiasActExtra<LINES> bias_act_extra(const BiasActArgs& a) {
-    return BiasActExtra<LINES>{a.sA, a.sB, a.sOut, a.bias, a.residual, a.C, a.Z, a.zscale, a.act, a.res_dtype, a.out_dtype,
-                        a.z_dtype, a.channel};
+template <bool LINES = false, int HOW = EITHER>
+BiasActExtra<LINES, HOW> bias_act_extra(const BiasActArgs& a) {
+    return BiasActExtra<LINES, HOW>{a.sA, a.sB, a.sOut, a.bias, a.residual, a.C, a.Z, a.zscale, a.act, a.res_dtype,
+                                    a.out_dtype, a.z_dtype, a.channel};
 }
 
 }  // namespace libgemm

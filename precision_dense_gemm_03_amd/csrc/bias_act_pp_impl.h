@@ -12,17 +12,17 @@
 namespace libgemm {
 namespace bias_act {
 
-template <int ES, int FA, int FB, bool BT, int BM, bool LINES>
+template <int ES, int FA, int FB, bool BT, int BM, bool LINES, int HOW>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void bias_act_pp_kernel(
     const uint8_t* __restrict__ A, const uint8_t* __restrict__ B, int M, int N, int K, int tiles_m, int tiles_n,
-    BiasActExtra<LINES> ext) {
+    BiasActExtra<LINES, HOW> ext) {
     using T = pp::Pp<ES, BM>;
     LIBGEMM_PP_LDS(T);
     if (past_last_block((int64_t)tiles_m * tiles_n)) return;
     int tm, tn;
     tile_coords((int)wide_block(), tiles_m, tiles_n, tm, tn);
-    pp::pp_body<ES, OUT_F32, FA, FB, BT, false, BM, true, BiasActExtra<LINES>>(A, B, nullptr, M, N, K, nullptr, nullptr, nullptr,
-                                                                        tm * BM, tn * 256, 0, 0, lds, ext);
+    pp::pp_body<ES, OUT_F32, FA, FB, BT, false, BM, true, BiasActExtra<LINES, HOW>>(
+        A, B, nullptr, M, N, K, nullptr, nullptr, nullptr, tm * BM, tn * 256, 0, 0, lds, ext);
 }
 
 // Rows of whole 128-byte lines in every FP16 and FP32 matrix of the epilogue.
@@ -37,11 +37,15 @@ hipError_t launch_pp(const BiasActArgs& a) {
     if (tiles_m * tiles_n > kMostWorkgroups) return hipErrorInvalidValue;
     const uint8_t* A = reinterpret_cast<const uint8_t*>(a.A);
     const uint8_t* B = reinterpret_cast<const uint8_t*>(a.B);
-#define LIBGEMM_GO(LINES)                                                                              \
-    bias_act_pp_kernel<ES, FA, FB, BT, BM, LINES><<<wide_grid(tiles_m * tiles_n), 512, 0, a.stream>>>( \
-        A, B, (int)a.M, (int)a.N, (int)a.K, (int)tiles_m, (int)tiles_n, bias_act_extra<LINES>(a))
-    if (whole_lines(a)) LIBGEMM_GO(true);
-    else LIBGEMM_GO(false);
+#define LIBGEMM_GO(LINES, HOW)                                                                              \
+    bias_act_pp_kernel<ES, FA, FB, BT, BM, LINES, HOW><<<wide_grid(tiles_m * tiles_n), 512, 0, a.stream>>>( \
+        A, B, (int)a.M, (int)a.N, (int)a.K, (int)tiles_m, (int)tiles_n, bias_act_extra<LINES, HOW>(a))
+    const bool fine = a.out_dtype == OUT_F32 && a.act >= ACT_GELU;   // (none and RELU have one form)
+    const bool lines = whole_lines(a);
+    if (fine && lines) LIBGEMM_GO(true, FINE);
+    else if (fine) LIBGEMM_GO(false, FINE);
+    else if (lines) LIBGEMM_GO(true, COARSE);
+    else LIBGEMM_GO(false, COARSE);
 #undef LIBGEMM_GO
     return hipGetLastError();
 }
