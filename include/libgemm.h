@@ -557,7 +557,8 @@ int rms_norm(const void* x, const void* residual, int dtype, const float* weight
  *   rstd        device, float[rows], as rms_norm wrote it
  *   dweight     device, float[width], written, or NULL
  *   workspace   device, 16-byte aligned, rms_norm_backward_workspace_size(rows,
- *               width) bytes; calls that share it must not overlap
+ *               width) bytes; without dweight none (NULL) for a width of up to 16384
+ *               and 4 * rows bytes beyond. Calls that share it must not overlap
  * Sums over rows are in a fixed order. rows = 0 writes zeros to dweight.
  */
 int rms_norm_backward(const void* dy, const void* dh, int dtype, const void* h, const uint8_t* hscale, int h_dtype,

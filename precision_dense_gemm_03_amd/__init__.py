@@ -1266,7 +1266,7 @@ def rms_norm_backward(dy, h, weight, rstd, dx=None, dweight=None, dh=None, hscal
                       stream=None):
     """(dx, dweight) of rms_norm. dy, dh (the gradient of h itself, added to dx) and dx are of one type, float32 or
     float16; h as rms_norm wrote it, or 8-bit values of it with hscale; rstd[rows] as rms_norm wrote it. dweight is
-    computed when given (None otherwise)."""
+    computed when given (None otherwise; the workspace is then needed for rows of more than 16384 values only)."""
     torch = _torch()
     dt = _float_dtype(dy, "dy")
     _need(dy, dy.dtype, 2, "dy")
@@ -1276,7 +1276,8 @@ def rms_norm_backward(dy, h, weight, rstd, dx=None, dweight=None, dh=None, hscal
         dx = _new(shape, dy.dtype, dy.device, stream)
     ph, ps, ht = _held(h, hscale, h_fmt, shape, "h")
     if workspace is None:
-        n = rms_norm_backward_workspace_size(rows, width)
+        # (without dweight the long rows' own words alone)
+        n = rms_norm_backward_workspace_size(rows, width) if dweight is not None else (4 * rows if width > 16384 else 0)
         workspace = _new(n, torch.uint8, dy.device, stream) if n else None
     _check(lib().rms_norm_backward(_ptr(dy), _opt(dh, dy.dtype, shape, "dh"), dt, ph, ps, ht,
                                    _arg(weight, f32, (width,), "weight"), _arg(rstd, f32, (rows,), "rstd"),

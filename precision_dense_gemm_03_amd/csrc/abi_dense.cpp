@@ -82,7 +82,7 @@ int rms_norm(const void* x, const void* residual, int dtype, const float* weight
 
 int64_t rms_norm_backward_workspace_size(int64_t rows, int64_t width) {
     if (!dim_ok(rows) || !dim_ok(width) || !bytes_ok(rows, width, 4)) return GEMM_ERR_DIM;
-    return 4 * norm_backward_words(rows, width);
+    return 4 * norm_backward_words(rows, width, true);
 }
 
 int rms_norm_backward(const void* dy, const void* dh, int dtype, const void* h, const uint8_t* hscale, int h_dtype,
@@ -94,11 +94,11 @@ int rms_norm_backward(const void* dy, const void* dh, int dtype, const void* h, 
     if (rows > 0 && (!dy || !h || !weight || !rstd || !dx)) return GEMM_ERR_NULL;
     const bool mx = fp8_out(h_dtype);
     if (rows > 0 && mx && !hscale) return GEMM_ERR_SCALE;
-    const int64_t need = rms_norm_backward_workspace_size(rows, width);
+    const int64_t need = 4 * norm_backward_words(rows, width, dweight != nullptr);
     if (need > 0 && !workspace) return GEMM_ERR_NULL;
     if (need > 0 && (workspace_bytes < need || ((uintptr_t)workspace & 15u) != 0)) return GEMM_ERR_WORKSPACE;
     const int64_t n = rows * width, bytes = n * out_size(dtype);
-    const Range w[3] = {{dx, bytes}, {dweight, 4 * width}, {workspace, need}};
+    const Range w[3] = {{dx, bytes}, {dweight, 4 * width}, {need > 0 ? workspace : nullptr, need}};
     const Range r[6] = {{dy, bytes}, {dh, bytes}, {h, n * out_size(h_dtype)},
                         {mx ? hscale : nullptr, scales_of(rows, width)}, {weight, 4 * width}, {rstd, 4 * rows}};
     if (aliased(w, r)) return GEMM_ERR_ALIAS;

@@ -40,9 +40,10 @@ struct NormBackwardArgs {
 
 hipError_t launch_rms_norm(const NormArgs& a, int dtype, int out_dtype, hipStream_t s);
 hipError_t launch_rms_norm_backward(const NormBackwardArgs& a, int dtype, int h_dtype, float* dweight, hipStream_t s);
-// Rows of partial sums of the gradient to the weights, and all FP32 words of the workspace.
+// Rows of partial sums of the gradient to the weights, and all FP32 words of the
+// workspace (without that gradient: the long rows' own).
 int64_t norm_backward_parts(int64_t rows, int64_t width);
-int64_t norm_backward_words(int64_t rows, int64_t width);
+int64_t norm_backward_words(int64_t rows, int64_t width, bool dweight);
 
 // dz = dy act'(z), dbias = column sums of dz (FP32, before rounding).
 struct ActBackwardArgs {

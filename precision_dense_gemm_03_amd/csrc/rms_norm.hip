@@ -498,8 +498,8 @@ int64_t norm_backward_parts(int64_t rows, int64_t width) {
     return sets < most ? sets : most;
 }
 
-int64_t norm_backward_words(int64_t rows, int64_t width) {
-    return norm_backward_parts(rows, width) * width + (width > kMostWidth ? rows : 0);
+int64_t norm_backward_words(int64_t rows, int64_t width, bool dweight) {
+    return (dweight ? norm_backward_parts(rows, width) * width : 0) + (width > kMostWidth ? rows : 0);
 }
 
 hipError_t launch_rms_norm(const NormArgs& a, int dtype, int out_dtype, hipStream_t s) {
