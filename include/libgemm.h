@@ -632,7 +632,10 @@ int64_t bias_act_backward_workspace_size(int64_t rows, int64_t cols);
 /*
  * quantize_mx_fp8 — 8-bit values of x[rows*cols] (F32 or F16). Values of F16 x above
  * 61440 (E5M2: 57344) in magnitude, the largest F16 number with the format's
- * mantissa, count as that, so that what the codes stand for are F16 numbers.
+ * mantissa, count as that, so that what the codes stand for are F16 numbers. Those of
+ * F32 x need not be: where they are read as F16 (dequantize_mx_fp8 into F16,
+ * gemm_mx_wgrad), what lies past 65504 becomes infinite, what lies below 2^-14 loses
+ * bits and below 2^-25 is 0.
  * dequantize_mx_fp8 — what they stand for, as F32 or F16 (nearest even, overflow to
  * inf).
  */
@@ -644,7 +647,8 @@ int dequantize_mx_fp8(const uint8_t* q, const uint8_t* scale, int fmt, int64_t r
 /*
  * gemm_mx_wgrad — the gradient to the weights with 8-bit activations: C[g] =
  * X[rows of g]ᵀ · B[rows of g], X the values that Q and Qscale stand for as FP16
- * numbers (nearest even, overflow to inf); zeros for an empty group.
+ * numbers (nearest even, overflow to inf; exact for values packed from F16, not for
+ * all that are packed from F32: quantize_mx_fp8); zeros for an empty group.
  *   Q, Qscale  device, 8-bit values [rows*M] of format fmt
  *   B          device, _Float16[rows*N]
  *   offsets    device, int32[groups + 1], as gemm_f16_grouped_wgrad; or NULL: one

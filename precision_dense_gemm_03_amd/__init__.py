@@ -1392,7 +1392,8 @@ def bias_act_backward(dy, Z, act, dZ=None, dbias=None, Zscale=None, z_fmt=None, 
 
 def quantize_mx_fp8(x, fmt=FMT_E4M3, q=None, scale=None, stream=None):
     """8-bit values of float32 or float16 x[rows, cols]: (codes[rows, cols], scale[rows, ceil(cols / 32)]), a power of
-    two 2^(scale - 127) per 32 values of a row."""
+    two 2^(scale - 127) per 32 values of a row. What the codes of float16 x stand for are float16 numbers; float32 x may
+    lie past their range, which gemm_mx_wgrad and dequantize_mx_fp8 into float16 read as infinities or zeros."""
     torch = _torch()
     dt = _float_dtype(x, "x")
     _need(x, x.dtype, 2, "x")
@@ -1419,8 +1420,8 @@ def dequantize_mx_fp8(q, scale, fmt, y, stream=None):
 
 
 def gemm_mx_wgrad(q, scale, fmt, B, C, offsets=None, q_second=False, stream=None):
-    """X.T @ B for 8-bit values X (q[rows, M], scale) and float16 B[rows, N], into float32 or float16 C[M, N]; with
-    q_second B.T @ X into C[N, M]. With offsets[groups + 1] one product per group of rows, C[groups, ...]."""
+    """X.T @ B for 8-bit values X (q[rows, M], scale; multiplied as float16 numbers, past 65504 infinite, below 2^-25
+    zero) and float16 B[rows, N], into float32 or float16 C[M, N]; with q_second B.T @ X into C[N, M]. With offsets[groups + 1] one product per group of rows, C[groups, ...]."""
     torch = _torch()
     pq, ps = _mx_codes(q, scale, fmt, "q")
     rows, M = q.shape
