@@ -602,6 +602,8 @@ int gemm_f16_bias_act_bt(const void* A, const void* Bt, const float* bias, const
  *            FP8((act(z) + residual) / sOut), the quotient formed as a product with
  *            1 / sOut (an FP32 ulp or two from it), for every positive sOut
  *   C        F32, F16, E4M3 or E5M2
+ * Sums have the precision of the FP8 matrix cores (gemm_fp8_exact): of 8-bit Z one
+ * code in a thousand or so is its neighbour, nearer to the inexact sum.
  */
 int gemm_fp8_bias_act(const uint8_t* A, int fmt_a, const uint8_t* B, int fmt_b, const float* sA, const float* sB,
                       int channel, const float* sOut, const float* bias, const void* residual, int res_dtype, void* C,

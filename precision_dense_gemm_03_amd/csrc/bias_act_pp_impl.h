@@ -1,9 +1,9 @@
 // Products with bias, activation and residual on the ping-pong tile kernel
 // (gemm_pp_impl.h), whose epilogue they replace (bias_act_extra.h). Bound by the tile
-// loop; one workgroup fills a CU, so the epilogue is not hidden. 16384 x 12288 x 4096
-// FP8, per channel: 651 us without, 688 with bias and GELU_TANH, 750 to 774 with an FP16
-// residual too (plain product 657); 4096^3 FP16 with GELU and z in 8 bits 123 to 125
-// (118 to 125).
+// loop; one workgroup fills a CU, so the epilogue is not hidden. On one machine 16384 x
+// 12288 x 4096 FP8, per channel: 652 us without, 697 with bias and GELU_TANH, 757 to 760
+// with an FP16 residual too (plain product 637; 756 to 799 over five machines); 4096^3
+// FP16 with GELU and z in 8 bits 122.5 (plain 112; 122 to 130).
 #pragma once
 
 #include "bias_act_extra.h"

@@ -56,7 +56,7 @@ struct MxOperand {
     int64_t blocks;   // scales of a row
 };
 
-// Eight codes as FP16, scaled (rounded to nearest even, overflow to infinity; checked
+// Eight codes as FP16, scaled (rounded to nearest even, overflow to infinity; tested
 // for every code and scale).
 template <int FMT>
 __device__ __forceinline__ v4u mx_halves(uint32_t lo, uint32_t hi, float scale) {
@@ -741,9 +741,11 @@ int choose_wgrad(const GroupedArgs& a, int qs = 0) {
                        a.N % (qs == 2 ? 16 : 8) == 0 && a.M < (1 << 21) && a.N < (1 << 21);
     // (launches of 1024 threads in a workgroup: far below 2^32 of them)
     const bool split_ok = qs && a.M >= 8 && a.N >= 8 && wgrad_blocks(a.groups, (a.M + 63) / 64, (a.N + 63) / 64) < (1 << 20);
-    // Estimated us, fits to measured times of 90 shapes (choosing by them costs
-    // 2 % over the fastest of each shape; the ping-pong kernel wherever it is
-    // possible 24 %): tiles over compute units, `more` for the uneven end, no
+    // Estimated us, fits to measured times of 90 shapes, taken before the tile kernels'
+    // loops lost their address products (13 to 17 % of them); with the present kernels
+    // choosing by them costs 1.9 % over the fastest of each of 290 further shapes, 20 of
+    // which lose more than 10 % (the ping-pong kernel wherever it is possible: 24 % over
+    // the 90): tiles over compute units, `more` for the uneven end, no
     // less than `least` for one alone, per_k ns for each of a group's rows, and C
     // stored at no more than tb TB/s.
     struct Cost {

@@ -35,8 +35,8 @@ __device__ __forceinline__ int mx_exponent(float m) {
 __device__ __forceinline__ float mx_power(int e) { return mx_scale((uint32_t)(e + 127)); }
 
 // Four codes of values / 2^e (given as mx_power) that are in the format's range,
-// infinite or NaN. The scaled conversions round to nearest even (checked against the
-// plain ones for every FP16 value and every scale that leaves it in range).
+// infinite or NaN. The scaled conversions round to nearest even (tested for every FP16
+// value and every scale that holds it, and for FP32 values at every scale).
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d, float power) {
     typedef short v2s __attribute__((ext_vector_type(2)));
