@@ -9,9 +9,11 @@ an E4M3 and 2^-3 of an E5M2 code (2^-10 and 2^-17 below the smallest normal
 code). An activation of z in FP32 is a product of z and a factor in [0, 1] that
 comes from one exponential, whose argument's rounding adds its size times 2^-24
 (|z| and z^2 / 2 at most, with the cubic of the tanh form 2 |z|^3 where the
-factor is not 0 or 1), a reciprocal and a fitted polynomial of 2.6e-7: off by
-at most 2^-19 (1 + z^2) of the value, and 2^-33 |z| where the factor is below
-the polynomial's range. A derivative is that factor and z times its slope: off by at
+factor is not 0 or 1), and either from a reciprocal and, for GELU, a fitted
+polynomial of 2.7e-7 or less (FP32 results, derivatives) or, for GELU into FP16 and
+FP8, from a polynomial in the exponent, off by 1.4e-6 of the factor up to |z| = 3 and
+5.2e-6 up to 7: off by at most 2^-19 (1 + z^2) of the value, and 2^-33 |z| where the
+factor is below that polynomial's range. A derivative is that factor and z times its slope: off by at
 most 2^-19 (1 + |z| + z^2) absolutely, the slope being at most 1.13."""
 import math
 
