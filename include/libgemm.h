@@ -583,9 +583,9 @@ int64_t rms_norm_backward_workspace_size(int64_t rows, int64_t width);
  *   Z          device, [M*N], written with z: F32, F16, or 8-bit values with Zscale
  *              (z_dtype; GEMM_ERR_SCALE if Zscale is NULL); or NULL
  * All of it in FP32, each output rounded once; an activation into FP32 is within
- * 1.2e-6 of its value, small tails included. M = 0 or N = 0 is a no-op; K = 0 is the
- * empty sum. M, N and K are at most 2^31 - 65536. Otherwise as gemm_f16; the _bt call
- * takes the weight K-major, Bt[N,K].
+ * 1.2e-6 of its value down to 2^-120 (less may be 0). M = 0 or N = 0 is a no-op; K = 0
+ * is the empty sum. M, N and K are at most 2^31 - 65536. Otherwise as gemm_f16; the
+ * _bt call takes the weight K-major, Bt[N,K].
  */
 int gemm_f16_bias_act(const void* A, const void* B, const float* bias, const void* residual, int res_dtype, void* C,
                       int out_dtype, int act, void* Z, uint8_t* Zscale, int z_dtype, int64_t M, int64_t N, int64_t K,
